@@ -365,6 +365,85 @@ int ltx3drope_unpatchify(void* x, const void* y, int elem_bytes, int64_t B, int6
 int ltx3drope_dit_freq_grid(double theta, int64_t dim, int64_t num_rope_elems, int double_precision, float* out,
                             void* stream, int64_t* count);
 
+/*
+ * RMS norms before and after a transformer block, fused with the block's gate,
+ * its scaled residual and the next norm's scale and shift.
+ *
+ * Row tensors are contiguous [batch, rows, dim] of `dtype` (F32 or BF16).
+ * Vectors are contiguous and of `param_dtype` (F32, or BF16 with BF16 rows):
+ * weights [dim]; gate, next_scale and next_shift [batch, dim].  Any vector may
+ * be NULL; its factor is then 1 and its term 0.  With
+ * hat(v) = v / sqrt(mean(v^2) + eps), per row of sample b and all in fp32:
+ *     branch = (post_norm ? hat(y) : y) * (weight + weight_offset)
+ *     r      = residual_scale * residual + gate_b * branch
+ *     n      = hat(r) * (next_weight + weight_offset) * (1 + next_scale_b) + next_shift_b
+ * each output rounded once to `dtype` (n is formed from the unrounded r).
+ * weight_offset counts only where its weight is given.  mean(v^2) has to be
+ * finite in fp32: a row whose squares pass it gives zeros or NaN.
+ *
+ * after = 1: y, residual and r are required; next_norm = 1 also writes n.
+ * after = 0 is the norm before a block alone: n from `residual`; y, weight,
+ * gate and r must be NULL, post_norm 0, next_norm 1 and residual_scale 1.
+ *
+ * An output may be exactly one of the row inputs (r over residual, n over y);
+ * every other overlap is refused.  batch = 0 or rows = 0 is an empty call: OK,
+ * nothing launched, no pointer looked at.
+ * E_INVALID: a NULL descriptor; eps not finite or <= 0; weight_offset or
+ * residual_scale not finite; a flag other than 0 or 1 or a combination other
+ * than the above.  E_UNSUPPORTED, with the reason in *reason (which may be
+ * NULL), the first that fails of: DTYPE; NONPOSITIVE_DIM (dim <= 0, batch or
+ * rows < 0); TOO_LARGE (dim > 16384, batch * rows of 2^31 or more, or batch >
+ * 65535 where a [batch, dim] vector is given); NULLPTR; ALIGN (a pointer not
+ * aligned to its element); OVERLAP; then NOT_DEVICE_PTR, TABLE_DEVICE (memory
+ * of two devices) and EXTENT.  E_HIP: the launch failed.  Asynchronous on
+ * `stream`; allocates nothing.
+ */
+typedef struct {
+    int32_t dtype, param_dtype;
+    int32_t after, post_norm, next_norm, reserved; /* reserved must be 0 */
+    int64_t batch, rows, dim;
+    float eps, weight_offset, residual_scale;
+    const void *y, *residual, *weight, *gate, *next_weight, *next_scale, *next_shift;
+    void *r, *n;
+} ltx3drope_norm_t;
+int ltx3drope_norm(const ltx3drope_norm_t* call, void* stream, int* reason);
+
+/*
+ * The gradients of ltx3drope_norm.  `r` is the forward's output r (after = 1)
+ * or its input (after = 0); dr (may be NULL: zero) is the gradient that reaches
+ * r past the next norm, dn (required with next_norm = 1, else NULL) that of n.
+ * With v = dn * (next_weight + weight_offset) * (1 + next_scale_b):
+ *     dR        = dr + (v - hat(r) * mean(v * hat(r))) / sqrt(mean(r^2) + eps)
+ *     dresidual = residual_scale * dR
+ *     q         = dR * gate_b * (weight + weight_offset)
+ *     dy        = post_norm ? (q - hat(y) * mean(q * hat(y))) / sqrt(mean(y^2) + eps) : q
+ * and the vectors' gradients, sums over rows (weights: over rows and samples)
+ * held in fp32, in param_dtype.  dresidual is required, dy too with after = 1;
+ * the vectors' gradients may each be NULL, and must be where the vector itself
+ * is (dnext_shift alone needs no vector).  y may be NULL where nothing needs it
+ * (no post norm, no gate and no weight); r where next_norm = 0.
+ * `workspace`: ltx3drope_norm_backward_workspace bytes of device memory, 16-byte
+ * aligned, that nothing else uses until the call's work on `stream` has run; 0
+ * bytes where no vector's gradient is asked for (then it may be NULL).  Sums are
+ * added in a fixed order: equal inputs give equal bits.  Empty calls write zeros
+ * into the vectors' gradients.  Aliasing, statuses and reasons as above;
+ * a workspace that is too small is E_INVALID.
+ */
+typedef struct {
+    int32_t dtype, param_dtype;
+    int32_t after, post_norm, next_norm, reserved;
+    int64_t batch, rows, dim;
+    float eps, weight_offset, residual_scale;
+    const void *dr, *dn, *y, *r, *weight, *gate, *next_weight, *next_scale;
+    void *dresidual, *dy, *dweight, *dgate, *dnext_weight, *dnext_scale, *dnext_shift;
+    void* workspace;
+    int64_t workspace_bytes;
+} ltx3drope_norm_backward_t;
+int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream, int* reason);
+/* Bytes of workspace for a call (its sizes and which gradients are not NULL; no pointer is looked
+   at), or a negative status for a malformed descriptor. */
+int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call);
+
 /* Gate state of one unsharded configuration (tables built for the tensor's own grid, no offsets):
  * LTX3DROPE_GATE_*, or a negative status. */
 int ltx3drope_gate_state(int device, int dtype, int64_t B, int64_t T, int64_t H, int64_t W,

@@ -15,7 +15,7 @@ forward_pair() the decoder-side entry that ties them together.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 from . import _lib
 from ._lib import (  # noqa: F401
@@ -36,7 +36,8 @@ __all__ = [
     "apply_qk_noalloc",
     "forward_pair", "kernel_choice", "stats", "stats_reset", "set_option", "get_option", "gate_state", "gate_reset",
     "cache_clear", "copy_bytes", "version", "neox_can_use", "neox_apply_qk", "neox_position_errors", "patchify",
-    "unpatchify", "dit_freq_grid",
+    "unpatchify", "dit_freq_grid", "norm_before", "norm_after", "norm_before_backward", "norm_after_backward",
+    "NormBeforeGrads", "NormAfterGrads",
 ]
 
 
@@ -422,6 +423,205 @@ def dit_freq_grid(theta: float, dim: int, num_rope_elems: int, double_precision:
         raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR", st)
     _check(st, "dit_freq_grid")
     return out
+
+
+class _On:
+    """Allocations for a call on `stream`: memory taken from that stream's pool (its earlier uses are
+    ordered before the call, its later reuse after it), or from the current stream's without one."""
+
+    def __init__(self, stream):
+        self._ctx = None if stream is None else _torch().cuda.stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _block_check(status: int, reason: ctypes.c_int, what: str) -> None:
+    if status == _lib.E_UNSUPPORTED:
+        raise Ltx3dRopeUnsupported(_lib.REASONS.get(reason.value, str(reason.value)), status)
+    _check(status, what)
+
+
+def _rows_marshal(first, others):
+    """(batch, rows, dim) of a [batch, rows, dim] or [rows, dim] row tensor; `others` must match it."""
+    if first.dim() not in (2, 3):
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    if _dtype_code(first) < 0:
+        raise Ltx3dRopeUnsupported("DTYPE")
+    if not first.is_cuda:
+        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+    if not first.is_contiguous():
+        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    for t in others:
+        if t is None:
+            continue
+        if t.shape != first.shape:
+            raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+        if t.dtype != first.dtype:
+            raise Ltx3dRopeUnsupported("DTYPE")
+        if t.device != first.device:
+            raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+        if not t.is_contiguous():
+            raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    s = first.shape
+    return (1, s[0], s[1]) if len(s) == 2 else (s[0], s[1], s[2])
+
+
+def _vectors_marshal(row, batch, dim, weights, per_sample):
+    """The vectors' common dtype: the rows' own or float32."""
+    dtype = None
+    for t, per in [(t, False) for t in weights] + [(t, True) for t in per_sample]:
+        if t is None:
+            continue
+        shape = tuple(t.shape)
+        if shape != ((batch, dim) if per else (dim,)) and not (per and batch == 1 and row.dim() == 2 and shape == (dim,)):
+            raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+        if _dtype_code(t) < 0 or (dtype is not None and t.dtype != dtype):
+            raise Ltx3dRopeUnsupported("DTYPE")
+        dtype = t.dtype
+        if t.device != row.device:
+            raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+        if not t.is_contiguous():
+            raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    return row.dtype if dtype is None else dtype
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_call(cls, row, param_dtype, after, post_norm, next_norm, size, eps, weight_offset, residual_scale, **ptrs):
+    return cls(dtype=_dtype_code(row), param_dtype=DTYPE_F32 if param_dtype == _torch().float32 else DTYPE_BF16,
+               after=after, post_norm=post_norm, next_norm=next_norm, batch=size[0], rows=size[1], dim=size[2],
+               eps=eps, weight_offset=weight_offset, residual_scale=residual_scale, **ptrs)
+
+
+def norm_before(x, weight=None, scale=None, shift=None, *, eps: float = 1e-6, weight_offset: float = 0.0, out=None,
+                stream=None):
+    """The RMS norm before a block: hat(x) * (weight + weight_offset) * (1 + scale) + shift, one pass.
+
+    x [batch, rows, dim] or [rows, dim] (one sample), float32 or bfloat16; weight [dim]; scale and
+    shift [batch, dim], one row a sample; the vectors float32 or x's dtype, any of them None.  out
+    may be x itself."""
+    size = _rows_marshal(x, (out,))
+    pd = _vectors_marshal(x, size[0], size[2], (weight,), (scale, shift))
+    if out is None:
+        with _On(stream):
+            out = _torch().empty_like(x)
+    c = _norm_call(_lib.Norm, x, pd, 0, 0, 1, size, eps, weight_offset, 1.0, residual=x.data_ptr(),
+                   next_weight=_ptr(weight), next_scale=_ptr(scale), next_shift=_ptr(shift), n=out.data_ptr())
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_norm(c, _stream_ptr(x.device, stream), reason)
+    _block_check(st, reason, "norm_before")
+    return out
+
+
+def norm_after(y, residual, weight=None, gate=None, *, post_norm: bool = True, residual_scale: float = 1.0,
+               next_norm: bool = True, next_weight=None, next_scale=None, next_shift=None, eps: float = 1e-6,
+               weight_offset: float = 0.0, r_out=None, n_out=None, stream=None):
+    """After a block, in one pass: (r, n) with
+    r = residual_scale * residual + gate * (hat(y) if post_norm else y) * (weight + weight_offset) and n
+    the next block's norm_before(r, next_weight, next_scale, next_shift) (None with next_norm=False).
+
+    y, residual [batch, rows, dim] or [rows, dim]; weight, next_weight [dim]; gate, next_scale,
+    next_shift [batch, dim].  n is formed from r before r is rounded to its dtype.  r_out may be
+    residual and n_out may be y."""
+    size = _rows_marshal(y, (residual, r_out, n_out))
+    pd = _vectors_marshal(y, size[0], size[2], (weight, next_weight), (gate, next_scale, next_shift))
+    if not next_norm and any(t is not None for t in (next_weight, next_scale, next_shift, n_out)):
+        raise ValueError("next_norm=False takes no vector or output of the next norm")
+    with _On(stream):
+        if r_out is None:
+            r_out = _torch().empty_like(y)
+        if next_norm and n_out is None:
+            n_out = _torch().empty_like(y)
+    c = _norm_call(_lib.Norm, y, pd, 1, bool(post_norm), bool(next_norm), size, eps, weight_offset, residual_scale,
+                   y=y.data_ptr(), residual=residual.data_ptr(), weight=_ptr(weight), gate=_ptr(gate),
+                   next_weight=_ptr(next_weight), next_scale=_ptr(next_scale), next_shift=_ptr(next_shift),
+                   r=r_out.data_ptr(), n=_ptr(n_out))
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_norm(c, _stream_ptr(y.device, stream), reason)
+    _block_check(st, reason, "norm_after")
+    return r_out, n_out
+
+
+class NormBeforeGrads(NamedTuple):
+    """Gradients of norm_before; None where the vector was not given (dshift: where not asked for)."""
+
+    dx: object
+    dweight: object
+    dscale: object
+    dshift: object
+
+
+class NormAfterGrads(NamedTuple):
+    """Gradients of norm_after; None where the vector was not given."""
+
+    dy: object
+    dresidual: object
+    dweight: object
+    dgate: object
+    dnext_weight: object
+    dnext_scale: object
+    dnext_shift: object
+
+
+def _norm_backward(row, pd, after, post_norm, next_norm, size, eps, weight_offset, residual_scale, stream, dr, dn, y, r,
+                   weight, gate, next_weight, next_scale, next_shift):
+    torch = _torch()
+
+    def like(t):
+        return None if t is None else torch.empty_like(t)
+
+    with _On(stream):
+        dresidual = torch.empty_like(row)
+        dy = torch.empty_like(row) if after else None
+        dweight, dgate, dnw, dns, dnsh = like(weight), like(gate), like(next_weight), like(next_scale), like(next_shift)
+        c = _norm_call(_lib.NormBackward, row, pd, after, post_norm, next_norm, size, eps, weight_offset, residual_scale,
+                       dr=_ptr(dr), dn=_ptr(dn), y=_ptr(y), r=_ptr(r), weight=_ptr(weight), gate=_ptr(gate),
+                       next_weight=_ptr(next_weight), next_scale=_ptr(next_scale), dresidual=dresidual.data_ptr(),
+                       dy=_ptr(dy), dweight=_ptr(dweight), dgate=_ptr(dgate), dnext_weight=_ptr(dnw),
+                       dnext_scale=_ptr(dns), dnext_shift=_ptr(dnsh))
+        ws_bytes = int(_lib.lib().ltx3drope_norm_backward_workspace(c))
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=row.device) if ws_bytes > 0 else None
+    if workspace is not None:
+        c.workspace, c.workspace_bytes = workspace.data_ptr(), ws_bytes
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_norm_backward(c, _stream_ptr(row.device, stream), reason)
+    _block_check(st, reason, "norm_backward")
+    return dy, dresidual, dweight, dgate, dnw, dns, dnsh
+
+
+def norm_before_backward(dn, x, weight=None, scale=None, shift=None, *, dresidual=None, eps: float = 1e-6,
+                         weight_offset: float = 0.0, stream=None) -> NormBeforeGrads:
+    """Gradients of norm_before at x for the output's gradient dn.  dresidual, if given, is what
+    reaches x past the block and is added to dx.  shift only asks for its gradient."""
+    size = _rows_marshal(dn, (x, dresidual))
+    pd = _vectors_marshal(dn, size[0], size[2], (weight,), (scale, shift))
+    g = _norm_backward(dn, pd, 0, 0, 1, size, eps, weight_offset, 1.0, stream, dresidual, dn, None, x, None, None,
+                       weight, scale, shift)
+    return NormBeforeGrads(g[1], g[4], g[5], g[6])
+
+
+def norm_after_backward(dr, dn, y, r, weight=None, gate=None, *, post_norm: bool = True, residual_scale: float = 1.0,
+                        next_norm: bool = True, next_weight=None, next_scale=None, next_shift=None, eps: float = 1e-6,
+                        weight_offset: float = 0.0, stream=None) -> NormAfterGrads:
+    """Gradients of norm_after for the gradients dr of r (None: zero) and dn of n (None with
+    next_norm=False); r is the forward's output.  next_shift only asks for its gradient."""
+    if (dn is not None) != bool(next_norm):
+        raise ValueError("dn belongs to next_norm=True")
+    size = _rows_marshal(y, (r, dr, dn))
+    pd = _vectors_marshal(y, size[0], size[2], (weight, next_weight), (gate, next_scale, next_shift))
+    if not next_norm and any(t is not None for t in (next_weight, next_scale, next_shift)):
+        raise ValueError("next_norm=False takes no vector of the next norm")
+    return NormAfterGrads(*_norm_backward(y, pd, 1, bool(post_norm), bool(next_norm), size, eps, weight_offset,
+                                          residual_scale, stream, dr, dn, y, r, weight, gate, next_weight, next_scale,
+                                          next_shift))
 
 
 def kernel_choice(q, k, tabs: Tables, q_out=None, k_out=None) -> str:

@@ -47,6 +47,7 @@ EXPORTS = (
     "ltx3drope_gate_reset", "ltx3drope_set_option", "ltx3drope_get_option", "ltx3drope_stats",
     "ltx3drope_stats_reset", "ltx3drope_kernel_choice", "ltx3drope_copy", "ltx3drope_status_string",
     "ltx3drope_reason_string", "ltx3drope_version",
+    "ltx3drope_norm", "ltx3drope_norm_backward", "ltx3drope_norm_backward_workspace",
 )
 
 i64 = ctypes.c_int64
@@ -71,6 +72,23 @@ class Stats(ctypes.Structure):
 
     def as_dict(self):
         return {n: int(getattr(self, n)) for n, _ in self._fields_}
+
+
+_NORM_SCALARS = [(n, ctypes.c_int32) for n in ("dtype", "param_dtype", "after", "post_norm", "next_norm", "reserved")] + [
+    (n, i64) for n in ("batch", "rows", "dim")] + [
+    (n, ctypes.c_float) for n in ("eps", "weight_offset", "residual_scale")]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = _NORM_SCALARS + [(n, vp) for n in (
+        "y", "residual", "weight", "gate", "next_weight", "next_scale", "next_shift", "r", "n")]
+
+
+class NormBackward(ctypes.Structure):
+    _fields_ = _NORM_SCALARS + [(n, vp) for n in (
+        "dr", "dn", "y", "r", "weight", "gate", "next_weight", "next_scale",
+        "dresidual", "dy", "dweight", "dgate", "dnext_weight", "dnext_scale", "dnext_shift", "workspace")] + [
+        ("workspace_bytes", i64)]
 
 
 _lock = threading.Lock()
@@ -133,6 +151,10 @@ def lib() -> ctypes.CDLL:
             "ltx3drope_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "ltx3drope_reason_string": (ctypes.c_char_p, [ctypes.c_int]),
             "ltx3drope_version": (ctypes.c_int, []),
+            "ltx3drope_norm": (ctypes.c_int, [ctypes.POINTER(Norm), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_norm_backward": (ctypes.c_int, [ctypes.POINTER(NormBackward), vp,
+                                                       ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_norm_backward_workspace": (i64, [ctypes.POINTER(NormBackward)]),
         }
         assert set(sig) == set(EXPORTS)
         for name, (res, args) in sig.items():

@@ -38,7 +38,9 @@ SOURCES = [  # (file, language, extra flags)
     ("neox.hip", "hip", DEVICE),
     ("patchify.hip", "hip", DEVICE),
     ("dit_freqs.hip", "hip", DEVICE),
+    ("norm.hip", "hip", DEVICE),
     ("api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),
+    ("block_api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),
     ("tables.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include"), "-fno-builtin"]),
 ]
 

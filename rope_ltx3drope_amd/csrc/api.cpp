@@ -133,6 +133,8 @@ int device_res(int device, DeviceRes** out) {
 
 // ---- precheck --------------------------------------------------------------
 
+}  // namespace
+
 bool ranges_overlap(const void* a, size_t an, const void* b, size_t bn) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return a0 < b0 + bn && b0 < a0 + an;
@@ -159,6 +161,8 @@ int check_device_ptr(const void* p, size_t bytes, int device) {
     if (q < b || q + bytes > b + size) return LTX3DROPE_REASON_EXTENT;
     return LTX3DROPE_REASON_OK;
 }
+
+namespace {
 
 // Where the tensor sits in the tables' grid.  exact_grid: the unsharded rule of
 // the page's predicate (the tables' grid equals the tensor's); otherwise the
@@ -271,19 +275,6 @@ int status_for_reason(int reason) {
     return LTX3DROPE_E_UNSUPPORTED;
 }
 
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int device) {
-        if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-        if (prev != device) (void)hipSetDevice(device);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-    }
-};
-
 // Batch elements per launch: all of them when the tensor holds fewer than 2^32 elements, else as
 // many whole batch elements as stay below 2^32 (the precheck keeps one below it).
 uint32_t batch_per_launch(const Problem& p) {
@@ -374,6 +365,16 @@ int verify_fast(const Problem& p, hipStream_t stream, int device, bool noalloc, 
 }
 
 }  // namespace
+
+void count_launch() { stats().fast.fetch_add(1); }
+void count_rejected() { stats().rejected.fetch_add(1); }
+
+int device_cu_count(int device, int* out) {
+    DeviceRes* res = nullptr;
+    const int st = device_res(device, &res);
+    if (st == LTX3DROPE_OK) *out = res->cu_count;
+    return st;
+}
 
 int64_t option(int which) {
     switch (which) {

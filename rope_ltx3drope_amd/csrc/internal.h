@@ -106,4 +106,24 @@ void cache_counters_reset();
 // Options (api.cpp).
 int64_t option(int which);
 
+// Argument checks and bookkeeping that every entry point shares (api.cpp).
+bool ranges_overlap(const void* a, size_t an, const void* b, size_t bn);
+int check_device_ptr(const void* p, size_t bytes, int device);
+int device_cu_count(int device, int* out);  // a status; the device must be the current one
+void count_launch();
+void count_rejected();
+
+// Restores the caller's current device on scope exit.
+struct DeviceGuard {
+    int prev = -1;
+    explicit DeviceGuard(int device) {
+        if (hipGetDevice(&prev) != hipSuccess) prev = -1;
+        if (prev != device) (void)hipSetDevice(device);
+    }
+    ~DeviceGuard() {
+        int cur = -1;
+        if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+    }
+};
+
 }  // namespace ltx3drope

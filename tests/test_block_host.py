@@ -1,0 +1,167 @@
+"""CPU tests of the transformer-block operators: the oracle's gradients against central differences,
+and the C ABI's refusals, which come before anything touches a GPU."""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import oracle.block as ob
+
+rla = pytest.importorskip("rope_ltx3drope_amd")
+from rope_ltx3drope_amd import _lib  # noqa: E402
+
+if not os.path.exists(_lib.LIB_PATH):
+    pytest.skip("libltx3drope.so not built (python -m rope_ltx3drope_amd.build)", allow_module_level=True)
+
+L = _lib.lib()
+
+
+def slope(f, args, i, direction, h=1e-5):
+    def at(s):
+        moved = list(args)
+        moved[i] = moved[i] + s * direction
+        return f(*moved)
+
+    return float((at(h) - at(-h)) / (2 * h))
+
+
+def check_differences(f, args, grads, seed=0):
+    """The gradient of the scalar f along a random direction of each argument.  In float64 with h = 1e-5
+    truncation (h^2) and rounding (1e-16 / h) are both about 1e-10 of the terms' sum: 1e-6 covers it."""
+    gen = torch.Generator().manual_seed(seed)
+    for i, g in enumerate(grads):
+        if g is None:
+            continue
+        v = torch.randn(args[i].shape, generator=gen, dtype=torch.float64)
+        want = slope(f, args, i, v)
+        got = float((g * v).sum())
+        assert abs(got - want) <= 1e-6 * (1 + float((g * v).abs().sum())), (i, got, want)
+
+
+@pytest.mark.parametrize("offset,res_scale,post", [(0.0, 1.0, True), (1.0, 0.5, True), (1.0, 2.0, False)])
+def test_norm_gradients_of_the_oracle(offset, res_scale, post):
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)  # noqa: E731
+    B, S, D = 2, 3, 10
+    y, res, w, gate, nw, ns, nb, dr, dn = r(B, S, D), r(B, S, D), r(D), r(B, D), r(D), r(B, D), r(B, D), r(B, S, D), \
+        r(B, S, D)
+
+    def f(y, res, w, gate, nw, ns, nb):
+        x = ob.norm_after(y, res, w, gate, post, res_scale, 1e-3, offset)
+        return (x * dr).sum() + (ob.norm_before(x, nw, ns, nb, 1e-3, offset) * dn).sum()
+
+    x = ob.norm_after(y, res, w, gate, post, res_scale, 1e-3, offset)
+    dR, dnw, dns, dnb = ob.norm_before_backward(dn, x, nw, ns, dr, 1e-3, offset)
+    dy, dres, dw, dgate = ob.norm_after_backward(dR, y, w, gate, post, res_scale, 1e-3, offset)
+    check_differences(f, (y, res, w, gate, nw, ns, nb), (dy, dres, dw, dgate, dnw, dns, dnb))
+    # the oracle's own mistakes are found: a wrong offset or a lost projection fails the same check
+    with pytest.raises(AssertionError):
+        check_differences(f, (y, res, w, gate, nw, ns, nb), (dy + 1e-3 * y, dres, dw, dgate, dnw, dns, dnb))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh"])
+def test_ffn_gradients_of_the_oracle(kind):
+    g = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)  # noqa: E731
+    x, wg, wu, dh = r(4, 6), r(7, 6), r(7, 6), r(4, 7)
+
+    def f(x, wg, wu):
+        return (ob.gated_ffn(x, wg, wu, kind)[0] * dh).sum()
+
+    _, gg, uu = ob.gated_ffn(x, wg, wu, kind)
+    check_differences(f, (x, wg, wu), ob.gated_ffn_backward(dh, x, wg, wu, gg, uu, kind))
+
+
+# ---- refusals of the norm --------------------------------------------------------------------------
+
+FAKE = 1 << 20  # an aligned address that no rule below dereferences
+
+
+def norm_call(**kw):
+    c = dict(dtype=0, param_dtype=0, after=1, post_norm=1, next_norm=1, batch=2, rows=3, dim=64, eps=1e-6,
+             weight_offset=0.0, residual_scale=1.0, y=FAKE, residual=FAKE * 2, r=FAKE * 3, n=FAKE * 4)
+    c.update(kw)
+    return _lib.Norm(**c)
+
+
+def norm_status(**kw):
+    reason = ctypes.c_int(-1)
+    return L.ltx3drope_norm(norm_call(**kw), None, reason), _lib.REASONS[reason.value]
+
+
+@pytest.mark.parametrize("kw", [dict(eps=0.0), dict(eps=float("nan")), dict(eps=-1.0), dict(weight_offset=float("inf")),
+                                dict(residual_scale=float("nan")), dict(after=2), dict(post_norm=-1),
+                                dict(next_norm=3), dict(reserved=1), dict(after=0), dict(next_norm=0),
+                                dict(after=0, y=None, r=None, post_norm=0, next_norm=0, n=None),
+                                dict(after=0, y=None, r=None, post_norm=0, residual_scale=2.0),
+                                dict(after=0, y=None, r=FAKE, post_norm=0)])
+def test_norm_invalid(kw):
+    assert norm_status(**kw)[0] == _lib.E_INVALID
+
+
+@pytest.mark.parametrize("kw,reason", [
+    (dict(dtype=2), "DTYPE"), (dict(param_dtype=1), "DTYPE"), (dict(dtype=1, param_dtype=3), "DTYPE"),
+    (dict(dim=0), "NONPOSITIVE_DIM"), (dict(rows=-1), "NONPOSITIVE_DIM"), (dict(batch=-1), "NONPOSITIVE_DIM"),
+    (dict(dim=16385), "TOO_LARGE"), (dict(batch=1 << 16, rows=1 << 15), "TOO_LARGE"),
+    (dict(batch=65536, rows=1, gate=FAKE * 5), "TOO_LARGE"),
+    (dict(y=None), "NULLPTR"), (dict(n=None), "NULLPTR"), (dict(r=None), "NULLPTR"), (dict(residual=None), "NULLPTR"),
+    (dict(y=FAKE + 2), "ALIGN"), (dict(next_weight=FAKE * 5 + 1), "ALIGN"), (dict(n=FAKE * 3), "OVERLAP"),
+    (dict(r=FAKE * 2 + 64), "OVERLAP"), (dict(weight=FAKE * 4), "OVERLAP"), (dict(), "NOT_DEVICE_PTR"),
+    (dict(r=FAKE * 2, n=FAKE), "NOT_DEVICE_PTR"),  # exactly over the inputs: passes the overlap rule
+])
+def test_norm_refusals(kw, reason):
+    assert norm_status(**kw) == (_lib.E_UNSUPPORTED, reason)
+
+
+def test_norm_empty_calls_look_at_no_pointer():
+    for kw in (dict(rows=0), dict(batch=0)):
+        assert norm_status(y=None, residual=None, r=None, n=None, **kw) == (_lib.OK, "OK")
+    assert L.ltx3drope_norm(None, None, None) == _lib.E_INVALID
+
+
+def backward_call(**kw):
+    c = dict(dtype=0, param_dtype=0, after=1, post_norm=1, next_norm=1, batch=2, rows=3, dim=64, eps=1e-6,
+             weight_offset=0.0, residual_scale=1.0, dr=FAKE, dn=FAKE * 2, y=FAKE * 3, r=FAKE * 4,
+             weight=FAKE * 5, dweight=FAKE * 6, dresidual=FAKE * 7, dy=FAKE * 8, workspace=FAKE * 9,
+             workspace_bytes=1 << 20)
+    c.update(kw)
+    return _lib.NormBackward(**c)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(workspace_bytes=16), (_lib.E_INVALID, "OK")), (dict(weight=None), (_lib.E_INVALID, "OK")),
+    (dict(dgate=FAKE * 10), (_lib.E_INVALID, "OK")), (dict(next_norm=0), (_lib.E_INVALID, "OK")),
+    (dict(dn=None), (_lib.E_UNSUPPORTED, "NULLPTR")), (dict(y=None), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(dy=None), (_lib.E_UNSUPPORTED, "NULLPTR")), (dict(workspace=None), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(workspace=FAKE * 9 + 8), (_lib.E_UNSUPPORTED, "ALIGN")),
+    (dict(workspace=FAKE * 3), (_lib.E_UNSUPPORTED, "OVERLAP")), (dict(dy=FAKE * 7), (_lib.E_UNSUPPORTED, "OVERLAP")),
+    (dict(dim=16385), (_lib.E_UNSUPPORTED, "TOO_LARGE")), (dict(), (_lib.E_UNSUPPORTED, "NOT_DEVICE_PTR")),
+])
+def test_norm_backward_refusals(kw, want):
+    reason = ctypes.c_int(-1)
+    st = L.ltx3drope_norm_backward(backward_call(**kw), None, reason)
+    assert (st, _lib.REASONS[reason.value]) == want
+
+
+def test_norm_workspace_sizes():
+    size = L.ltx3drope_norm_backward_workspace
+    assert size(backward_call(dweight=None)) == 0
+    assert size(backward_call(rows=0)) == 0
+    assert size(backward_call()) == 3 * 1 * 64 * 4  # 6 rows of one workgroup, no per-sample vector
+    assert size(backward_call(gate=FAKE, dgate=FAKE)) == 3 * 2 * 64 * 4  # one partial row a sample
+    assert size(backward_call(batch=1, rows=100000, dim=2048)) == 3 * 512 * 2048 * 4
+    assert size(backward_call(eps=0.0)) == _lib.E_INVALID and size(None) == _lib.E_INVALID
+
+
+@pytest.mark.parametrize("call", [
+    lambda: rla.norm_before(torch.zeros(2, 3, 8)),
+    lambda: rla.norm_after(torch.zeros(2, 3, 8), torch.zeros(2, 3, 8)),
+    lambda: rla.norm_before_backward(torch.zeros(2, 3, 8), torch.zeros(2, 3, 8)),
+])
+def test_host_tensors_are_refused(call):
+    with pytest.raises(rla.Ltx3dRopeUnsupported) as e:
+        call()
+    assert e.value.reason == "NOT_DEVICE_PTR"
