@@ -444,6 +444,111 @@ int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream,
    at), or a negative status for a malformed descriptor. */
 int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call);
 
+/*
+ * The gated feed-forward block: both projections, the activation and the
+ * product in one kernel.
+ *     g = x Wg^T,  u = x Wu^T,  h = act(g) * u
+ * x [tokens, dim], w_gate and w_up [hidden, dim], h [tokens, hidden], all
+ * contiguous and of `dtype` (F32 or BF16); sums, activation and product in fp32,
+ * h rounded once.  g and u (both or neither, [tokens, hidden] fp32 whatever the
+ * dtype) receive the projections for the backward pass: in fp32, so that the
+ * gradients carry no rounding of theirs.
+ * `workspace`: ltx3drope_gated_ffn_workspace bytes of device memory, 16-byte
+ * aligned, that nothing else uses until the call's work on `stream` has run.  It
+ * is 0 (then workspace may be NULL) but where more than 64 tokens meet rows that
+ * are not whole 16-byte chunks, or tensors that do not start on one: the call
+ * then lays padded copies of x and the weights there.
+ * tokens = 0 or hidden = 0 is an empty call: OK, nothing launched, no pointer
+ * looked at.  E_INVALID: a NULL descriptor, an unknown activation, one of g and u without the other, a workspace that is too small.
+ * E_UNSUPPORTED with the reason in *reason (which may be NULL), the first that
+ * fails of: DTYPE; NONPOSITIVE_DIM (dim <= 0, tokens or hidden < 0); TOO_LARGE
+ * (tokens, 2 * hidden or dim of 2^21 or more, or more than 2^23 output tiles of
+ * 128 x 64: 2^36 outputs); NULLPTR; ALIGN (a pointer not
+ * aligned to its element, the workspace not to 16 bytes); OVERLAP (an output or
+ * the workspace over anything else); then NOT_DEVICE_PTR, TABLE_DEVICE (memory
+ * of two devices) and EXTENT.  E_HIP: a launch failed.  Asynchronous on
+ * `stream`; allocates nothing.
+ */
+enum { LTX3DROPE_ACT_SILU = 0, LTX3DROPE_ACT_GELU = 1, LTX3DROPE_ACT_GELU_TANH = 2 };
+typedef struct {
+    int32_t dtype, activation;
+    int64_t tokens, dim, hidden;
+    const void *x, *w_gate, *w_up;
+    void* h;
+    float *g, *u;
+    void* workspace;
+    int64_t workspace_bytes;
+} ltx3drope_gated_ffn_t;
+int ltx3drope_gated_ffn(const ltx3drope_gated_ffn_t* call, void* stream, int* reason);
+/* Bytes of workspace for a call (its sizes, and whether x and the weights are 16-byte aligned), or a
+   negative status for a malformed descriptor. */
+int64_t ltx3drope_gated_ffn_workspace(const ltx3drope_gated_ffn_t* call);
+
+/*
+ * The gradients of ltx3drope_gated_ffn from the g and u that it kept:
+ *     dg = dh * u * act'(g),  du = dh * act(g)
+ *     dx = dg Wg + du Wu,  dw_gate = dg^T x,  dw_up = du^T x
+ * dg and du are formed in fp32 and rounded once to `dtype` for the matrix cores;
+ * the sums are held in fp32 and each output rounded once.  dx may be NULL, and
+ * so may dw_gate and dw_up together; what is NULL is not computed.  Sums are
+ * added in a fixed order: equal inputs give equal bits.  An empty call
+ * (tokens = 0 or hidden = 0) writes zeros into what it is given.  Workspace,
+ * statuses and reasons as above; the
+ * workspace is needed by every call that is not empty.
+ */
+typedef struct {
+    int32_t dtype, activation;
+    int64_t tokens, dim, hidden;
+    const void *dh, *x, *w_gate, *w_up;
+    const float *g, *u;
+    void *dx, *dw_gate, *dw_up;
+    void* workspace;
+    int64_t workspace_bytes;
+} ltx3drope_gated_ffn_backward_t;
+int ltx3drope_gated_ffn_backward(const ltx3drope_gated_ffn_backward_t* call, void* stream, int* reason);
+int64_t ltx3drope_gated_ffn_backward_workspace(const ltx3drope_gated_ffn_backward_t* call);
+
+/*
+ * Rows to 8-bit integers, one scale a row:
+ *     scale[r] = max |x[r]| * (1/127),  q[r][c] = round(x[r][c] / scale[r])
+ * in fp32, each step (and the constant) rounded once to nearest even, |q| <= 127.  x [rows, dim] of
+ * `dtype` (F32 or BF16), q [rows, dim] int8, scale [rows] fp32, contiguous.  A
+ * row of zeros gets scale 0 and zeros.  A row with a NaN or an infinity keeps
+ * that as its scale and gets zeros: its products come out NaN.  rows = 0 is an
+ * empty call.  E_UNSUPPORTED: DTYPE; NONPOSITIVE_DIM; TOO_LARGE (rows or dim of
+ * 2^31 or more, or 2^48 elements or more); NULLPTR; ALIGN; OVERLAP;
+ * NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.  E_HIP.  Asynchronous, allocates nothing.
+ */
+int ltx3drope_q8_quantize(int dtype, int64_t rows, int64_t dim, const void* x, void* q, float* scale, void* stream,
+                          int* reason);
+
+/*
+ * A linear layer in 8-bit integers:
+ *     y[m][n] = (sum_k a[m][k] * b[n][k]) * a_scale[m] * b_scale[n] + bias[n]
+ * a [tokens, dim] and b [out, dim] int8, a_scale [tokens], b_scale and bias
+ * [out] fp32 (bias may be NULL), y [tokens, out] of `dtype` (F32 or BF16),
+ * contiguous.  The integer sums are exact; the rest is fp32, y rounded once.
+ * `workspace` as for ltx3drope_gated_ffn: needed only where more than 64 tokens
+ * meet a dim that is not a multiple of 16, or an a or b that does not start on a
+ * 16-byte boundary.  tokens = 0 or out = 0 is an empty call.  E_INVALID: a NULL
+ * descriptor, reserved not 0, a workspace that is too small.  E_UNSUPPORTED:
+ * DTYPE; NONPOSITIVE_DIM; TOO_LARGE (dim > 131071, whose sums could pass 32
+ * bits, tokens or out of 2^26 or more, or more than 2^23 output tiles of 128 x
+ * 64); NULLPTR; ALIGN; OVERLAP;
+ * NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.  E_HIP.  Asynchronous, allocates nothing.
+ */
+typedef struct {
+    int32_t dtype, reserved;
+    int64_t tokens, dim, out;
+    const void *a, *b;
+    const float *a_scale, *b_scale, *bias;
+    void* y;
+    void* workspace;
+    int64_t workspace_bytes;
+} ltx3drope_q8_matmul_t;
+int ltx3drope_q8_matmul(const ltx3drope_q8_matmul_t* call, void* stream, int* reason);
+int64_t ltx3drope_q8_matmul_workspace(const ltx3drope_q8_matmul_t* call);
+
 /* Gate state of one unsharded configuration (tables built for the tensor's own grid, no offsets):
  * LTX3DROPE_GATE_*, or a negative status. */
 int ltx3drope_gate_state(int device, int dtype, int64_t B, int64_t T, int64_t H, int64_t W,

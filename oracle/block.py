@@ -108,3 +108,23 @@ def gated_ffn_backward(dh, x, w_gate, w_up, g, u, kind):
     """dx, dw_gate, dw_up from the saved projections g and u."""
     dg, du = dh * u * act_slope(g, kind), dh * act(g, kind)
     return dg @ w_gate + du @ w_up, dg.T @ x, du.T @ x
+
+
+def q8_quantize(x):
+    """q and scale of float32 rows (numpy arithmetic in float32, each step rounded once)."""
+    import numpy as np
+
+    x = x.float().numpy()
+    top = np.abs(x).max(axis=-1) if x.shape[-1] else np.zeros(x.shape[:-1], np.float32)
+    scale = (top * (np.float32(1.0) / np.float32(127.0))).astype(np.float32)
+    plain = np.isfinite(scale) & (scale > 0)
+    safe = np.where(plain, scale, np.float32(1.0))[..., None]
+    with np.errstate(invalid="ignore"):
+        q = np.where(plain[..., None], np.rint((x / safe).astype(np.float32)), np.float32(0.0))
+    return torch.from_numpy(np.clip(q, -127, 127).astype(np.int8)), torch.from_numpy(scale)
+
+
+def q8_matmul(a, a_scale, b, b_scale, bias):
+    """The product in float64 (integer sums below 2^53 are exact)."""
+    y = (a.double() @ b.double().T) * a_scale.double()[:, None] * b_scale.double()
+    return y if bias is None else y + bias.double()

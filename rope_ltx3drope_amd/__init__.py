@@ -37,7 +37,7 @@ __all__ = [
     "forward_pair", "kernel_choice", "stats", "stats_reset", "set_option", "get_option", "gate_state", "gate_reset",
     "cache_clear", "copy_bytes", "version", "neox_can_use", "neox_apply_qk", "neox_position_errors", "patchify",
     "unpatchify", "dit_freq_grid", "norm_before", "norm_after", "norm_before_backward", "norm_after_backward",
-    "NormBeforeGrads", "NormAfterGrads",
+    "NormBeforeGrads", "NormAfterGrads", "gated_ffn", "gated_ffn_backward", "q8_quantize", "q8_matmul",
 ]
 
 
@@ -622,6 +622,148 @@ def norm_after_backward(dr, dn, y, r, weight=None, gate=None, *, post_norm: bool
     return NormAfterGrads(*_norm_backward(y, pd, 1, bool(post_norm), bool(next_norm), size, eps, weight_offset,
                                           residual_scale, stream, dr, dn, y, r, weight, gate, next_weight, next_scale,
                                           next_shift))
+
+
+def _matrix(t, shape, dtype, device):
+    """Checks of an operand of a product: its shape, dtype and device, contiguous."""
+    if tuple(t.shape) != tuple(shape):
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    if t.dtype != dtype:
+        raise Ltx3dRopeUnsupported("DTYPE")
+    if not t.is_cuda or t.device != device:
+        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+    if not t.is_contiguous():
+        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+
+
+def _activation(name: str) -> int:
+    try:
+        return _lib.ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {sorted(_lib.ACTIVATIONS)}") from None
+
+
+def _with_workspace(call, query, device):
+    """Gives a call the workspace that it asks for; returns the tensor, to be held until the launch."""
+    n = int(query(call))
+    if n <= 0:
+        return None
+    ws = _torch().empty(n, dtype=_torch().uint8, device=device)
+    call.workspace, call.workspace_bytes = ws.data_ptr(), n
+    return ws
+
+
+def gated_ffn(x, w_gate, w_up, activation: str = "silu", *, save: bool = False, out=None, stream=None):
+    """The gated feed-forward block act(x w_gate^T) * (x w_up^T), in one kernel.
+
+    x [..., dim]; w_gate, w_up [hidden, dim]; float32 or bfloat16, all of one dtype; activation "silu",
+    "gelu" or "gelu_tanh".  Returns h [..., hidden]; with save=True (h, g, u), g and u being the two
+    projections for gated_ffn_backward, in float32 whatever x's dtype."""
+    torch = _torch()
+    act = _activation(activation)
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    dim, hidden = int(x.shape[-1]), int(w_gate.shape[0])
+    shape = tuple(x.shape[:-1]) + (hidden,)
+    _matrix(x, x.shape, x.dtype, x.device)
+    for w in (w_gate, w_up):
+        _matrix(w, (hidden, dim), x.dtype, x.device)
+    if out is not None:
+        _matrix(out, shape, x.dtype, x.device)
+    with _On(stream):
+        h = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
+        g, u = (torch.empty(shape, dtype=torch.float32, device=x.device) for _ in range(2)) if save else (None, None)
+        c = _lib.GatedFfn(dtype=_dtype_code(x), activation=act, tokens=x.numel() // dim if dim else 0, dim=dim,
+                          hidden=hidden, x=x.data_ptr(), w_gate=w_gate.data_ptr(), w_up=w_up.data_ptr(),
+                          h=h.data_ptr(), g=_ptr(g), u=_ptr(u))
+        ws = _with_workspace(c, _lib.lib().ltx3drope_gated_ffn_workspace, x.device)
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_gated_ffn(c, _stream_ptr(x.device, stream), reason)
+    del ws
+    _block_check(st, reason, "gated_ffn")
+    return (h, g, u) if save else h
+
+
+def gated_ffn_backward(dh, x, w_gate, w_up, g, u, activation: str = "silu", *, need_dx: bool = True,
+                       need_dw: bool = True, stream=None):
+    """(dx, dw_gate, dw_up) of gated_ffn for the gradient dh of h, from the g and u that it saved.
+    need_dx=False or need_dw=False leaves those out (None)."""
+    torch = _torch()
+    act = _activation(activation)
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    dim, hidden = int(x.shape[-1]), int(w_gate.shape[0])
+    _matrix(x, x.shape, x.dtype, x.device)
+    for w in (w_gate, w_up):
+        _matrix(w, (hidden, dim), x.dtype, x.device)
+    for t, dtype in ((dh, x.dtype), (g, torch.float32), (u, torch.float32)):
+        _matrix(t, tuple(x.shape[:-1]) + (hidden,), dtype, x.device)
+    with _On(stream):
+        dx = torch.empty_like(x) if need_dx else None
+        dwg, dwu = (torch.empty_like(w_gate), torch.empty_like(w_up)) if need_dw else (None, None)
+        c = _lib.GatedFfnBackward(dtype=_dtype_code(x), activation=act, tokens=x.numel() // dim if dim else 0, dim=dim,
+                                  hidden=hidden, dh=dh.data_ptr(), x=x.data_ptr(), w_gate=w_gate.data_ptr(),
+                                  w_up=w_up.data_ptr(), g=g.data_ptr(), u=u.data_ptr(), dx=_ptr(dx),
+                                  dw_gate=_ptr(dwg), dw_up=_ptr(dwu))
+        ws = _with_workspace(c, _lib.lib().ltx3drope_gated_ffn_backward_workspace, x.device)
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_gated_ffn_backward(c, _stream_ptr(x.device, stream), reason)
+    del ws
+    _block_check(st, reason, "gated_ffn_backward")
+    return dx, dwg, dwu
+
+
+def q8_quantize(x, *, q_out=None, scale_out=None, stream=None):
+    """Rows to 8-bit integers: (q int8 like x, scale float32 [...]) with scale = max |row| * (1/127) and
+    q = round(x / scale).  x [..., dim], float32 or bfloat16."""
+    torch = _torch()
+    if x.dim() < 1:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    _matrix(x, x.shape, x.dtype, x.device)
+    dim = int(x.shape[-1])
+    with _On(stream):
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device) if q_out is None else q_out
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if scale_out is None else scale_out
+    _matrix(q, x.shape, torch.int8, x.device)
+    _matrix(scale, x.shape[:-1], torch.float32, x.device)
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_q8_quantize(_dtype_code(x), scale.numel(), dim, x.data_ptr(), q.data_ptr(),
+                                          scale.data_ptr(), _stream_ptr(x.device, stream), reason)
+    _block_check(st, reason, "q8_quantize")
+    return q, scale
+
+
+def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream=None):
+    """The 8-bit linear layer (a b^T) * a_scale[:, None] * b_scale + bias.
+
+    a int8 [..., dim] with a_scale float32 [...] (one a token, as q8_quantize gives them); b int8
+    [out, dim] with b_scale float32 [out] (one a channel); bias float32 [out] or None; dtype of the
+    result: bfloat16 (default) or float32."""
+    torch = _torch()
+    if a.dim() < 1 or b.dim() != 2:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    dim, n = int(a.shape[-1]), int(b.shape[0])
+    _matrix(a, a.shape, torch.int8, a.device)
+    _matrix(b, (n, dim), torch.int8, a.device)
+    _matrix(a_scale, a.shape[:-1], torch.float32, a.device)
+    _matrix(b_scale, (n,), torch.float32, a.device)
+    if bias is not None:
+        _matrix(bias, (n,), torch.float32, a.device)
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    shape = tuple(a.shape[:-1]) + (n,)
+    if out is not None:
+        _matrix(out, shape, dtype, a.device)
+    with _On(stream):
+        y = torch.empty(shape, dtype=dtype, device=a.device) if out is None else out
+        c = _lib.Q8Matmul(dtype=_dtype_code(y), tokens=a_scale.numel(), dim=dim, out=n, a=a.data_ptr(), b=b.data_ptr(),
+                          a_scale=a_scale.data_ptr(), b_scale=b_scale.data_ptr(), bias=_ptr(bias), y=y.data_ptr())
+        ws = _with_workspace(c, _lib.lib().ltx3drope_q8_matmul_workspace, a.device)
+    reason = ctypes.c_int(0)
+    st = _lib.lib().ltx3drope_q8_matmul(c, _stream_ptr(a.device, stream), reason)
+    del ws
+    _block_check(st, reason, "q8_matmul")
+    return y
 
 
 def kernel_choice(q, k, tabs: Tables, q_out=None, k_out=None) -> str:

@@ -48,7 +48,12 @@ EXPORTS = (
     "ltx3drope_stats_reset", "ltx3drope_kernel_choice", "ltx3drope_copy", "ltx3drope_status_string",
     "ltx3drope_reason_string", "ltx3drope_version",
     "ltx3drope_norm", "ltx3drope_norm_backward", "ltx3drope_norm_backward_workspace",
+    "ltx3drope_gated_ffn", "ltx3drope_gated_ffn_workspace", "ltx3drope_gated_ffn_backward",
+    "ltx3drope_gated_ffn_backward_workspace", "ltx3drope_q8_quantize", "ltx3drope_q8_matmul",
+    "ltx3drope_q8_matmul_workspace",
 )
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 i64 = ctypes.c_int64
 vp = ctypes.c_void_p
@@ -88,6 +93,26 @@ class NormBackward(ctypes.Structure):
     _fields_ = _NORM_SCALARS + [(n, vp) for n in (
         "dr", "dn", "y", "r", "weight", "gate", "next_weight", "next_scale",
         "dresidual", "dy", "dweight", "dgate", "dnext_weight", "dnext_scale", "dnext_shift", "workspace")] + [
+        ("workspace_bytes", i64)]
+
+
+_FFN_SIZES = [("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)] + [(n, i64) for n in (
+    "tokens", "dim", "hidden")]
+
+
+class GatedFfn(ctypes.Structure):
+    _fields_ = _FFN_SIZES + [(n, vp) for n in ("x", "w_gate", "w_up", "h", "g", "u", "workspace")] + [
+        ("workspace_bytes", i64)]
+
+
+class GatedFfnBackward(ctypes.Structure):
+    _fields_ = _FFN_SIZES + [(n, vp) for n in (
+        "dh", "x", "w_gate", "w_up", "g", "u", "dx", "dw_gate", "dw_up", "workspace")] + [("workspace_bytes", i64)]
+
+
+class Q8Matmul(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)] + [(n, i64) for n in (
+        "tokens", "dim", "out")] + [(n, vp) for n in ("a", "b", "a_scale", "b_scale", "bias", "y", "workspace")] + [
         ("workspace_bytes", i64)]
 
 
@@ -155,6 +180,15 @@ def lib() -> ctypes.CDLL:
             "ltx3drope_norm_backward": (ctypes.c_int, [ctypes.POINTER(NormBackward), vp,
                                                        ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_norm_backward_workspace": (i64, [ctypes.POINTER(NormBackward)]),
+            "ltx3drope_gated_ffn": (ctypes.c_int, [ctypes.POINTER(GatedFfn), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_gated_ffn_workspace": (i64, [ctypes.POINTER(GatedFfn)]),
+            "ltx3drope_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(GatedFfnBackward), vp,
+                                                            ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_gated_ffn_backward_workspace": (i64, [ctypes.POINTER(GatedFfnBackward)]),
+            "ltx3drope_q8_quantize": (ctypes.c_int, [ctypes.c_int, i64, i64, vp, vp, vp, vp,
+                                                     ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_q8_matmul": (ctypes.c_int, [ctypes.POINTER(Q8Matmul), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_q8_matmul_workspace": (i64, [ctypes.POINTER(Q8Matmul)]),
         }
         assert set(sig) == set(EXPORTS)
         for name, (res, args) in sig.items():

@@ -39,6 +39,8 @@ SOURCES = [  # (file, language, extra flags)
     ("patchify.hip", "hip", DEVICE),
     ("dit_freqs.hip", "hip", DEVICE),
     ("norm.hip", "hip", DEVICE),
+    ("ffn.hip", "hip", DEVICE),
+    ("q8.hip", "hip", DEVICE),
     ("api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),
     ("block_api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),
     ("tables.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include"), "-fno-builtin"]),

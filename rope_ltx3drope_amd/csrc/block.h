@@ -1,5 +1,5 @@
 // The transformer-block operators: what the host side (block_api.cpp) hands to the kernel launchers
-// (norm.hip).  Sizes fit in 32 bits unless they are size_t; offsets into tensors are formed in 64.
+// (norm.hip, ffn.hip, q8.hip).  Sizes fit in 32 bits unless they are size_t; offsets into tensors are formed in 64.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -36,5 +36,44 @@ constexpr int64_t kNormMaxBatch = 65535;  // one grid row a sample
 hipError_t launch_norm_forward(const NormForward& p, bool f32, bool vec, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackward& p, bool f32, bool vec, hipStream_t stream);
 size_t norm_backward_workspace(uint32_t batch, uint32_t rows, uint32_t dim);
+
+// The gated feed-forward block (ffn.hip).  x [tokens, dim], weights [hidden, dim], h, g, u and dh
+// [tokens, hidden], g and u in fp32.  activation: LTX3DROPE_ACT_*.
+struct FfnProblem {
+    const void *x, *w_gate, *w_up;
+    void* h;
+    float *g, *u;  // both or neither
+    void* workspace;
+    uint32_t tokens, dim, hidden;
+    int activation;
+};
+struct FfnBackwardProblem {
+    const void *dh, *x, *w_gate, *w_up;
+    const float *g, *u;
+    void *dx, *dw_gate, *dw_up;  // dx may be NULL; the weights' both or neither
+    void* workspace;
+    uint32_t tokens, dim, hidden;
+    int activation;
+};
+constexpr int64_t kFfnMaxSize = int64_t(1) << 21;  // a tile of 256 rows of 2 * hidden fp32 stays within 2^31 bytes
+constexpr int64_t kMaxTiles = int64_t(1) << 23;    // 128 x 64 output tiles of a launch of 256 threads each
+size_t ffn_workspace(const FfnProblem& p, bool f32);
+size_t ffn_backward_workspace(const FfnBackwardProblem& p, bool f32);
+hipError_t launch_ffn(const FfnProblem& p, bool f32, hipStream_t stream);
+hipError_t launch_ffn_backward(const FfnBackwardProblem& p, bool f32, hipStream_t stream);
+
+// The 8-bit linear layer (q8.hip): a [tokens, dim] and b [out, dim] int8, y [tokens, out].
+struct Q8Problem {
+    const void *a, *b;
+    const float *a_scale, *b_scale, *bias;  // [tokens], [out], [out] or NULL
+    void* y;
+    void* workspace;
+    uint32_t tokens, dim, out;
+};
+constexpr int64_t kQ8MaxDim = 131071;  // (2^31 - 1) / 2^14: the sums stay within 32-bit integers
+size_t q8_workspace(const Q8Problem& p);
+hipError_t launch_q8(const Q8Problem& p, bool f32, hipStream_t stream);
+hipError_t launch_q8_quantize(const void* x, void* q, float* scale, uint32_t rows, uint32_t dim, bool f32,
+                              hipStream_t stream);
 
 }  // namespace ltx3drope

@@ -102,6 +102,97 @@ size_t norm_workspace(const ltx3drope_norm_backward_t& c) {
                                    static_cast<uint32_t>(c.dim));
 }
 
+// A product's launch: 128 x 64 tiles (the smallest) of 256 threads stay below 2^31 threads.
+bool too_many_tiles(int64_t M, int64_t N) { return (M / 128 + 1) * (N / 64 + 1) > kMaxTiles; }
+
+// The feed-forward block's scalars, both directions.
+template <class Call>
+int check_ffn(const Call& c, int* why) {
+    if (c.activation < LTX3DROPE_ACT_SILU || c.activation > LTX3DROPE_ACT_GELU_TANH) return LTX3DROPE_E_INVALID;
+    if (c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) {
+        *why = LTX3DROPE_REASON_DTYPE;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    if (c.dim <= 0 || c.tokens < 0 || c.hidden < 0) {
+        *why = LTX3DROPE_REASON_NONPOSITIVE_DIM;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    if (c.tokens >= kFfnMaxSize || c.dim >= kFfnMaxSize || 2 * c.hidden >= kFfnMaxSize ||
+        too_many_tiles(c.tokens, c.hidden) || too_many_tiles(c.tokens, c.dim) || too_many_tiles(2 * c.hidden, c.dim)) {
+        *why = LTX3DROPE_REASON_TOO_LARGE;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    return LTX3DROPE_OK;
+}
+
+FfnProblem ffn_problem(const ltx3drope_gated_ffn_t& c) {
+    FfnProblem p;
+    p.x = c.x;
+    p.w_gate = c.w_gate;
+    p.w_up = c.w_up;
+    p.h = c.h;
+    p.g = c.g;
+    p.u = c.u;
+    p.workspace = c.workspace;
+    p.tokens = static_cast<uint32_t>(c.tokens);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.hidden = static_cast<uint32_t>(c.hidden);
+    p.activation = c.activation;
+    return p;
+}
+
+FfnBackwardProblem ffn_problem(const ltx3drope_gated_ffn_backward_t& c) {
+    FfnBackwardProblem p;
+    p.dh = c.dh;
+    p.x = c.x;
+    p.w_gate = c.w_gate;
+    p.w_up = c.w_up;
+    p.g = c.g;
+    p.u = c.u;
+    p.dx = c.dx;
+    p.dw_gate = c.dw_gate;
+    p.dw_up = c.dw_up;
+    p.workspace = c.workspace;
+    p.tokens = static_cast<uint32_t>(c.tokens);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.hidden = static_cast<uint32_t>(c.hidden);
+    p.activation = c.activation;
+    return p;
+}
+
+int check_q8(const ltx3drope_q8_matmul_t& c, int* why) {
+    if (c.reserved != 0) return LTX3DROPE_E_INVALID;
+    if (c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) {
+        *why = LTX3DROPE_REASON_DTYPE;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    if (c.dim <= 0 || c.tokens < 0 || c.out < 0) {
+        *why = LTX3DROPE_REASON_NONPOSITIVE_DIM;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    const int64_t lim = int64_t(1) << 26;
+    if (c.dim > kQ8MaxDim || c.tokens >= lim || c.out >= lim || too_many_tiles(c.tokens, c.out)) {
+        *why = LTX3DROPE_REASON_TOO_LARGE;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    return LTX3DROPE_OK;
+}
+
+Q8Problem q8_problem(const ltx3drope_q8_matmul_t& c) {
+    Q8Problem p;
+    p.a = c.a;
+    p.b = c.b;
+    p.a_scale = c.a_scale;
+    p.b_scale = c.b_scale;
+    p.bias = c.bias;
+    p.y = c.y;
+    p.workspace = c.workspace;
+    p.tokens = static_cast<uint32_t>(c.tokens);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.out = static_cast<uint32_t>(c.out);
+    return p;
+}
+
 bool aligned16(const Spans& t) {
     for (int i = 0; i < t.n; ++i)
         if ((t.s[i].role == Role::RowIn || t.s[i].role == Role::RowOut) && reinterpret_cast<uintptr_t>(t.s[i].p) % 16)
@@ -258,6 +349,164 @@ int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream,
     const bool vectors = aligned16(t) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
     DeviceGuard guard(device);
     if (launch_norm_backward(p, f32, vectors, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int64_t ltx3drope_gated_ffn_workspace(const ltx3drope_gated_ffn_t* call) {
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_ffn(*call, &why);
+    if (st != LTX3DROPE_OK) return st;
+    if (call->tokens == 0 || call->hidden == 0) return 0;
+    return static_cast<int64_t>(ffn_workspace(ffn_problem(*call), call->dtype == LTX3DROPE_DTYPE_F32));
+}
+
+int ltx3drope_gated_ffn(const ltx3drope_gated_ffn_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_gated_ffn_t& c = *call;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_ffn(c, &why);
+    if (st == LTX3DROPE_E_UNSUPPORTED) return refuse(why, reason);
+    if (st != LTX3DROPE_OK) return st;
+    if ((c.g == nullptr) != (c.u == nullptr)) return LTX3DROPE_E_INVALID;
+    if (c.tokens == 0 || c.hidden == 0) return LTX3DROPE_OK;
+    const bool f32 = c.dtype == LTX3DROPE_DTYPE_F32;
+    const FfnProblem p = ffn_problem(c);
+    const size_t ws = ffn_workspace(p, f32);
+    if (c.workspace_bytes < 0 || static_cast<size_t>(c.workspace_bytes) < ws) return LTX3DROPE_E_INVALID;
+    if (!c.x || !c.w_gate || !c.w_up || !c.h || (ws != 0 && !c.workspace))
+        return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t es = elem(c.dtype), M = p.tokens, D = p.dim, F = p.hidden;
+    Spans t;
+    t.add(c.x, M * D * es, es, Role::Param);
+    t.add(c.w_gate, F * D * es, es, Role::Param);
+    t.add(c.w_up, F * D * es, es, Role::Param);
+    t.add(c.h, M * F * es, es, Role::ParamOut);
+    for (const void* o : {c.g, c.u}) t.add(o, M * F * 4, 4, Role::ParamOut);
+    if (ws != 0) t.add(c.workspace, ws, 16, Role::Scratch);
+    int device = -1;
+    why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    DeviceGuard guard(device);
+    if (launch_ffn(p, f32, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int64_t ltx3drope_gated_ffn_backward_workspace(const ltx3drope_gated_ffn_backward_t* call) {
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_ffn(*call, &why);
+    if (st != LTX3DROPE_OK) return st;
+    if (call->tokens == 0 || call->hidden == 0) return 0;
+    return static_cast<int64_t>(ffn_backward_workspace(ffn_problem(*call), call->dtype == LTX3DROPE_DTYPE_F32));
+}
+
+int ltx3drope_gated_ffn_backward(const ltx3drope_gated_ffn_backward_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_gated_ffn_backward_t& c = *call;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_ffn(c, &why);
+    if (st == LTX3DROPE_E_UNSUPPORTED) return refuse(why, reason);
+    if (st != LTX3DROPE_OK) return st;
+    if ((c.dw_gate == nullptr) != (c.dw_up == nullptr)) return LTX3DROPE_E_INVALID;
+    if (c.dx == nullptr && c.dw_gate == nullptr) return LTX3DROPE_OK;
+    const bool f32 = c.dtype == LTX3DROPE_DTYPE_F32, empty = c.tokens == 0 || c.hidden == 0;
+    const FfnBackwardProblem p = ffn_problem(c);
+    const size_t ws = empty ? 0 : ffn_backward_workspace(p, f32);
+    if (c.workspace_bytes < 0 || static_cast<size_t>(c.workspace_bytes) < ws) return LTX3DROPE_E_INVALID;
+    const size_t es = elem(c.dtype), M = p.tokens, D = p.dim, F = p.hidden;
+    if (!empty && (!c.dh || !c.g || !c.u || (c.dw_gate && !c.x) || (c.dx && (!c.w_gate || !c.w_up)) || !c.workspace))
+        return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    Spans t;
+    if (!empty) {
+        t.add(c.dh, M * F * es, es, Role::Param);
+        for (const void* i : {c.g, c.u}) t.add(i, M * F * 4, 4, Role::Param);
+        if (c.dw_gate) t.add(c.x, M * D * es, es, Role::Param);
+        if (c.dx)
+            for (const void* i : {c.w_gate, c.w_up}) t.add(i, F * D * es, es, Role::Param);
+        t.add(c.workspace, ws, 16, Role::Scratch);
+    }
+    t.add(c.dx, M * D * es, es, Role::ParamOut);
+    t.add(c.dw_gate, F * D * es, es, Role::ParamOut);
+    t.add(c.dw_up, F * D * es, es, Role::ParamOut);
+    if (t.n == 0) return LTX3DROPE_OK;
+    int device = -1;
+    why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    DeviceGuard guard(device);
+    if (launch_ffn_backward(p, f32, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int ltx3drope_q8_quantize(int dtype, int64_t rows, int64_t dim, const void* x, void* q, float* scale, void* stream,
+                          int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (dtype != LTX3DROPE_DTYPE_F32 && dtype != LTX3DROPE_DTYPE_BF16) return refuse(LTX3DROPE_REASON_DTYPE, reason);
+    if (dim <= 0 || rows < 0) return refuse(LTX3DROPE_REASON_NONPOSITIVE_DIM, reason);
+    const int64_t lim = int64_t(1) << 31;
+    if (dim >= lim || rows >= lim || (rows != 0 && dim > (int64_t(1) << 48) / rows))
+        return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
+    if (rows == 0) return LTX3DROPE_OK;
+    if (!x || !q || !scale) return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(dim), es = elem(dtype);
+    Spans t;
+    t.add(x, n * es, es, Role::Param);
+    t.add(q, n, 1, Role::ParamOut);
+    t.add(scale, static_cast<size_t>(rows) * 4, 4, Role::ParamOut);
+    int device = -1;
+    const int why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    DeviceGuard guard(device);
+    if (launch_q8_quantize(x, q, scale, static_cast<uint32_t>(rows), static_cast<uint32_t>(dim),
+                           dtype == LTX3DROPE_DTYPE_F32, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int64_t ltx3drope_q8_matmul_workspace(const ltx3drope_q8_matmul_t* call) {
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_q8(*call, &why);
+    if (st != LTX3DROPE_OK) return st;
+    if (call->tokens == 0 || call->out == 0) return 0;
+    return static_cast<int64_t>(q8_workspace(q8_problem(*call)));
+}
+
+int ltx3drope_q8_matmul(const ltx3drope_q8_matmul_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_q8_matmul_t& c = *call;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_q8(c, &why);
+    if (st == LTX3DROPE_E_UNSUPPORTED) return refuse(why, reason);
+    if (st != LTX3DROPE_OK) return st;
+    if (c.tokens == 0 || c.out == 0) return LTX3DROPE_OK;
+    const Q8Problem p = q8_problem(c);
+    const size_t ws = q8_workspace(p);
+    if (c.workspace_bytes < 0 || static_cast<size_t>(c.workspace_bytes) < ws) return LTX3DROPE_E_INVALID;
+    if (!c.a || !c.b || !c.a_scale || !c.b_scale || !c.y || (ws != 0 && !c.workspace))
+        return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t M = p.tokens, K = p.dim, N = p.out, es = elem(c.dtype);
+    Spans t;
+    t.add(c.a, M * K, 1, Role::Param);
+    t.add(c.b, N * K, 1, Role::Param);
+    t.add(c.a_scale, M * 4, 4, Role::Param);
+    t.add(c.b_scale, N * 4, 4, Role::Param);
+    t.add(c.bias, N * 4, 4, Role::Param);
+    t.add(c.y, M * N * es, es, Role::ParamOut);
+    if (ws != 0) t.add(c.workspace, ws, 16, Role::Scratch);
+    int device = -1;
+    why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    DeviceGuard guard(device);
+    if (launch_q8(p, c.dtype == LTX3DROPE_DTYPE_F32, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return LTX3DROPE_E_HIP;
     count_launch();
     return LTX3DROPE_OK;
 }

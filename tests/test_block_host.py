@@ -156,7 +156,116 @@ def test_norm_workspace_sizes():
     assert size(backward_call(eps=0.0)) == _lib.E_INVALID and size(None) == _lib.E_INVALID
 
 
+# ---- refusals of the feed-forward block and the 8-bit linear layer -----------------------------------
+
+def ffn_call(**kw):
+    c = dict(dtype=1, activation=0, tokens=4, dim=64, hidden=32, x=FAKE, w_gate=FAKE * 2, w_up=FAKE * 3, h=FAKE * 4)
+    c.update(kw)
+    return _lib.GatedFfn(**c)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(activation=3), (_lib.E_INVALID, "OK")), (dict(activation=-1), (_lib.E_INVALID, "OK")),
+    (dict(g=FAKE * 5), (_lib.E_INVALID, "OK")),
+    (dict(tokens=65, dim=63), (_lib.E_INVALID, "OK")),  # rows to be padded, no workspace
+    (dict(tokens=65, dim=63, workspace_bytes=-1), (_lib.E_INVALID, "OK")),
+    (dict(tokens=65, dim=63, workspace_bytes=1 << 20), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(dtype=2), (_lib.E_UNSUPPORTED, "DTYPE")), (dict(dim=0), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")),
+    (dict(tokens=-1), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")), (dict(dim=1 << 21), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
+    (dict(hidden=1 << 20), (_lib.E_UNSUPPORTED, "TOO_LARGE")), (dict(tokens=1 << 21), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
+    (dict(tokens=1 << 20, hidden=1 << 19), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
+    (dict(x=None), (_lib.E_UNSUPPORTED, "NULLPTR")), (dict(h=None), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(x=FAKE + 1), (_lib.E_UNSUPPORTED, "ALIGN")), (dict(h=FAKE + 64), (_lib.E_UNSUPPORTED, "OVERLAP")),
+    (dict(g=FAKE * 4, u=FAKE * 5), (_lib.E_UNSUPPORTED, "OVERLAP")), (dict(), (_lib.E_UNSUPPORTED, "NOT_DEVICE_PTR")),
+    (dict(tokens=0, x=None, h=None), (_lib.OK, "OK")), (dict(hidden=0, x=None, h=None), (_lib.OK, "OK")),
+])
+def test_ffn_refusals(kw, want):
+    reason = ctypes.c_int(-1)
+    st = L.ltx3drope_gated_ffn(ffn_call(**kw), None, reason)
+    assert (st, _lib.REASONS[reason.value]) == want
+
+
+def ffn_backward_call(**kw):
+    c = dict(dtype=1, activation=0, tokens=4, dim=64, hidden=32, dh=FAKE, x=FAKE * 2, w_gate=FAKE * 3, w_up=FAKE * 4,
+             g=FAKE * 5, u=FAKE * 6, dx=FAKE * 7, dw_gate=FAKE * 8, dw_up=FAKE * 9, workspace=FAKE * 10,
+             workspace_bytes=1 << 19)
+    c.update(kw)
+    return _lib.GatedFfnBackward(**c)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dw_up=None), (_lib.E_INVALID, "OK")), (dict(workspace_bytes=64), (_lib.E_INVALID, "OK")),
+    (dict(activation=9), (_lib.E_INVALID, "OK")), (dict(dtype=5), (_lib.E_UNSUPPORTED, "DTYPE")),
+    (dict(workspace=None), (_lib.E_UNSUPPORTED, "NULLPTR")), (dict(g=None), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(x=None), (_lib.E_UNSUPPORTED, "NULLPTR")), (dict(w_up=None), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(workspace=FAKE * 10 + 4), (_lib.E_UNSUPPORTED, "ALIGN")), (dict(dx=FAKE), (_lib.E_UNSUPPORTED, "OVERLAP")),
+    (dict(dx=None, dw_gate=None, dw_up=None), (_lib.OK, "OK")), (dict(), (_lib.E_UNSUPPORTED, "NOT_DEVICE_PTR")),
+])
+def test_ffn_backward_refusals(kw, want):
+    reason = ctypes.c_int(-1)
+    st = L.ltx3drope_gated_ffn_backward(ffn_backward_call(**kw), None, reason)
+    assert (st, _lib.REASONS[reason.value]) == want
+
+
+def test_product_workspace_sizes():
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=64, dim=63)) == 0
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=65)) == 0
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=65, dim=63)) == (65 + 64) * 128
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=65, x=FAKE + 2)) == (65 + 64) * 128
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=0)) == 0
+    assert L.ltx3drope_gated_ffn_backward_workspace(ffn_backward_call(tokens=0)) == 0
+    assert L.ltx3drope_gated_ffn_backward_workspace(ffn_backward_call()) > 0
+    assert L.ltx3drope_q8_matmul_workspace(q8_call(tokens=65)) == 0
+    assert L.ltx3drope_q8_matmul_workspace(q8_call(tokens=65, dim=65)) == (65 + 8) * 80
+    for f in (L.ltx3drope_gated_ffn_workspace, L.ltx3drope_gated_ffn_backward_workspace,
+              L.ltx3drope_q8_matmul_workspace):
+        assert f(None) == _lib.E_INVALID
+
+
+def q8_call(**kw):
+    c = dict(dtype=1, reserved=0, tokens=4, dim=64, out=8, a=FAKE, b=FAKE * 2, a_scale=FAKE * 3, b_scale=FAKE * 4,
+             y=FAKE * 5)
+    c.update(kw)
+    return _lib.Q8Matmul(**c)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(reserved=1), (_lib.E_INVALID, "OK")), (dict(tokens=65, dim=65), (_lib.E_INVALID, "OK")),
+    (dict(dtype=2), (_lib.E_UNSUPPORTED, "DTYPE")), (dict(dim=0), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")),
+    (dict(dim=131072), (_lib.E_UNSUPPORTED, "TOO_LARGE")), (dict(out=1 << 26), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
+    (dict(tokens=1 << 20, out=1 << 20), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
+    (dict(a_scale=None), (_lib.E_UNSUPPORTED, "NULLPTR")), (dict(y=None), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(bias=FAKE * 6 + 2), (_lib.E_UNSUPPORTED, "ALIGN")), (dict(y=FAKE), (_lib.E_UNSUPPORTED, "OVERLAP")),
+    (dict(out=0, a=None), (_lib.OK, "OK")), (dict(tokens=0, a=None), (_lib.OK, "OK")),
+    (dict(), (_lib.E_UNSUPPORTED, "NOT_DEVICE_PTR")),
+])
+def test_q8_matmul_refusals(kw, want):
+    reason = ctypes.c_int(-1)
+    st = L.ltx3drope_q8_matmul(q8_call(**kw), None, reason)
+    assert (st, _lib.REASONS[reason.value]) == want
+
+
+@pytest.mark.parametrize("args,want", [
+    ((2, 3, 8, FAKE, FAKE * 2, FAKE * 3), (_lib.E_UNSUPPORTED, "DTYPE")),
+    ((0, 3, 0, FAKE, FAKE * 2, FAKE * 3), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")),
+    ((0, 1 << 31, 8, FAKE, FAKE * 2, FAKE * 3), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
+    ((0, 3, 8, None, FAKE * 2, FAKE * 3), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    ((0, 3, 8, FAKE + 2, FAKE * 2, FAKE * 3), (_lib.E_UNSUPPORTED, "ALIGN")),
+    ((0, 3, 8, FAKE, FAKE, FAKE * 3), (_lib.E_UNSUPPORTED, "OVERLAP")),
+    ((0, 3, 8, FAKE, FAKE * 2, FAKE * 3), (_lib.E_UNSUPPORTED, "NOT_DEVICE_PTR")),
+    ((0, 0, 8, None, None, None), (_lib.OK, "OK")),
+])
+def test_q8_quantize_refusals(args, want):
+    reason = ctypes.c_int(-1)
+    st = L.ltx3drope_q8_quantize(*args, None, reason)
+    assert (st, _lib.REASONS[reason.value]) == want
+
+
 @pytest.mark.parametrize("call", [
+    lambda: rla.gated_ffn(torch.zeros(4, 8), torch.zeros(6, 8), torch.zeros(6, 8)),
+    lambda: rla.q8_quantize(torch.zeros(4, 8)),
+    lambda: rla.q8_matmul(torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4), torch.zeros(6, 8, dtype=torch.int8),
+                          torch.zeros(6)),
     lambda: rla.norm_before(torch.zeros(2, 3, 8)),
     lambda: rla.norm_after(torch.zeros(2, 3, 8), torch.zeros(2, 3, 8)),
     lambda: rla.norm_before_backward(torch.zeros(2, 3, 8), torch.zeros(2, 3, 8)),
