@@ -455,9 +455,8 @@ int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call)
  * gradients carry no rounding of theirs.
  * `workspace`: ltx3drope_gated_ffn_workspace bytes of device memory, 16-byte
  * aligned, that nothing else uses until the call's work on `stream` has run.  It
- * is 0 (then workspace may be NULL) but where more than 64 tokens meet rows that
- * are not whole 16-byte chunks, or tensors that do not start on one: the call
- * then lays padded copies of x and the weights there.
+ * is 0 (then workspace may be NULL) but where more than 64 tokens meet long sums
+ * and few outputs: the sums are then split over the chip and their parts lie there.
  * tokens = 0 or hidden = 0 is an empty call: OK, nothing launched, no pointer
  * looked at.  E_INVALID: a NULL descriptor, an unknown activation, one of g and u without the other, a workspace that is too small.
  * E_UNSUPPORTED with the reason in *reason (which may be NULL), the first that
@@ -480,8 +479,8 @@ typedef struct {
     int64_t workspace_bytes;
 } ltx3drope_gated_ffn_t;
 int ltx3drope_gated_ffn(const ltx3drope_gated_ffn_t* call, void* stream, int* reason);
-/* Bytes of workspace for a call (its sizes, and whether x and the weights are 16-byte aligned), or a
-   negative status for a malformed descriptor. */
+/* Bytes of workspace for a call (its sizes, and the alignment of x and the weights), or a negative
+   status for a malformed descriptor. */
 int64_t ltx3drope_gated_ffn_workspace(const ltx3drope_gated_ffn_t* call);
 
 /*
@@ -528,9 +527,7 @@ int ltx3drope_q8_quantize(int dtype, int64_t rows, int64_t dim, const void* x, v
  * a [tokens, dim] and b [out, dim] int8, a_scale [tokens], b_scale and bias
  * [out] fp32 (bias may be NULL), y [tokens, out] of `dtype` (F32 or BF16),
  * contiguous.  The integer sums are exact; the rest is fp32, y rounded once.
- * `workspace` as for ltx3drope_gated_ffn: needed only where more than 64 tokens
- * meet a dim that is not a multiple of 16, or an a or b that does not start on a
- * 16-byte boundary.  tokens = 0 or out = 0 is an empty call.  E_INVALID: a NULL
+ * `workspace` as for ltx3drope_gated_ffn.  tokens = 0 or out = 0 is an empty call.  E_INVALID: a NULL
  * descriptor, reserved not 0, a workspace that is too small.  E_UNSUPPORTED:
  * DTYPE; NONPOSITIVE_DIM; TOO_LARGE (dim > 131071, whose sums could pass 32
  * bits, tokens or out of 2^26 or more, or more than 2^23 output tiles of 128 x

@@ -49,21 +49,28 @@ struct OpF32 {
     }
 };
 
-// One product.  Sizes are 32-bit; the host keeps a tile's rows (at most 256 of them) within 2^31 bytes.
+// One product, C[m][n] = sum_k A[m][k] * B[n][k].  An operand is stored with k innermost (rows of the
+// output's index, k_bytes bytes of k each) or with k outermost (rows of k, the output's index along
+// them).  Sizes are 32-bit; the host keeps what a tile addresses (256 rows of an operand with k
+// innermost, 64 of one with k outermost) within 2^31 bytes.
 struct Product {
     const char* a;
-    const char* b[2];  // [1] only for gated products
+    const char* b[2];           // [1]: the second matrix of a gated product, or B's rows of k from k_second on
     uint64_t a_pitch, b_pitch;  // bytes from row to row
-    uint32_t M, N;              // rows of A, rows of each B
-    uint32_t k_bytes;           // bytes of k in a row
+    uint32_t M, N;              // output sizes (N: of each B)
+    uint32_t k;                 // length of the sums
+    uint32_t k_second;          // k outermost: where b[1] takes over (a multiple of a step), or 0 for never
+    uint32_t k_rows;            // ... and the rows of k that b[0] and b[1] hold each (zeros from there on)
+    float* partial;             // splits > 1: [splits][tiles][BM * BN] sums
+    uint32_t splits;
 };
 
 constexpr int kRowBytes = 128;  // bytes of k that a tile holds of each row at a time
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
-// Tile (tm, tn) of workgroup `id`.  Workgroups go to the 8 XCDs in turn: each XCD gets one contiguous
-// run of tiles, and a run walks down groups of 8 tile rows, so that the tiles that one XCD's L2 serves
-// at a time share their rows of A and B.
+// Tile (tm, tn) of workgroup `id` of tiles_m * tiles_n.  Workgroups go to the 8 XCDs in turn: each XCD
+// gets one contiguous run of tiles, and a run walks down groups of 8 tile rows, so that the tiles that
+// one XCD's L2 serves at a time share their rows of A and B.
 __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
     const uint32_t total = tiles_m * tiles_n, q = total / 8, r = total % 8, x = id % 8, i = id / 8;
     const uint32_t t = x < r ? x * (q + 1) + i : r * (q + 1) + (x - r) * q + i;
@@ -77,126 +84,11 @@ __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t r, char* lds, 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voffset, soffset, 0, 0);
 }
 
-// All outstanding loads into LDS have landed, this wavefront's LDS reads are done, and so are every
-// other wavefront's.
-__device__ __forceinline__ void wait_all_and_meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// Position of chunk c of tile row r inside the row's 128 bytes: spread so that the lanes of one LDS
-// read fall into different banks.
-__device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
-
-// BM x BN tiles, WM x WN wavefronts, each with (BM / WM) x (BN / WN) of the tile in registers.
-// A row's next 128 bytes travel from memory to the other half of the LDS while this half is multiplied.
-// k_bytes and the pitches are multiples of 16 and the pointers 16-byte aligned (host's duty).
-template <class Op, int BM, int BN, int WM, int WN, bool GATED, class Done>
-__global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done done) {
-    constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
-    constexpr int kStage = (BM + BN) * kRowBytes;
-    constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // copies a wavefront makes of each operand
-    static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN, "tile rows split evenly over the wavefronts");
-    static_assert(!GATED || (CB % 2 == 0 && FN % 2 == 0), "both halves of B in every wavefront");
-    __shared__ __align__(1024) char lds[2 * kStage];
-
-    const uint32_t tid = threadIdx.x, lane = tid & 63;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t wm = wave / WN, wn = wave % WN;
-    constexpr int BNB = GATED ? BN / 2 : BN;  // rows of each B in a tile
-    uint32_t tm, tn;
-    tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BNB - 1) / BNB, tm, tn);
-    const uint32_t m0 = tm * BM, n0 = tn * BNB;
-    const uint32_t rows_a = p.M - m0 < BM ? p.M - m0 : BM, rows_b = p.N - n0 < BNB ? p.N - n0 : BNB;
-
-    auto resource = [&](const char* base, uint32_t row, uint64_t pitch, uint32_t rows) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base + row * pitch), 0,
-                                                 static_cast<int>((rows - 1) * pitch + p.k_bytes), 0x00020000);
-    };
-    const __amdgpu_buffer_rsrc_t ra = resource(p.a, m0, p.a_pitch, rows_a);
-    const __amdgpu_buffer_rsrc_t rb0 = resource(p.b[0], n0, p.b_pitch, rows_b);
-    const __amdgpu_buffer_rsrc_t rb1 = GATED ? resource(p.b[1], n0, p.b_pitch, rows_b) : rb0;
-
-    // copy i of this wavefront fills rows 8 * (i * NW + wave) .. + 7 of the tile; lane l brings the
-    // 16 bytes that belong at slot l % 8 of row l / 8.  Rows that do not exist are out of range: zeros.
-    uint32_t va[CA], vb[CB];
-    uint32_t chunk;
-    {
-        const uint32_t r8 = lane >> 3;
-#pragma unroll
-        for (int i = 0; i < CA; ++i) {
-            const uint32_t r = (i * NW + wave) * 8 + r8, c = (lane & 7) ^ swizzle(r);
-            va[i] = r < rows_a ? static_cast<uint32_t>(r * p.a_pitch) + c * 16 : kOutOfRange;
-        }
-#pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            const uint32_t r = ((GATED ? i % (CB / 2) : i) * NW + wave) * 8 + r8;
-            const uint32_t c = (lane & 7) ^ swizzle(r);
-            vb[i] = r < rows_b ? static_cast<uint32_t>(r * p.b_pitch) + c * 16 : kOutOfRange;
-        }
-        // NW is even: every copy of a lane has the same chunk
-        chunk = ((lane & 7) ^ swizzle(wave * 8 + r8)) * 16;
-    }
-    static_assert(NW % 2 == 0, "one chunk a lane");
-
-    const uint32_t steps = (p.k_bytes + kRowBytes - 1) / kRowBytes;
-    auto fetch = [&](uint32_t step) {
-        char* at = lds + (step & 1) * kStage;
-        const uint32_t k = step * kRowBytes;
-        const bool past = k + chunk >= p.k_bytes;  // only in the last step
-#pragma unroll
-        for (int i = 0; i < CA; ++i)
-            lds_copy16(ra, at + (i * NW + wave) * 1024, past ? kOutOfRange : va[i], k);
-#pragma unroll
-        for (int i = 0; i < CB; ++i)
-            lds_copy16(GATED && i >= CB / 2 ? rb1 : rb0, at + BM * kRowBytes + (i * NW + wave) * 1024,
-                       past ? kOutOfRange : vb[i], k);
-    };
-
-    using Acc = typename Op::Acc;
-    Acc acc[FM][FN] = {};
-    // this lane's place in a 16-row block; the blocks start at multiples of 16 rows
-    const uint32_t row = (lane & 15) * kRowBytes, sw = swizzle(lane & 15);
-    const uint32_t pos[2] = {row + (((lane >> 4) ^ sw) << 4), row + (((4 + (lane >> 4)) ^ sw) << 4)};
-    const uint32_t a_at = wm * (BM / WM) * kRowBytes;
-    // gated: half of the wavefront's blocks are rows of the gate, half the same rows of the other
-    auto b_block = [&](int j) {
-        if constexpr (GATED) return (j < FN / 2 ? 0 : BN / 2) + wn * (BN / WN / 2) + (j % (FN / 2)) * 16;
-        else return wn * (BN / WN) + j * 16;
-    };
-
-    fetch(0);
-    for (uint32_t s = 0; s < steps; ++s) {
-        wait_all_and_meet();
-        if (s + 1 < steps) fetch(s + 1);
-        const char* at = lds + (s & 1) * kStage;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 a[FM], b[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                b[j] = *reinterpret_cast<const u32x4*>(at + BM * kRowBytes + b_block(j) * kRowBytes + pos[kk]);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                a[i] = *reinterpret_cast<const u32x4*>(at + a_at + i * 16 * kRowBytes + pos[kk]);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) Op::mac(acc[i][j], b[j], a[i]);
-        }
-    }
-
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const uint32_t m = m0 + wm * (BM / WM) + i * 16 + (lane & 15);
-        if (m >= p.M) continue;
-#pragma unroll
-        for (int j = 0; j < (GATED ? FN / 2 : FN); ++j) {
-            const uint32_t n = n0 + (GATED ? wn * (BN / WN / 2) : wn * (BN / WN)) + j * 16 + (lane >> 4) * 4;
-            if (n >= p.N) continue;
-            if constexpr (GATED) done(m, n, p.N, acc[i][j], acc[i][j + FN / 2]);
-            else done(m, n, p.N, acc[i][j]);
-        }
-    }
+// All but this wavefront's N newest loads have landed, its LDS reads and writes are done, and so are
+// every other wavefront's.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // 16 bytes of a row from byte k on; what lies past `end` is zero.  Without alignment the last chunk is
@@ -222,6 +114,335 @@ __device__ __forceinline__ u32x4 load_chunk(const char* row, uint32_t k, uint32_
     return v;
 }
 
+// One operand's part of a tile: R rows of the output's index against 128 bytes of k, in LDS.
+//
+// k innermost: tile row r is 128 bytes, eight 16-byte chunks; chunk c lies at slot c ^ (r / 2 % 8).
+// k outermost: LDS rows are rows of k, R elements each, in units of 16 elements; unit u of row k lies at
+// unit u ^ spread(k).  Both keep the lanes of one LDS read in different banks.
+template <class Op, int R, bool K_OUTER>
+struct Side {
+    static constexpr int kStepK = kRowBytes / Op::kElem;  // k of a step
+    static constexpr int kBytes = R * kRowBytes;          // LDS bytes of a step
+    static constexpr int kLdsRow = K_OUTER ? R * Op::kElem : kRowBytes;
+    static constexpr int kUnit = 16 * Op::kElem;
+
+    static __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
+    static __device__ __forceinline__ uint32_t spread(uint32_t k) {
+        return Op::kElem == 4 ? (k >> 2) & 3 : (k & 3) | ((k >> 3) & 1) << 2;
+    }
+
+    // What 16-byte place `at` of the LDS image holds: row `line` (of the output's index or of k) of the
+    // tile, 16 bytes from byte `byte` of the line on.
+    static __device__ __forceinline__ void place(uint32_t at, uint32_t& line, uint32_t& byte) {
+        line = at * 16 / kLdsRow;
+        const uint32_t slot = at % (kLdsRow / 16);
+        if constexpr (K_OUTER) {
+            constexpr uint32_t c = kUnit / 16;
+            byte = (((slot / c) ^ spread(line)) * c + slot % c) * 16;
+        } else {
+            byte = (slot ^ swizzle(line)) * 16;
+        }
+    }
+
+    // This lane's 16 bytes of block `blk` (16 rows of the output's index), half step kk.
+    // base: block_base(lane, blk) for k outermost, lane_base(lane) otherwise.
+    static __device__ __forceinline__ uint32_t lane_base(uint32_t lane, int kk) {
+        return (lane & 15) * kRowBytes + (((kk * 4 + (lane >> 4)) ^ swizzle(lane & 15)) << 4);
+    }
+    static __device__ __forceinline__ uint32_t block_base(uint32_t lane, uint32_t blk) {
+        const uint32_t q = lane >> 4;
+        if constexpr (Op::kElem == 4) {
+            return q * 4 * kLdsRow + ((blk ^ q) * kUnit) + (lane & 15) * 4;  // k = 16 kk + 4 q + j
+        } else {
+            const uint32_t k = q * 8 + (lane & 15) / 4;  // 4 lanes bring 16 numbers of one k
+            return k * kLdsRow + ((blk ^ spread(k)) * kUnit) + (lane & 3) * 8;
+        }
+    }
+    static __device__ __forceinline__ u32x4 outer_frag(const char* lds, uint32_t base, int kk) {
+        if constexpr (Op::kElem == 4) {
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(lds + base + (kk * 16 + j) * kLdsRow);
+            return v;
+        } else {
+            // each read turns 4 rows of k by 16 numbers: lane l gets number l % 16 of all four
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+            u32x2 h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                h[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                     (__attribute__((address_space(3))) s16x4*)(lds + base + (kk * 32 + j * 4) * kLdsRow)));
+            return u32x4{h[0][0], h[0][1], h[1][0], h[1][1]};
+        }
+    }
+};
+
+// BM x BN tiles, WM x WN wavefronts, each with (BM / WM) x (BN / WN) of the tile in registers; NS steps'
+// worth of LDS, so that NS - 1 steps travel from memory while one is multiplied.
+// DIRECT: 16-byte aligned operands go from memory to LDS without passing through registers; otherwise
+// they pass through them (any alignment).  A_OUTER, B_OUTER: k outermost.
+template <class Op, int BM, int BN, int WM, int WN, int NS, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
+          class Done>
+__global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done done) {
+    constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int BNB = GATED ? BN / 2 : BN;  // rows of each B in a tile
+    using SA = Side<Op, BM, A_OUTER>;
+    using SB = Side<Op, BNB, B_OUTER>;
+    constexpr int kStage = (BM + BN) * kRowBytes, kStepK = SA::kStepK;
+    constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies a wavefront makes of each operand
+    static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN, "a tile's copies split evenly over the wavefronts");
+    static_assert(!GATED || (CB % 2 == 0 && FN % 2 == 0 && !B_OUTER), "both halves of B in every wavefront");
+    __shared__ __align__(1024) char lds[NS * kStage];
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t wm = wave / WN, wn = wave % WN;
+    const uint32_t tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BNB - 1) / BNB, tiles = tiles_m * tiles_n;
+    const uint32_t tile = blockIdx.x % tiles, split = blockIdx.x / tiles;
+    uint32_t tm, tn;
+    tile_of(tile, tiles_m, tiles_n, tm, tn);
+    const uint32_t m0 = tm * BM, n0 = tn * BNB;
+    const uint32_t all_steps = (p.k + kStepK - 1) / kStepK;
+    const uint32_t first = split * all_steps / p.splits, last = (split + 1) * all_steps / p.splits;
+
+    // ---- from memory to LDS: copy i of this wavefront fills KB i * NW + wave of an operand's image
+    uint32_t line_a[CA], byte_a[CA], line_b[CB], byte_b[CB];
+#pragma unroll
+    for (int i = 0; i < CA; ++i) SA::place((i * NW + wave) * 64 + lane, line_a[i], byte_a[i]);
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+        SB::place(((GATED ? i % (CB / 2) : i) * NW + wave) * 64 + lane, line_b[i], byte_b[i]);
+
+    // the descriptor of an operand for one step, and this lane's byte in it (or out of range: zeros)
+    auto resource = [](const char* base, uint64_t pitch, uint32_t lines, uint32_t bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0,
+                                                 static_cast<int>(lines == 0 ? 0 : (lines - 1) * pitch + bytes),
+                                                 0x00020000);
+    };
+    auto inner_rsrc = [&](const char* base, uint64_t pitch, uint32_t row0, uint32_t rows, uint32_t R) {
+        const uint32_t n = rows - row0 < R ? rows - row0 : R;
+        return resource(base + row0 * pitch, pitch, n, p.k * Op::kElem);
+    };
+    __amdgpu_buffer_rsrc_t ra, rb0, rb1;
+    uint32_t va[CA], vb[CB];
+    if constexpr (DIRECT) {
+        if constexpr (!A_OUTER) ra = inner_rsrc(p.a, p.a_pitch, m0, p.M, BM);
+        if constexpr (!B_OUTER) {
+            rb0 = inner_rsrc(p.b[0], p.b_pitch, n0, p.N, BNB);
+            rb1 = GATED ? inner_rsrc(p.b[1], p.b_pitch, n0, p.N, BNB) : rb0;
+        }
+#pragma unroll
+        for (int i = 0; i < CA; ++i) {
+            const bool in = A_OUTER ? m0 * Op::kElem + byte_a[i] < p.M * Op::kElem : m0 + line_a[i] < p.M;
+            va[i] = in ? static_cast<uint32_t>(line_a[i] * p.a_pitch) + byte_a[i] : kOutOfRange;
+        }
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+            const bool in = B_OUTER ? n0 * Op::kElem + byte_b[i] < p.N * Op::kElem : n0 + line_b[i] < p.N;
+            vb[i] = in ? static_cast<uint32_t>(line_b[i] * p.b_pitch) + byte_b[i] : kOutOfRange;
+        }
+    }
+    // for k outermost: which matrix a step belongs to, its first row of k, and how many of a step's rows exist
+    auto b_segment = [&](uint32_t step, uint32_t& k0, uint32_t& rows) {
+        const uint32_t k = step * kStepK;
+        const bool second = p.k_second != 0 && k >= p.k_second;
+        k0 = second ? k - p.k_second : k;
+        const uint32_t have = p.k_second != 0 ? p.k_rows : p.k;
+        rows = k0 < have ? (have - k0 < kStepK ? have - k0 : kStepK) : 0;
+        return second ? p.b[1] : p.b[0];
+    };
+    auto fetch = [&](uint32_t step, uint32_t slot) {
+        char* at = lds + slot * kStage;
+        const uint32_t k = step * kRowBytes;
+        if constexpr (A_OUTER) {
+            const uint32_t k0 = step * kStepK, rows = p.k - k0 < kStepK ? p.k - k0 : kStepK;
+            ra = resource(p.a + k0 * p.a_pitch + m0 * Op::kElem, p.a_pitch, rows, (p.M - m0) * Op::kElem);
+        }
+        if constexpr (B_OUTER) {
+            uint32_t k0, rows;
+            const char* base = b_segment(step, k0, rows);
+            rb0 = resource(base + k0 * p.b_pitch + n0 * Op::kElem, p.b_pitch, rows, (p.N - n0) * Op::kElem);
+        }
+#pragma unroll
+        for (int i = 0; i < CA; ++i) {
+            const bool past = !A_OUTER && k + byte_a[i] >= p.k * Op::kElem;  // only in the last step
+            lds_copy16(ra, at + (i * NW + wave) * 1024, past ? kOutOfRange : va[i], A_OUTER ? 0 : k);
+        }
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+            const bool past = !B_OUTER && k + byte_b[i] >= p.k * Op::kElem;
+            lds_copy16(GATED && i >= CB / 2 ? rb1 : rb0, at + SA::kBytes + (i * NW + wave) * 1024,
+                       past ? kOutOfRange : vb[i], B_OUTER ? 0 : k);
+        }
+    };
+    u32x4 held[DIRECT ? 1 : CA + CB];
+    auto hold = [&](uint32_t step) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < CA; ++i) {
+                held[i] = u32x4{0, 0, 0, 0};
+                if constexpr (A_OUTER) {
+                    const uint32_t k = step * kStepK + line_a[i];
+                    if (k < p.k)
+                        held[i] = load_chunk<Op, false>(p.a + k * p.a_pitch, m0 * Op::kElem + byte_a[i], p.M * Op::kElem);
+                } else if (m0 + line_a[i] < p.M) {
+                    held[i] = load_chunk<Op, false>(p.a + (m0 + line_a[i]) * p.a_pitch, step * kRowBytes + byte_a[i],
+                                                    p.k * Op::kElem);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < CB; ++i) {
+                u32x4& h = held[CA + i];
+                h = u32x4{0, 0, 0, 0};
+                if constexpr (B_OUTER) {
+                    uint32_t k0, rows;
+                    const char* base = b_segment(step, k0, rows);
+                    if (line_b[i] < rows)
+                        h = load_chunk<Op, false>(base + (k0 + line_b[i]) * p.b_pitch, n0 * Op::kElem + byte_b[i],
+                                                  p.N * Op::kElem);
+                } else if (n0 + line_b[i] < p.N) {
+                    h = load_chunk<Op, false>(p.b[GATED && i >= CB / 2] + (n0 + line_b[i]) * p.b_pitch,
+                                              step * kRowBytes + byte_b[i], p.k * Op::kElem);
+                }
+            }
+        }
+    };
+    auto put_held = [&](uint32_t slot) {
+        if constexpr (!DIRECT) {
+            char* at = lds + slot * kStage;
+#pragma unroll
+            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(at + (i * NW + wave) * 1024 + lane * 16) = held[i];
+#pragma unroll
+            for (int i = 0; i < CB; ++i)
+                *reinterpret_cast<u32x4*>(at + SA::kBytes + (i * NW + wave) * 1024 + lane * 16) = held[CA + i];
+        }
+    };
+
+    // ---- from LDS to the matrix cores
+    using Acc = typename Op::Acc;
+    Acc acc[FM][FN] = {};
+    // the wavefront's block j of B; gated: half are rows of the first matrix, half the same rows of the other
+    auto b_block = [&](int j) -> uint32_t {
+        if constexpr (GATED) return (j < FN / 2 ? 0 : BN / 32) + wn * (FN / 2) + j % (FN / 2);
+        else return wn * FN + j;
+    };
+    uint32_t base_a[A_OUTER ? FM : 2], base_b[B_OUTER ? FN : 2];
+    if constexpr (A_OUTER) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) base_a[i] = SA::block_base(lane, wm * FM + i);
+    } else {
+        for (int kk = 0; kk < 2; ++kk) base_a[kk] = wm * FM * 16 * kRowBytes + SA::lane_base(lane, kk);
+    }
+    if constexpr (B_OUTER) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) base_b[j] = SA::kBytes + SB::block_base(lane, b_block(j));
+    } else {
+        for (int kk = 0; kk < 2; ++kk) base_b[kk] = SA::kBytes + SB::lane_base(lane, kk);
+    }
+    auto multiply = [&](uint32_t slot) {
+        const char* at = lds + slot * kStage;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 a[FM], b[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if constexpr (B_OUTER) b[j] = SB::outer_frag(at, base_b[j], kk);
+                else b[j] = *reinterpret_cast<const u32x4*>(at + base_b[kk] + b_block(j) * 16 * kRowBytes);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                if constexpr (A_OUTER) a[i] = SA::outer_frag(at, base_a[i], kk);
+                else a[i] = *reinterpret_cast<const u32x4*>(at + base_a[kk] + i * 16 * kRowBytes);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) Op::mac(acc[i][j], b[j], a[i]);
+        }
+    };
+
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s)
+            if (first + s < last) fetch(first + s, s);
+        uint32_t slot = 0;
+        for (uint32_t s = first; s < last; ++s) {
+            // a step's copies are awaited before the copies of the steps after it
+            const uint32_t behind = last - 1 - s;
+            if (NS >= 4 && behind >= 2) wait_and_meet<2 * (CA + CB)>();
+            else if (NS >= 3 && behind >= 1) wait_and_meet<CA + CB>();
+            else wait_and_meet<0>();
+            // the slot of the step before this one is free: everyone has passed its multiplication
+            if (s + NS - 1 < last) fetch(s + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+            multiply(slot);
+            slot = slot == NS - 1 ? 0 : slot + 1;
+        }
+    } else {
+        static_assert(DIRECT || NS == 2, "the way through registers has two halves");
+        hold(first);
+        put_held(0);
+        for (uint32_t s = first; s < last; ++s) {
+            const uint32_t slot = (s - first) & 1;
+            wait_and_meet<0>();
+            if (s + 1 < last) hold(s + 1);
+            multiply(slot);
+            if (s + 1 < last) put_held(slot ^ 1);
+        }
+    }
+
+    if (p.splits > 1) {
+        Acc* out = reinterpret_cast<Acc*>(p.partial) +
+                   (static_cast<size_t>(split) * tiles + tile) * (FM * FN * NW * 64) + tid;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) out[(i * FN + j) * NW * 64] = acc[i][j];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int j = 0; j < (GATED ? FN / 2 : FN); ++j) {
+            const uint32_t n = n0 + b_block(j) * 16 + (lane >> 4) * 4;
+            if (n >= p.N) continue;
+            if constexpr (GATED) done(m, n, p.N, acc[i][j], acc[i][j + FN / 2]);
+            else done(m, n, p.N, acc[i][j]);
+        }
+    }
+}
+
+// The parts of a product whose sums were split over k, added in order of k.  One workgroup a tile and
+// block of 16 rows, the lanes as in product_tiles.
+template <class Op, int BM, int BN, int WM, int WN, bool GATED, class Done>
+__global__ __launch_bounds__(WM* WN * 64) void product_join(Product p, Done done) {
+    constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int BNB = GATED ? BN / 2 : BN;
+    using Acc = typename Op::Acc;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave / WN, wn = wave % WN;
+    const uint32_t tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BNB - 1) / BNB, tiles = tiles_m * tiles_n;
+    const uint32_t tile = blockIdx.x / FM, i = blockIdx.x % FM;
+    uint32_t tm, tn;
+    tile_of(tile, tiles_m, tiles_n, tm, tn);
+    const uint32_t m = tm * BM + (wm * FM + i) * 16 + (lane & 15);
+    if (m >= p.M) return;
+    const Acc* in = reinterpret_cast<const Acc*>(p.partial) + static_cast<size_t>(tile) * (FM * FN * NW * 64) + tid;
+    const size_t step = static_cast<size_t>(tiles) * (FM * FN * NW * 64);
+    Acc sum[FN] = {};
+    for (uint32_t s = 0; s < p.splits; ++s)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sum[j] += in[s * step + (i * FN + j) * NW * 64];
+#pragma unroll
+    for (int j = 0; j < (GATED ? FN / 2 : FN); ++j) {
+        const uint32_t n = tn * BNB + (GATED ? wn * (FN / 2) + j : wn * FN + j) * 16 + (lane >> 4) * 4;
+        if (n >= p.N) continue;
+        if constexpr (GATED) done(m, n, p.N, sum[j], sum[j + FN / 2]);
+        else done(m, n, p.N, sum[j]);
+    }
+}
+
 // Few rows of A (at most 16 * MF): B is read once, straight into registers, 16 of its rows a workgroup,
 // and the wavefronts of a workgroup share out k.  Their sums meet in LDS.  Bound by the bytes of B.
 template <class Op, int MF, int NW, bool GATED, bool ALIGNED, class Done>
@@ -242,17 +463,18 @@ __global__ __launch_bounds__(NW * 64) void product_rows(Product p, Done done) {
         ra[i] = p.a + m * p.a_pitch;
     }
     Acc acc[NB][MF] = {};
+    const uint32_t k_bytes = p.k * Op::kElem;
     const uint32_t kl = (lane >> 4) * 16;
     constexpr int U = MF > 1 ? 2 : 4;  // steps of k in flight; 128 bytes or more of a row at a time
-    for (uint32_t k0 = wave * 64 * U; k0 < p.k_bytes; k0 += NW * 64 * U) {
+    for (uint32_t k0 = wave * 64 * U; k0 < k_bytes; k0 += NW * 64 * U) {
         u32x4 b[U][NB], a[U][MF];
 #pragma unroll
         for (int s = 0; s < U; ++s) {
             const uint32_t k = k0 + s * 64 + kl;
 #pragma unroll
-            for (int q = 0; q < NB; ++q) b[s][q] = load_chunk<Op, ALIGNED>(rb[q], k, p.k_bytes);
+            for (int q = 0; q < NB; ++q) b[s][q] = load_chunk<Op, ALIGNED>(rb[q], k, k_bytes);
 #pragma unroll
-            for (int i = 0; i < MF; ++i) a[s][i] = load_chunk<Op, ALIGNED>(ra[i], k, p.k_bytes);
+            for (int i = 0; i < MF; ++i) a[s][i] = load_chunk<Op, ALIGNED>(ra[i], k, k_bytes);
         }
 #pragma unroll
         for (int s = 0; s < U; ++s)
@@ -303,61 +525,82 @@ __device__ __forceinline__ void store4(void* row, uint32_t n, uint32_t N, f32x4 
     }
 }
 
-// Copies rows of `bytes` bytes into rows of `pitch` bytes (a multiple of 16) with zeros behind: operands
-// whose rows are not whole 16-byte chunks, or that do not start on one.
-template <typename T>
-__global__ __launch_bounds__(256) void pad_rows(const T* src, T* dst, uint32_t rows, uint32_t width,
-                                                uint32_t pitch) {
-    for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (uint32_t c = threadIdx.x; c < pitch; c += 256)
-            dst[static_cast<size_t>(r) * pitch + c] = c < width ? src[static_cast<size_t>(r) * width + c] : T(0);
-}
-
 inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
-
-template <typename T>
-inline void launch_pad_rows(const void* src, void* dst, uint32_t rows, size_t bytes, hipStream_t stream) {
-    pad_rows<T><<<rows < 8192 ? rows : 8192, 256, 0, stream>>>(
-        static_cast<const T*>(src), static_cast<T*>(dst), rows, static_cast<uint32_t>(bytes / sizeof(T)),
-        static_cast<uint32_t>(up16(bytes) / sizeof(T)));
-}
-
-// The tile product's grid.
-template <int BM, int BN>
-inline uint32_t tile_count(uint32_t M, uint32_t N) {
-    return ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-}
-
-inline bool aligned16(const Product& p, bool gated) {
-    uintptr_t bits = reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b[0]) | p.a_pitch | p.b_pitch |
-                     p.k_bytes;
-    if (gated) bits |= reinterpret_cast<uintptr_t>(p.b[1]);
-    return bits % 16 == 0;
-}
 
 constexpr uint32_t kFewRows = 64;  // most rows of A that product_rows takes
 
-template <class Op, bool GATED, class Done>
-hipError_t launch_product(const Product& p, const Done& done, hipStream_t stream) {
-    const bool al = aligned16(p, GATED);
-    const uint32_t groups = (p.N + 15) / 16;
-    if (p.M <= kFewRows) {
-        if (p.M <= 16) {
-            if (al) product_rows<Op, 1, 8, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
-            else product_rows<Op, 1, 8, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
-        } else {
-            if (al) product_rows<Op, 4, 8, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
-            else product_rows<Op, 4, 8, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
-        }
-        return hipGetLastError();
+// How a product runs: the tile, and over how many workgroups its sums are split.
+struct Plan {
+    bool large;  // 256 x 256 tiles, else 128 x 128
+    uint32_t tiles, splits;
+    size_t partial_bytes;
+};
+
+// Large tiles where at least 3 of 4 compute units get one.  Otherwise small ones, two of which a compute
+// unit holds at a time; where they do not fill the chip, the sums are split until they do, as long as
+// every part keeps 8 steps of k.
+template <class Op, bool GATED>
+inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct) {
+    Plan plan{};
+    auto tiles = [&](uint32_t bm, uint32_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    const uint32_t big = tiles(256, GATED ? 128 : 256);
+    plan.large = Op::kElem != 4 && direct && big >= 192;
+    plan.tiles = plan.large ? big : tiles(128, GATED ? 64 : 128);
+    plan.splits = 1;
+    if (!plan.large) {
+        const uint32_t steps = (k * Op::kElem + kRowBytes - 1) / kRowBytes;
+        const uint32_t room = 512 / plan.tiles, depth = steps / 8;
+        plan.splits = room < depth ? room : depth;
+        if (plan.splits < 1) plan.splits = 1;
     }
-    if (!al) return hipErrorInvalidValue;  // the caller lays such operands out first
-    const uint32_t big = tile_count<256, GATED ? 128 : 256>(p.M, p.N);
-    if (big >= 192)
-        product_tiles<Op, 256, 256, 2, 4, GATED, Done><<<big, 512, 0, stream>>>(p, done);
-    else
-        product_tiles<Op, 128, 128, 2, 2, GATED, Done>
-            <<<tile_count<128, GATED ? 64 : 128>(p.M, p.N), 256, 0, stream>>>(p, done);
+    if (plan.splits > 1) plan.partial_bytes = size_t(plan.splits) * plan.tiles * 128 * 128 * 4;
+    return plan;
+}
+
+// Whether an operand can go to LDS directly.
+inline bool chunks16(const void* p, uint64_t pitch, uint64_t row_bytes) {
+    return ((reinterpret_cast<uintptr_t>(p) | pitch | row_bytes) & 15) == 0;
+}
+
+template <class Op, int BM, int BN, int WM, int WN, int NS, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
+          class Done>
+inline hipError_t launch_tiles(const Product& p, const Plan& plan, const Done& done, hipStream_t stream) {
+    product_tiles<Op, BM, BN, WM, WN, NS, GATED, A_OUTER, B_OUTER, DIRECT, Done>
+        <<<plan.tiles * p.splits, WM * WN * 64, 0, stream>>>(p, done);
+    const hipError_t e = hipGetLastError();
+    if constexpr (BM != 128) return e;  // large tiles are never split
+    if (e != hipSuccess || p.splits == 1) return e;
+    if constexpr (BM == 128)
+        product_join<Op, BM, BN, WM, WN, GATED, Done>
+            <<<plan.tiles * (BM / WM / 16), WM * WN * 64, 0, stream>>>(p, done);
+    return hipGetLastError();
+}
+
+template <class Op, bool GATED, bool A_OUTER, bool B_OUTER, class Done>
+hipError_t launch_product(Product p, bool direct, void* workspace, const Done& done, hipStream_t stream) {
+    const Plan plan = plan_product<Op, GATED>(p.M, p.N, p.k, direct);
+    p.splits = plan.splits;
+    p.partial = static_cast<float*>(workspace);
+    if constexpr (Op::kElem != 4)
+        if (plan.large)
+            return launch_tiles<Op, 256, 256, 2, 4, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+    if (direct) return launch_tiles<Op, 128, 128, 2, 2, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+    return launch_tiles<Op, 128, 128, 2, 2, 2, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+}
+
+template <class Op, bool GATED, class Done>
+hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t stream) {
+    const uint64_t bytes = uint64_t(p.k) * Op::kElem;
+    const bool al = chunks16(p.a, p.a_pitch, bytes) && chunks16(p.b[0], p.b_pitch, bytes) &&
+                    (!GATED || chunks16(p.b[1], p.b_pitch, bytes));
+    const uint32_t groups = (p.N + 15) / 16;
+    if (p.M <= 16) {
+        if (al) product_rows<Op, 1, 8, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
+        else product_rows<Op, 1, 8, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
+    } else {
+        if (al) product_rows<Op, 4, 8, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
+        else product_rows<Op, 4, 8, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
+    }
     return hipGetLastError();
 }
 

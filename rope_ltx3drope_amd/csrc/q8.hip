@@ -57,8 +57,8 @@ __global__ __launch_bounds__(256) void quantize_rows(const void* x, int8_t* q, f
     }
 }
 
-template <bool F32>
 struct ScaledDone {
+    bool f32;
     void* y;
     const float *a_scale, *b_scale, *bias;
     __device__ __forceinline__ void operator()(uint32_t m, uint32_t n, uint32_t N, i32x4 v) const {
@@ -71,19 +71,18 @@ struct ScaledDone {
             o[i] = static_cast<float>(v[i]) * sm * b_scale[c];
             if (bias) o[i] += bias[c];
         }
-        store4<F32>(static_cast<char*>(y) + static_cast<size_t>(m) * N * (F32 ? 4 : 2), n, N, o);
+        if (f32) store4<true>(static_cast<float*>(y) + static_cast<size_t>(m) * N, n, N, o);
+        else store4<false>(static_cast<uint16_t*>(y) + static_cast<size_t>(m) * N, n, N, o);
     }
 };
 
-bool unaligned(const Q8Problem& p) {
-    return (reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | p.dim) % 16 != 0;
-}
+bool direct(const Q8Problem& p) { return chunks16(p.a, p.dim, p.dim) && chunks16(p.b, p.dim, p.dim); }
 
 }  // namespace
 
 size_t q8_workspace(const Q8Problem& p) {
-    if (p.tokens <= kFewRows || !unaligned(p)) return 0;
-    return (size_t(p.tokens) + p.out) * up16(p.dim);
+    if (p.tokens <= kFewRows) return 0;
+    return plan_product<OpI8, false>(p.tokens, p.out, p.dim, direct(p)).partial_bytes;
 }
 
 hipError_t launch_q8(const Q8Problem& p, bool f32, hipStream_t stream) {
@@ -93,19 +92,10 @@ hipError_t launch_q8(const Q8Problem& p, bool f32, hipStream_t stream) {
     q.a_pitch = q.b_pitch = p.dim;
     q.M = p.tokens;
     q.N = p.out;
-    q.k_bytes = p.dim;
-    if (q8_workspace(p) != 0) {
-        char* a = static_cast<char*>(p.workspace);
-        char* b = a + size_t(p.tokens) * up16(p.dim);
-        launch_pad_rows<uint8_t>(p.a, a, p.tokens, p.dim, stream);
-        launch_pad_rows<uint8_t>(p.b, b, p.out, p.dim, stream);
-        q.a = a;
-        q.b[0] = b;
-        q.a_pitch = q.b_pitch = up16(p.dim);
-        q.k_bytes = static_cast<uint32_t>(up16(p.dim));
-    }
-    return f32 ? launch_product<OpI8, false>(q, ScaledDone<true>{p.y, p.a_scale, p.b_scale, p.bias}, stream)
-               : launch_product<OpI8, false>(q, ScaledDone<false>{p.y, p.a_scale, p.b_scale, p.bias}, stream);
+    q.k = p.dim;
+    const ScaledDone done{f32, p.y, p.a_scale, p.b_scale, p.bias};
+    if (p.tokens <= kFewRows) return launch_few_rows<OpI8, false>(q, done, stream);
+    return launch_product<OpI8, false, false, false>(q, direct(p), p.workspace, done, stream);
 }
 
 hipError_t launch_q8_quantize(const void* x, void* q, float* scale, uint32_t rows, uint32_t dim, bool f32,

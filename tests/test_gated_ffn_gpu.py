@@ -113,7 +113,8 @@ def test_hidden_widths(F, M, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,D,F", [(2048, 128, 3200), (2047, 72, 3201), (300, 2056, 700), (1025, 4096, 64)])
+@pytest.mark.parametrize("M,D,F", [(2048, 128, 3200), (2047, 72, 3201), (2300, 2304, 1152), (300, 2056, 700),
+                                   (1025, 4096, 64), (70, 8200, 20), (1700, 640, 65), (90, 1025, 1700)])
 def test_large_tiles(M, D, F, dtype):
     """Enough tiles for the large ones; long sums; odd edges of both."""
     run(M, D, F, dtype, "silu", 300 + M)
@@ -233,11 +234,11 @@ def test_gradients_against_differences():
 def test_other_stream_and_graph():
     t = inputs(130, 200, 264, torch.bfloat16, 8)
     dev = {k: v.to(DEV) for k, v in t.items()}
-    odd = {k: v.to(DEV) for k, v in inputs(70, 101, 90, torch.bfloat16, 8).items()}
+    odd = {k: v.to(DEV) for k, v in inputs(70, 2051, 90, torch.bfloat16, 8).items()}
 
     def step():
         outs = []
-        for v in (dev, odd):  # the second needs a workspace in the forward as well
+        for v in (dev, odd):  # the second's sums are split: a workspace in the forward as well
             h, g, u = rla.gated_ffn(v["x"], v["w_gate"], v["w_up"], "gelu", save=True)
             outs += [h, *rla.gated_ffn_backward(v["dh"], v["x"], v["w_gate"], v["w_up"], g, u, "gelu")]
         return outs

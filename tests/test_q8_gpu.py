@@ -154,8 +154,8 @@ def test_leading_dimensions_out_and_empty():
 
 
 def test_other_stream_and_graph():
-    a, sa, b, sb, bias = (v.to(DEV) for v in operands(70, 101, 50, 5))
-    x = randn(torch.Generator().manual_seed(1), 70, 101).to(DEV)
+    a, sa, b, sb, bias = (v.to(DEV) for v in operands(70, 4101, 50, 5))  # sums split: a workspace
+    x = randn(torch.Generator().manual_seed(1), 70, 4101).to(DEV)
 
     def step(stream=None):
         q, s = rla.q8_quantize(x, stream=stream)
@@ -172,7 +172,7 @@ def test_other_stream_and_graph():
     with torch.cuda.graph(graph):
         outs = step()
     for i in range(4):
-        x.copy_(randn(torch.Generator().manual_seed(10 + i), 70, 101))
+        x.copy_(randn(torch.Generator().manual_seed(10 + i), 70, 4101))
         eager = step()
         graph.replay()
         torch.cuda.synchronize()
