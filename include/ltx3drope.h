@@ -462,7 +462,7 @@ int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call)
  * E_UNSUPPORTED with the reason in *reason (which may be NULL), the first that
  * fails of: DTYPE; NONPOSITIVE_DIM (dim <= 0, tokens or hidden < 0); TOO_LARGE
  * (tokens, 2 * hidden or dim of 2^21 or more, or more than 2^23 output tiles of
- * 128 x 64: 2^36 outputs); NULLPTR; ALIGN (a pointer not
+ * 64 x 32: 2^34 outputs); NULLPTR; ALIGN (a pointer not
  * aligned to its element, the workspace not to 16 bytes); OVERLAP (an output or
  * the workspace over anything else); then NOT_DEVICE_PTR, TABLE_DEVICE (memory
  * of two devices) and EXTENT.  E_HIP: a launch failed.  Asynchronous on
@@ -530,8 +530,8 @@ int ltx3drope_q8_quantize(int dtype, int64_t rows, int64_t dim, const void* x, v
  * `workspace` as for ltx3drope_gated_ffn.  tokens = 0 or out = 0 is an empty call.  E_INVALID: a NULL
  * descriptor, reserved not 0, a workspace that is too small.  E_UNSUPPORTED:
  * DTYPE; NONPOSITIVE_DIM; TOO_LARGE (dim > 131071, whose sums could pass 32
- * bits, tokens or out of 2^26 or more, or more than 2^23 output tiles of 128 x
- * 64); NULLPTR; ALIGN; OVERLAP;
+ * bits, tokens or out of 2^26 or more, or more than 2^23 output tiles of 64 x
+ * 32); NULLPTR; ALIGN; OVERLAP;
  * NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.  E_HIP.  Asynchronous, allocates nothing.
  */
 typedef struct {

@@ -56,7 +56,7 @@ struct FfnBackwardProblem {
     int activation;
 };
 constexpr int64_t kFfnMaxSize = int64_t(1) << 21;  // a tile of 256 rows of 2 * hidden fp32 stays within 2^31 bytes
-constexpr int64_t kMaxTiles = int64_t(1) << 23;    // 128 x 64 output tiles of a launch of 256 threads each
+constexpr int64_t kMaxTiles = int64_t(1) << 23;    // 64 x 32 output tiles of a launch of 256 threads each
 size_t ffn_workspace(const FfnProblem& p, bool f32);
 size_t ffn_backward_workspace(const FfnBackwardProblem& p, bool f32);
 hipError_t launch_ffn(const FfnProblem& p, bool f32, hipStream_t stream);

@@ -102,8 +102,8 @@ size_t norm_workspace(const ltx3drope_norm_backward_t& c) {
                                    static_cast<uint32_t>(c.dim));
 }
 
-// A product's launch: 128 x 64 tiles (the smallest) of 256 threads stay below 2^31 threads.
-bool too_many_tiles(int64_t M, int64_t N) { return (M / 128 + 1) * (N / 64 + 1) > kMaxTiles; }
+// A product's launch: 64 x 32 tiles (the smallest) of 256 threads stay below 2^32 threads.
+bool too_many_tiles(int64_t M, int64_t N) { return (M / 64 + 1) * (N / 32 + 1) > kMaxTiles; }
 
 // The feed-forward block's scalars, both directions.
 template <class Call>

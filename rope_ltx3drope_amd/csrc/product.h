@@ -80,11 +80,27 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
     tn = (t % width) / rows;
 }
 
-__device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voffset, uint32_t soffset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voffset, soffset, 0, 0);
+// A raw buffer descriptor of `lines` lines of `bytes` bytes, `pitch` apart (the same in every lane): what
+// lies past its end reads as zero.
+__device__ __forceinline__ u32x4 buffer_of(const char* base, uint64_t pitch, uint32_t lines, uint32_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    auto uniform = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
+    return u32x4{uniform(static_cast<uint32_t>(at)), uniform(static_cast<uint32_t>(at >> 32)),
+                 uniform(lines == 0 ? 0u : static_cast<uint32_t>((lines - 1) * pitch + bytes)), 0x00020000u};
 }
 
-// All but this wavefront's N newest loads have landed, its LDS reads and writes are done, and so are
+// Sends 16 bytes a lane from the buffer to LDS, lane l's to lds + 16 * l.  The instruction is written out
+// because the compiler, which cannot tell which LDS bytes a builtin copy fills, waits for all copies
+// before every turning read of another slot (4096 x 2048 x 16384 with k outermost: 308 us with the
+// builtin).  It leaves no register behind but m0, which
+// nothing else in these kernels uses; its arrival is awaited by wait_and_meet.
+__device__ __forceinline__ void lds_copy16(u32x4 buffer, char* lds, uint32_t voffset, uint32_t soffset) {
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voffset),
+                 "s"(buffer), "s"(soffset));
+}
+
+// All but this wavefront's N newest copies have landed, its LDS reads and writes are done, and so are
 // every other wavefront's.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
@@ -128,7 +144,7 @@ struct Side {
 
     static __device__ __forceinline__ uint32_t swizzle(uint32_t r) { return (r >> 1) & 7; }
     static __device__ __forceinline__ uint32_t spread(uint32_t k) {
-        return Op::kElem == 4 ? (k >> 2) & 3 : (k & 3) | ((k >> 3) & 1) << 2;
+        return (Op::kElem == 4 ? (k >> 2) & 3 : (k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1);
     }
 
     // What 16-byte place `at` of the LDS image holds: row `line` (of the output's index or of k) of the
@@ -178,22 +194,27 @@ struct Side {
     }
 };
 
-// BM x BN tiles, WM x WN wavefronts, each with (BM / WM) x (BN / WN) of the tile in registers; NS steps'
-// worth of LDS, so that NS - 1 steps travel from memory while one is multiplied.
+// BM x BN tiles, WM x WN wavefronts, each with (BM / WM) x (BN / WN) of the tile in registers.
 // DIRECT: 16-byte aligned operands go from memory to LDS without passing through registers; otherwise
 // they pass through them (any alignment).  A_OUTER, B_OUTER: k outermost.
-template <class Op, int BM, int BN, int WM, int WN, int NS, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
+template <class Op, int BM, int BN, int WM, int WN, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
           class Done>
 __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done done) {
     constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
     constexpr int BNB = GATED ? BN / 2 : BN;  // rows of each B in a tile
     using SA = Side<Op, BM, A_OUTER>;
     using SB = Side<Op, BNB, B_OUTER>;
-    constexpr int kStage = (BM + BN) * kRowBytes, kStepK = SA::kStepK;
+    // LDS: rings of kSlotsA steps of A and 2 of B (160 KB for 256 x 256: all there is).  The copies have a
+    // step's time to land at the least; with the third slot A's have two, and half as many bytes again
+    // are on their way at any time, which is what the copies' rate goes by (4096 x 16384 x 2048 in bf16:
+    // see the launch rule for both).
+    constexpr bool kPipelined = DIRECT && BM == 256;
+    constexpr int kSlotsA = kPipelined ? 3 : 2, kStepK = SA::kStepK;
+    constexpr int kBytesB = BN * kRowBytes, kAtB = kSlotsA * SA::kBytes;
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies a wavefront makes of each operand
     static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN, "a tile's copies split evenly over the wavefronts");
     static_assert(!GATED || (CB % 2 == 0 && FN % 2 == 0 && !B_OUTER), "both halves of B in every wavefront");
-    __shared__ __align__(1024) char lds[NS * kStage];
+    __shared__ __align__(1024) char lds[kAtB + 2 * kBytesB];
 
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -215,16 +236,11 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
         SB::place(((GATED ? i % (CB / 2) : i) * NW + wave) * 64 + lane, line_b[i], byte_b[i]);
 
     // the descriptor of an operand for one step, and this lane's byte in it (or out of range: zeros)
-    auto resource = [](const char* base, uint64_t pitch, uint32_t lines, uint32_t bytes) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0,
-                                                 static_cast<int>(lines == 0 ? 0 : (lines - 1) * pitch + bytes),
-                                                 0x00020000);
-    };
     auto inner_rsrc = [&](const char* base, uint64_t pitch, uint32_t row0, uint32_t rows, uint32_t R) {
         const uint32_t n = rows - row0 < R ? rows - row0 : R;
-        return resource(base + row0 * pitch, pitch, n, p.k * Op::kElem);
+        return buffer_of(base + row0 * pitch, pitch, n, p.k * Op::kElem);
     };
-    __amdgpu_buffer_rsrc_t ra, rb0, rb1;
+    u32x4 ra, rb0, rb1;
     uint32_t va[CA], vb[CB];
     if constexpr (DIRECT) {
         if constexpr (!A_OUTER) ra = inner_rsrc(p.a, p.a_pitch, m0, p.M, BM);
@@ -252,27 +268,33 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
         rows = k0 < have ? (have - k0 < kStepK ? have - k0 : kStepK) : 0;
         return second ? p.b[1] : p.b[0];
     };
-    auto fetch = [&](uint32_t step, uint32_t slot) {
-        char* at = lds + slot * kStage;
+    // a step past this workgroup's last one brings zeros without touching memory
+    const uint32_t k_end = last * kRowBytes < p.k * Op::kElem ? last * kRowBytes : p.k * Op::kElem;
+    auto fetch_a = [&](uint32_t step, uint32_t slot) {
         const uint32_t k = step * kRowBytes;
         if constexpr (A_OUTER) {
-            const uint32_t k0 = step * kStepK, rows = p.k - k0 < kStepK ? p.k - k0 : kStepK;
-            ra = resource(p.a + k0 * p.a_pitch + m0 * Op::kElem, p.a_pitch, rows, (p.M - m0) * Op::kElem);
-        }
-        if constexpr (B_OUTER) {
-            uint32_t k0, rows;
-            const char* base = b_segment(step, k0, rows);
-            rb0 = resource(base + k0 * p.b_pitch + n0 * Op::kElem, p.b_pitch, rows, (p.N - n0) * Op::kElem);
+            const uint32_t k0 = step * kStepK;
+            const uint32_t rows = step >= last ? 0 : (p.k - k0 < kStepK ? p.k - k0 : kStepK);
+            ra = buffer_of(p.a + k0 * p.a_pitch + m0 * Op::kElem, p.a_pitch, rows, (p.M - m0) * Op::kElem);
         }
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
-            const bool past = !A_OUTER && k + byte_a[i] >= p.k * Op::kElem;  // only in the last step
-            lds_copy16(ra, at + (i * NW + wave) * 1024, past ? kOutOfRange : va[i], A_OUTER ? 0 : k);
+            const bool past = !A_OUTER && k + byte_a[i] >= k_end;
+            lds_copy16(ra, lds + slot * SA::kBytes + (i * NW + wave) * 1024, past ? kOutOfRange : va[i], A_OUTER ? 0 : k);
+        }
+    };
+    auto fetch_b = [&](uint32_t step, uint32_t slot) {
+        const uint32_t k = step * kRowBytes;
+        if constexpr (B_OUTER) {
+            uint32_t k0, rows;
+            const char* base = b_segment(step, k0, rows);
+            rb0 = buffer_of(base + k0 * p.b_pitch + n0 * Op::kElem, p.b_pitch, step >= last ? 0 : rows,
+                            (p.N - n0) * Op::kElem);
         }
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
-            const bool past = !B_OUTER && k + byte_b[i] >= p.k * Op::kElem;
-            lds_copy16(GATED && i >= CB / 2 ? rb1 : rb0, at + SA::kBytes + (i * NW + wave) * 1024,
+            const bool past = !B_OUTER && k + byte_b[i] >= k_end;
+            lds_copy16(GATED && i >= CB / 2 ? rb1 : rb0, lds + kAtB + slot * kBytesB + (i * NW + wave) * 1024,
                        past ? kOutOfRange : vb[i], B_OUTER ? 0 : k);
         }
     };
@@ -310,12 +332,12 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
     };
     auto put_held = [&](uint32_t slot) {
         if constexpr (!DIRECT) {
-            char* at = lds + slot * kStage;
+            char* at = lds + wave * 1024 + lane * 16;
 #pragma unroll
-            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(at + (i * NW + wave) * 1024 + lane * 16) = held[i];
+            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(at + slot * SA::kBytes + i * NW * 1024) = held[i];
 #pragma unroll
             for (int i = 0; i < CB; ++i)
-                *reinterpret_cast<u32x4*>(at + SA::kBytes + (i * NW + wave) * 1024 + lane * 16) = held[CA + i];
+                *reinterpret_cast<u32x4*>(at + kAtB + slot * kBytesB + i * NW * 1024) = held[CA + i];
         }
     };
 
@@ -336,57 +358,101 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
     }
     if constexpr (B_OUTER) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) base_b[j] = SA::kBytes + SB::block_base(lane, b_block(j));
+        for (int j = 0; j < FN; ++j) base_b[j] = kAtB + SB::block_base(lane, b_block(j));
     } else {
-        for (int kk = 0; kk < 2; ++kk) base_b[kk] = SA::kBytes + SB::lane_base(lane, kk);
+        for (int kk = 0; kk < 2; ++kk) base_b[kk] = kAtB + SB::lane_base(lane, kk);
     }
-    auto multiply = [&](uint32_t slot) {
-        const char* at = lds + slot * kStage;
+    u32x4 fa[2][FM], fb[2][FN];
+    auto read = [&](uint32_t slot_a, uint32_t slot_b, int kk) {
+        const char *at_a = lds + slot_a * SA::kBytes, *at_b = lds + slot_b * kBytesB;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 a[FM], b[FN];
+        for (int j = 0; j < FN; ++j) {
+            if constexpr (B_OUTER) fb[kk][j] = SB::outer_frag(at_b, base_b[j], kk);
+            else fb[kk][j] = *reinterpret_cast<const u32x4*>(at_b + base_b[kk] + b_block(j) * 16 * kRowBytes);
+        }
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (B_OUTER) b[j] = SB::outer_frag(at, base_b[j], kk);
-                else b[j] = *reinterpret_cast<const u32x4*>(at + base_b[kk] + b_block(j) * 16 * kRowBytes);
-            }
+        for (int i = 0; i < FM; ++i) {
+            if constexpr (A_OUTER) fa[kk][i] = SA::outer_frag(at_a, base_a[i], kk);
+            else fa[kk][i] = *reinterpret_cast<const u32x4*>(at_a + base_a[kk] + i * 16 * kRowBytes);
+        }
+    };
+    auto multiply = [&](int kk) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                if constexpr (A_OUTER) a[i] = SA::outer_frag(at, base_a[i], kk);
-                else a[i] = *reinterpret_cast<const u32x4*>(at + base_a[kk] + i * 16 * kRowBytes);
-            }
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int j = 0; j < FN; ++j) Op::mac(acc[i][j], fb[kk][j], fa[kk][i]);
+    };
+    // a few LDS reads, a few products, and so on, instead of all of one and then all of the other
+    auto interleave = [&]() {
+        constexpr int reads = (FM * (A_OUTER ? (Op::kElem == 4 ? 4 : 2) : 1) + FN * (B_OUTER ? (Op::kElem == 4 ? 4 : 2) : 1));
+        constexpr int macs = FM * FN * (Op::kElem == 4 ? 4 : 1);
+        constexpr int per = macs / reads > 0 ? macs / reads : 1;
 #pragma unroll
-                for (int j = 0; j < FN; ++j) Op::mac(acc[i][j], b[j], a[i]);
+        for (int r = 0; r < reads; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, per, 0);
         }
     };
 
-    if constexpr (DIRECT) {
-#pragma unroll
-        for (int s = 0; s < NS - 1; ++s)
-            if (first + s < last) fetch(first + s, s);
-        uint32_t slot = 0;
+    if constexpr (kPipelined) {
+        // Half a step is multiplied while the next half step's operands are read from LDS.  The step
+        // after this one has to be in LDS, and this one's slots are free, once every wavefront has read
+        // its second half: they meet between the two multiplications, with operands for the second in
+        // registers, and the copies for the freed slots set out.
+        fetch_b(first, 0);
+        fetch_a(first, 0);
+        fetch_a(first + 1, 1);
+        fetch_b(first + 1, 1);
+        fetch_a(first + 2, 2);
+        wait_and_meet<2 * CA + CB>();
+        read(0, 0, 0);
+        uint32_t sa = 0, sb = 0;  // the step's slots
+        for (uint32_t s = first; s + 1 < last; ++s) {
+            const uint32_t next = sa == 2 ? 0 : sa + 1;
+            read(sa, sb, 1);
+            multiply(0);
+            interleave();
+            wait_and_meet<CA>();  // all but A's copies for the step after the next
+            fetch_b(s + 2, sb);
+            fetch_a(s + 3, sa);
+            read(next, sb ^ 1, 0);
+            multiply(1);
+            interleave();
+            sa = next;
+            sb ^= 1;
+        }
+        read(sa, sb, 1);
+        multiply(0);
+        multiply(1);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives its workgroup
+    } else if constexpr (DIRECT) {
+        // two workgroups share a compute unit and fill each other's waits
+        fetch_a(first, 0);
+        fetch_b(first, 0);
         for (uint32_t s = first; s < last; ++s) {
-            // a step's copies are awaited before the copies of the steps after it
-            const uint32_t behind = last - 1 - s;
-            if (NS >= 4 && behind >= 2) wait_and_meet<2 * (CA + CB)>();
-            else if (NS >= 3 && behind >= 1) wait_and_meet<CA + CB>();
-            else wait_and_meet<0>();
-            // the slot of the step before this one is free: everyone has passed its multiplication
-            if (s + NS - 1 < last) fetch(s + NS - 1, slot == 0 ? NS - 1 : slot - 1);
-            multiply(slot);
-            slot = slot == NS - 1 ? 0 : slot + 1;
+            const uint32_t slot = (s - first) & 1;
+            wait_and_meet<0>();
+            if (s + 1 < last) {
+                fetch_a(s + 1, slot ^ 1);
+                fetch_b(s + 1, slot ^ 1);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                read(slot, slot, kk);
+                multiply(kk);
+            }
         }
     } else {
-        static_assert(DIRECT || NS == 2, "the way through registers has two halves");
         hold(first);
         put_held(0);
         for (uint32_t s = first; s < last; ++s) {
             const uint32_t slot = (s - first) & 1;
             wait_and_meet<0>();
             if (s + 1 < last) hold(s + 1);
-            multiply(slot);
+            read(slot, slot, 0);
+            read(slot, slot, 1);
+            multiply(0);
+            multiply(1);
             if (s + 1 < last) put_held(slot ^ 1);
         }
     }
@@ -529,32 +595,60 @@ inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 constexpr uint32_t kFewRows = 64;  // most rows of A that product_rows takes
 
-// How a product runs: the tile, and over how many workgroups its sums are split.
+// How a product runs: square tiles of 256, 128 or 64 (gated: half as wide in either B), and over how many
+// workgroups its sums are split.
 struct Plan {
-    bool large;  // 256 x 256 tiles, else 128 x 128
-    uint32_t tiles, splits;
+    uint32_t tile, tiles, splits;
     size_t partial_bytes;
 };
 
-// Large tiles where at least 3 of 4 compute units get one.  Otherwise small ones, two of which a compute
-// unit holds at a time; where they do not fill the chip, the sums are split until they do, as long as
-// every part keeps 8 steps of k.
+// Microseconds that a tile's workgroup takes: a step of k alone on its compute unit (`alone`), its share
+// of a step when the unit is full (`full`), and a tile's start and end (`ends`).
+struct TileCost {
+    float alone, full, ends;
+};
+
+// Fitted to products timed on the card, k of 4096 unless stated: bf16 2048 x 2048 47 us with tiles of
+// 128, 49 with 64; 4096 x 2048 65, 94 (88 with 256); 4096 x 16384, k 2048: 239 with 256, 297 with 128;
+// 512 x 4352, k 1536: 16 with 64, 21 with 128; 256 x 1024: 32 with 64, 15 split in four.  fp32 4096 x
+// 4096, k 2048: 500 with 128, 507 with 64; 301 x 1152, k 5632: 126 with 64, 45 split in eight.
+template <class Op>
+constexpr TileCost tile_cost(uint32_t tile) {
+    if (Op::kElem == 4) return tile == 128 ? TileCost{2.05f, 1.95f, 3.5f} : TileCost{0.69f, 0.49f, 1.5f};
+    return tile == 256   ? TileCost{1.6f, 1.6f, 7.0f}
+           : tile == 128 ? TileCost{0.65f, 0.465f, 3.5f}
+                         : TileCost{0.42f, 0.17f, 1.0f};
+}
+
+// The tile and split with the least time by these costs.  Splitting adds the sums' way through memory
+// and a launch; every part keeps 4 steps of k.
 template <class Op, bool GATED>
 inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct) {
-    Plan plan{};
-    auto tiles = [&](uint32_t bm, uint32_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    const uint32_t big = tiles(256, GATED ? 128 : 256);
-    plan.large = Op::kElem != 4 && direct && big >= 192;
-    plan.tiles = plan.large ? big : tiles(128, GATED ? 64 : 128);
-    plan.splits = 1;
-    if (!plan.large) {
-        const uint32_t steps = (k * Op::kElem + kRowBytes - 1) / kRowBytes;
-        const uint32_t room = 512 / plan.tiles, depth = steps / 8;
-        plan.splits = room < depth ? room : depth;
-        if (plan.splits < 1) plan.splits = 1;
+    const float units = 256.f;
+    const uint32_t steps = (k * Op::kElem + kRowBytes - 1) / kRowBytes;
+    Plan best{};
+    float least = 0.f;
+    for (uint32_t tile : {256u, 128u, 64u}) {
+        if (tile == 256 && (Op::kElem == 4 || !direct)) continue;
+        const uint32_t bn = GATED ? tile / 2 : tile;
+        const uint32_t tiles = ((M + tile - 1) / tile) * ((N + bn - 1) / bn);
+        const TileCost c = tile_cost<Op>(tile);
+        for (uint32_t splits = 1; splits <= 16; splits += splits < 4 ? 1 : 2) {
+            if (splits > 1 && (steps / splits < 4 || tiles >= 512)) break;
+            const float depth = static_cast<float>((steps + splits - 1) / splits);
+            const float per_unit = static_cast<float>(tiles) * splits / units;
+            const float rounds = tile == 256 ? static_cast<float>((tiles * splits + 255) / 256) : per_unit;
+            const float one = depth * c.alone + c.ends, many = rounds * (depth * c.full + c.ends);
+            float us = one > many ? one : many;
+            const size_t bytes = splits > 1 ? size_t(splits) * tiles * tile * tile * 4 : 0;
+            if (splits > 1) us += 4.f + static_cast<float>(bytes) * 2 / 4e6f;
+            if (best.tiles == 0 || us < least) {
+                best = Plan{tile, tiles, splits, bytes};
+                least = us;
+            }
+        }
     }
-    if (plan.splits > 1) plan.partial_bytes = size_t(plan.splits) * plan.tiles * 128 * 128 * 4;
-    return plan;
+    return best;
 }
 
 // Whether an operand can go to LDS directly.
@@ -562,17 +656,15 @@ inline bool chunks16(const void* p, uint64_t pitch, uint64_t row_bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | pitch | row_bytes) & 15) == 0;
 }
 
-template <class Op, int BM, int BN, int WM, int WN, int NS, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
-          class Done>
+template <class Op, int TILE, int WM, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT, class Done>
 inline hipError_t launch_tiles(const Product& p, const Plan& plan, const Done& done, hipStream_t stream) {
-    product_tiles<Op, BM, BN, WM, WN, NS, GATED, A_OUTER, B_OUTER, DIRECT, Done>
-        <<<plan.tiles * p.splits, WM * WN * 64, 0, stream>>>(p, done);
+    constexpr int threads = WM * 2 * 64;
+    product_tiles<Op, TILE, TILE, WM, 2, GATED, A_OUTER, B_OUTER, DIRECT, Done>
+        <<<plan.tiles * p.splits, threads, 0, stream>>>(p, done);
     const hipError_t e = hipGetLastError();
-    if constexpr (BM != 128) return e;  // large tiles are never split
     if (e != hipSuccess || p.splits == 1) return e;
-    if constexpr (BM == 128)
-        product_join<Op, BM, BN, WM, WN, GATED, Done>
-            <<<plan.tiles * (BM / WM / 16), WM * WN * 64, 0, stream>>>(p, done);
+    product_join<Op, TILE, TILE, WM, 2, GATED, Done>
+        <<<plan.tiles * (TILE / WM / 16), threads, 0, stream>>>(p, done);
     return hipGetLastError();
 }
 
@@ -582,10 +674,12 @@ hipError_t launch_product(Product p, bool direct, void* workspace, const Done& d
     p.splits = plan.splits;
     p.partial = static_cast<float*>(workspace);
     if constexpr (Op::kElem != 4)
-        if (plan.large)
-            return launch_tiles<Op, 256, 256, 2, 4, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
-    if (direct) return launch_tiles<Op, 128, 128, 2, 2, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
-    return launch_tiles<Op, 128, 128, 2, 2, 2, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+        if (plan.tile == 256) return launch_tiles<Op, 256, 4, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+    if (plan.tile == 128)
+        return direct ? launch_tiles<Op, 128, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+                      : launch_tiles<Op, 128, 2, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+    return direct ? launch_tiles<Op, 64, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+                  : launch_tiles<Op, 64, 2, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
 }
 
 template <class Op, bool GATED, class Done>
