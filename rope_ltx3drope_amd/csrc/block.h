@@ -18,6 +18,7 @@ struct NormForward {
     uint32_t batch, rows, dim;
     float eps, weight_offset, residual_scale;
     bool has_y, post_norm, next_norm, param_f32;
+    bool chunks;  // the vectors, and each sample's part of them, start on 16 bytes
 };
 
 struct NormBackward {
@@ -26,7 +27,7 @@ struct NormBackward {
     float* partial;  // [3][batch][parts][dim], NULL when no vector's gradient is asked for
     uint32_t batch, rows, dim;
     float eps, weight_offset, residual_scale;
-    bool has_y, post_norm, next_norm, param_f32;
+    bool has_y, post_norm, next_norm, param_f32, chunks;
 };
 
 constexpr int64_t kNormMaxDim = 16384;    // 1024 threads of 16 elements hold one row

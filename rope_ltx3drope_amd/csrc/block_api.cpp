@@ -1,6 +1,7 @@
 // C ABI of the transformer-block operators: argument checks and dispatch.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "block.h"
 #include "internal.h"
@@ -193,10 +194,10 @@ Q8Problem q8_problem(const ltx3drope_q8_matmul_t& c) {
     return p;
 }
 
-bool aligned16(const Spans& t) {
+bool aligned16(const Spans& t, std::initializer_list<Role> roles) {
     for (int i = 0; i < t.n; ++i)
-        if ((t.s[i].role == Role::RowIn || t.s[i].role == Role::RowOut) && reinterpret_cast<uintptr_t>(t.s[i].p) % 16)
-            return false;
+        for (Role r : roles)
+            if (t.s[i].role == r && reinterpret_cast<uintptr_t>(t.s[i].p) % 16) return false;
     return true;
 }
 
@@ -258,7 +259,8 @@ int ltx3drope_norm(const ltx3drope_norm_t* call, void* stream, int* reason) {
     p.next_norm = c.next_norm != 0;
     p.param_f32 = c.param_dtype == LTX3DROPE_DTYPE_F32;
     const bool f32 = c.dtype == LTX3DROPE_DTYPE_F32;
-    const bool vectors = aligned16(t) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
+    const bool vectors = aligned16(t, {Role::RowIn, Role::RowOut}) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
+    p.chunks = aligned16(t, {Role::Param}) && vec % 16 == 0;
     DeviceGuard guard(device);
     if (launch_norm_forward(p, f32, vectors, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;
     count_launch();
@@ -346,7 +348,8 @@ int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream,
     p.next_norm = c.next_norm != 0;
     p.param_f32 = c.param_dtype == LTX3DROPE_DTYPE_F32;
     const bool f32 = c.dtype == LTX3DROPE_DTYPE_F32;
-    const bool vectors = aligned16(t) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
+    const bool vectors = aligned16(t, {Role::RowIn, Role::RowOut}) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
+    p.chunks = aligned16(t, {Role::Param}) && vec % 16 == 0;
     DeviceGuard guard(device);
     if (launch_norm_backward(p, f32, vectors, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;
     count_launch();

@@ -156,7 +156,7 @@ bool forward_direct(const FfnProblem& p) {
 template <bool F32>
 size_t forward_workspace(const FfnProblem& p) {
     if (p.tokens <= kFewRows) return 0;
-    return plan_product<OpOf<F32>, true>(p.tokens, p.hidden, p.dim, forward_direct<F32>(p)).partial_bytes;
+    return plan_product<OpOf<F32>, true, false>(p.tokens, p.hidden, p.dim, forward_direct<F32>(p)).partial_bytes;
 }
 
 template <bool F32>
@@ -190,8 +190,8 @@ BackwardLayout backward_layout(const FfnBackwardProblem& p) {
     l.dx_direct = chunks16(p.w_gate, row, row) && chunks16(p.w_up, row, row);
     l.dw_direct = chunks16(p.x, row, row);
     l.slopes = size_t(p.tokens) * 2 * l.Fp * es;  // whole 128-byte steps
-    const size_t a = p.dx ? plan_product<OpOf<F32>, false>(p.tokens, p.dim, 2 * l.Fp, l.dx_direct).partial_bytes : 0;
-    const size_t b = p.dw_gate ? plan_product<OpOf<F32>, false>(2 * l.Fp, p.dim, p.tokens, l.dw_direct).partial_bytes : 0;
+    const size_t a = p.dx ? plan_product<OpOf<F32>, false, true>(p.tokens, p.dim, 2 * l.Fp, l.dx_direct).partial_bytes : 0;
+    const size_t b = p.dw_gate ? plan_product<OpOf<F32>, false, true>(2 * l.Fp, p.dim, p.tokens, l.dw_direct).partial_bytes : 0;
     l.bytes = l.slopes + (a > b ? a : b);
     return l;
 }

@@ -119,6 +119,54 @@ __device__ __forceinline__ float load_param(const void* p, bool f32, size_t i) {
     return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
+// A thread's E parameters of one vector, or `otherwise` where there is no vector or no column.  VEC rows
+// with `chunks` (the vectors start on 16 bytes and so does every sample's part) read them 16 bytes at a time.
+template <bool F32, int E, bool VEC>
+__device__ __forceinline__ void load_params(float (&f)[E], const void* p, size_t first, bool f32, bool chunks,
+                                            float otherwise, uint32_t t, uint32_t T, uint32_t D) {
+    constexpr int V = RowPart<F32, E, VEC>::V;
+#pragma unroll
+    for (int k = 0; k < E; ++k) f[k] = otherwise;
+    if (p == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < E / V; ++i) {
+        const uint32_t c = (i * T + t) * V;
+        if (c >= D) continue;
+        if (VEC && chunks) {
+            if (f32) {
+#pragma unroll
+                for (int h = 0; h < V; h += 4) {
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + first + c + h);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) f[(i * V + h + k) % E] = __uint_as_float(v[k]);
+                }
+            } else if constexpr (V == 8) {
+                const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + first + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[i * V + 2 * k] = __uint_as_float(v[k] << 16);
+                    f[i * V + 2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[i * V + k] = load_param(p, f32, first + c + k);
+        }
+    }
+}
+
+// The factor that takes the place of (w + offset) * g, or (w + offset) * (1 + g), for one sample.
+template <bool F32, int E, bool VEC, class Call>
+__device__ __forceinline__ void load_factor(float (&f)[E], const Call& p, const void* w, const void* g, float one,
+                                            uint32_t b, uint32_t t, uint32_t T) {
+    float other[E];
+    load_params<F32, E, VEC>(f, w, 0, p.param_f32, p.chunks, 1.f, t, T, p.dim);
+    load_params<F32, E, VEC>(other, g, static_cast<size_t>(b) * p.dim, p.param_f32, p.chunks, 1.f - one, t, T, p.dim);
+    const float offset = w ? p.weight_offset : 0.f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) f[k] = (f[k] + offset) * (one + other[k]);
+}
+
 // Column of element k of thread t.
 template <bool F32, int E, bool VEC>
 __device__ __forceinline__ uint32_t column(int k, uint32_t t, uint32_t T) {
@@ -126,10 +174,21 @@ __device__ __forceinline__ uint32_t column(int k, uint32_t t, uint32_t T) {
     return ((k / V) * T + t) * V + k % V;
 }
 
+template <int CTRL>
+__device__ __forceinline__ float lanes(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over a wavefront: within each 16 lanes by register moves (pairs, quads, halves of 8, of 16), then
+// the four 16s.  No LDS on the way.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    v += lanes<0xb1>(v);   // quad_perm 1 0 3 2
+    v += lanes<0x4e>(v);   // quad_perm 2 3 0 1
+    v += lanes<0x141>(v);  // row_half_mirror
+    v += lanes<0x140>(v);  // row_mirror
+    const int b = __float_as_int(v);
+    return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
+           (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
 }
 
 // Sums of K values over the T threads of each row (T a multiple of 64; row g of the workgroup owns
@@ -162,51 +221,39 @@ __global__ __launch_bounds__(1024) void norm_forward(NormForward p) {
     __shared__ float lds[2][2][kMaxWaves];
     const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
     const uint32_t D = p.dim, b = blockIdx.y;
-    const bool pf = p.param_f32;
     const float inv_d = 1.0f / static_cast<float>(D);
-
-    // the factor on the branch, the factor and the shift of the next norm
-    float fy[HAS_Y ? E : 1], fn[NEXT ? E : 1], sh[NEXT ? E : 1];
-#pragma unroll
-    for (int k = 0; k < E; ++k) {
-        const uint32_t c = column<F32, E, VEC>(k, t, T);
-        const bool in = c < D;
-        const size_t bc = static_cast<size_t>(b) * D + c;
-        if constexpr (HAS_Y) {
-            float f = 1.f;
-            if (in && p.weight) f = load_param(p.weight, pf, c) + p.weight_offset;
-            if (in && p.gate) f *= load_param(p.gate, pf, bc);
-            fy[k] = f;
-        }
-        if constexpr (NEXT) {
-            float f = 1.f;
-            if (in && p.next_weight) f = load_param(p.next_weight, pf, c) + p.weight_offset;
-            if (in && p.next_scale) f *= 1.f + load_param(p.next_scale, pf, bc);
-            fn[k] = f;
-            sh[k] = in && p.next_shift ? load_param(p.next_shift, pf, bc) : 0.f;
-        }
-    }
 
     constexpr size_t es = F32 ? 4 : 2;
     const uint32_t step = gridDim.x * G;
-    int phase = 0;
-    for (uint32_t s0 = blockIdx.x * G; s0 < p.rows; s0 += step, phase ^= 1) {
-        const uint32_t s = s0 + g;
-        const bool live = s < p.rows;  // every thread keeps the barriers
+    RowPart<F32, E, VEC> yr, rr;
+    auto load = [&](uint32_t s) {
         const size_t off = (static_cast<size_t>(b) * p.rows + s) * D * es;
-        RowPart<F32, E, VEC> yr, rr;
-        if (live) {
+        if (s < p.rows) {
             if constexpr (HAS_Y) yr.load(static_cast<const char*>(p.y) + off, t, T, D);
             rr.load(static_cast<const char*>(p.residual) + off, t, T, D);
         } else {
             if constexpr (HAS_Y) yr.clear();
             rr.clear();
         }
-        float r[E];
+    };
+    load(blockIdx.x * G + g);
+    // the factor on the branch, the factor and the shift of the next norm
+    float fy[HAS_Y ? E : 1], fn[NEXT ? E : 1], sh[NEXT ? E : 1];
+    if constexpr (HAS_Y) load_factor<F32, E, VEC>(fy, p, p.weight, p.gate, 0.f, b, t, T);
+    if constexpr (NEXT) {
+        load_factor<F32, E, VEC>(fn, p, p.next_weight, p.next_scale, 1.f, b, t, T);
+        load_params<F32, E, VEC>(sh, p.next_shift, static_cast<size_t>(b) * D, p.param_f32, p.chunks, 0.f, t, T, D);
+    }
+    int phase = 0;
+    for (uint32_t s0 = blockIdx.x * G; s0 < p.rows; s0 += step, phase ^= 1) {
+        const uint32_t s = s0 + g;
+        const bool live = s < p.rows;  // every thread keeps the barriers
+        const size_t off = (static_cast<size_t>(b) * p.rows + s) * D * es;
+        float r[E], y[HAS_Y ? E : 1];
         rr.unpack(r);
+        if constexpr (HAS_Y) yr.unpack(y);
+        load(s + step);  // the next row travels while this one is summed
         if constexpr (HAS_Y) {
-            float y[E];
-            yr.unpack(y);
             float rstd = 1.f;
             if (p.post_norm) {
                 float ss[1] = {0.f};
@@ -238,32 +285,12 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
     extern __shared__ float cols[];  // (G - 1) * D: the rows' partial sums on their way to row 0
     const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
     const uint32_t D = p.dim, b = blockIdx.y;
-    const bool pf = p.param_f32;
     const float inv_d = 1.0f / static_cast<float>(D);
 
     float fy[HAS_Y ? E : 1], fn[NEXT ? E : 1];
-    float p1[NEXT ? E : 1], p2[NEXT ? E : 1], p3[HAS_Y ? E : 1];
-#pragma unroll
-    for (int k = 0; k < E; ++k) {
-        const uint32_t c = column<F32, E, VEC>(k, t, T);
-        const bool in = c < D;
-        const size_t bc = static_cast<size_t>(b) * D + c;
-        if constexpr (HAS_Y) {
-            float f = 1.f;
-            if (in && p.weight) f = load_param(p.weight, pf, c) + p.weight_offset;
-            if (in && p.gate) f *= load_param(p.gate, pf, bc);
-            fy[k] = f;
-            p3[k] = 0.f;
-        }
-        if constexpr (NEXT) {
-            float f = 1.f;
-            if (in && p.next_weight) f = load_param(p.next_weight, pf, c) + p.weight_offset;
-            if (in && p.next_scale) f *= 1.f + load_param(p.next_scale, pf, bc);
-            fn[k] = f;
-            p1[k] = 0.f;
-            p2[k] = 0.f;
-        }
-    }
+    float p1[NEXT ? E : 1] = {}, p2[NEXT ? E : 1] = {}, p3[HAS_Y ? E : 1] = {};
+    if constexpr (HAS_Y) load_factor<F32, E, VEC>(fy, p, p.weight, p.gate, 0.f, b, t, T);
+    if constexpr (NEXT) load_factor<F32, E, VEC>(fn, p, p.next_weight, p.next_scale, 1.f, b, t, T);
 
     constexpr size_t es = F32 ? 4 : 2;
     const uint32_t step = gridDim.x * G;
@@ -272,25 +299,21 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
         const uint32_t s = s0 + g;
         const bool live = s < p.rows;
         const size_t off = (static_cast<size_t>(b) * p.rows + s) * D * es;
-        RowPart<F32, E, VEC> raw;
-        float d[E], y[HAS_Y ? E : 1];
-        if (live && p.dr) raw.load(static_cast<const char*>(p.dr) + off, t, T, D);
-        else raw.clear();
-        raw.unpack(d);
-        if constexpr (HAS_Y) {
-            if (live && p.y) raw.load(static_cast<const char*>(p.y) + off, t, T, D);
+        float d[E], y[HAS_Y ? E : 1], r[NEXT ? E : 1], dn[NEXT ? E : 1];
+        auto get = [&](auto& to, const void* from) {
+            RowPart<F32, E, VEC> raw;
+            if (live && from) raw.load(static_cast<const char*>(from) + off, t, T, D);
             else raw.clear();
-            raw.unpack(y);
+            raw.unpack(to);
+        };
+        get(d, p.dr);
+        if constexpr (HAS_Y) get(y, p.y);
+        if constexpr (NEXT) {
+            get(r, p.r);
+            get(dn, p.dn);
         }
         float rstd_y = 1.f;
         if constexpr (NEXT) {
-            float r[E], dn[E];
-            if (live) raw.load(static_cast<const char*>(p.r) + off, t, T, D);
-            else raw.clear();
-            raw.unpack(r);
-            if (live) raw.load(static_cast<const char*>(p.dn) + off, t, T, D);
-            else raw.clear();
-            raw.unpack(dn);
             float ss[3] = {0.f, 0.f, 0.f};  // r.r, (dn fn).r, y.y
 #pragma unroll
             for (int k = 0; k < E; ++k) {
@@ -386,80 +409,80 @@ __device__ __forceinline__ void store_param(void* p, bool f32, size_t i, float v
         static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
 }
 
-// Sums over the partial rows of one sample (gridDim.y samples, kCols columns a workgroup, kLanes
-// threads down the parts), then the sample's gradients; the sums over samples are left in
-// partial row 0 of each sample for norm_backward_weights.
-constexpr int kCols = 32, kLanes = 32;
+// Sums over the partial rows, one of the three sums (blockIdx.z) and kCols columns a workgroup, kLanes
+// threads down the parts, and from them the gradients.  A workgroup goes through all samples, and adds up
+// the weight's gradient on the way, where they are few (gridDim.y = 1); else each has its own workgroup
+// and leaves its part in partial row 0 for norm_backward_weights.
+constexpr int kCols = 16, kLanes = 64;
 
-__global__ __launch_bounds__(kCols* kLanes) void norm_backward_samples(NormBackward p, uint32_t parts) {
-    __shared__ float lds[kLanes][kCols + 1];
-    const uint32_t col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
-    const uint32_t c = blockIdx.x * kCols + col, b = blockIdx.y;
-    const size_t plane = static_cast<size_t>(p.batch) * parts * p.dim;
-    const size_t base = static_cast<size_t>(b) * parts * p.dim + c;
-    float sum[3];
-    for (int which = 0; which < 3; ++which) {
-        const bool used = which == 2 ? p.has_y : p.next_norm;
-        if (!used) continue;  // uniform over the grid
-        float s = 0.f;
-        if (c < p.dim)
-            for (uint32_t i = lane; i < parts; i += kLanes) s += p.partial[which * plane + base + size_t(i) * p.dim];
-        __syncthreads();
-        lds[lane][col] = s;
-        __syncthreads();
+// The sum over the lanes of column `col`, in every thread of lane 0 (in lane order).
+__device__ __forceinline__ float lane_sum(float s, float (&lds)[kLanes][kCols + 1], uint32_t col, uint32_t lane) {
+    __syncthreads();
+    lds[lane][col] = s;
+    __syncthreads();
+    if (lane < 8) {
         s = 0.f;
-        if (lane == 0)
-            for (int i = 0; i < kLanes; ++i) s += lds[i][col];
-        sum[which] = s;
+#pragma unroll
+        for (int i = 0; i < kLanes / 8; ++i) s += lds[lane * (kLanes / 8) + i][col];
     }
-    if (lane != 0 || c >= p.dim) return;
-    const bool pf = p.param_f32;
-    const size_t bc = static_cast<size_t>(b) * p.dim + c;
-    if (p.next_norm) {
-        const float w = p.next_weight ? load_param(p.next_weight, pf, c) + p.weight_offset : 1.f;
-        const float f = p.next_scale ? 1.f + load_param(p.next_scale, pf, bc) : 1.f;
-        if (p.dnext_scale) store_param(p.dnext_scale, pf, bc, w * sum[0]);
-        if (p.dnext_shift) store_param(p.dnext_shift, pf, bc, sum[1]);
-        if (p.batch == 1) {
-            if (p.dnext_weight) store_param(p.dnext_weight, pf, c, f * sum[0]);
-        } else {
-            p.partial[base] = f * sum[0];
-        }
-    }
-    if (p.has_y) {
-        const float w = p.weight ? load_param(p.weight, pf, c) + p.weight_offset : 1.f;
-        const float f = p.gate ? load_param(p.gate, pf, bc) : 1.f;
-        if (p.dgate) store_param(p.dgate, pf, bc, w * sum[2]);
-        if (p.batch == 1) {
-            if (p.dweight) store_param(p.dweight, pf, c, f * sum[2]);
-        } else {
-            p.partial[2 * plane + base] = f * sum[2];
-        }
-    }
+    __syncthreads();
+    if (lane < 8) lds[lane][col] = s;
+    __syncthreads();
+    s = 0.f;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += lds[i][col];
+    return s;
 }
 
-// The weights' gradients: sums over samples of what norm_backward_samples left.
+__global__ __launch_bounds__(kCols* kLanes) void norm_backward_join(NormBackward p, uint32_t parts) {
+    __shared__ float lds[kLanes][kCols + 1];
+    const uint32_t which = blockIdx.z;
+    if (!(which == 2 ? p.has_y : p.next_norm)) return;
+    const uint32_t col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
+    const uint32_t c = blockIdx.x * kCols + col;
+    const bool all = gridDim.y == 1, pf = p.param_f32;
+    const void* weight = which == 2 ? p.weight : p.next_weight;
+    const void* factor = which == 2 ? p.gate : p.next_scale;
+    void* dfactor = which == 2 ? p.dgate : p.dnext_scale;
+    void* dweight = which == 2 ? p.dweight : p.dnext_weight;
+    float total = 0.f;
+    for (uint32_t b = blockIdx.y; b < (all ? p.batch : blockIdx.y + 1); ++b) {
+        float* part = p.partial + (static_cast<size_t>(which) * p.batch + b) * parts * p.dim + c;
+        float s = 0.f;
+        if (c < p.dim) {
+#pragma unroll 4
+            for (uint32_t i = lane; i < parts; i += kLanes) s += part[static_cast<size_t>(i) * p.dim];
+        }
+        s = lane_sum(s, lds, col, lane);
+        if (lane != 0 || c >= p.dim) continue;
+        const size_t bc = static_cast<size_t>(b) * p.dim + c;
+        if (which == 1) {
+            if (p.dnext_shift) store_param(p.dnext_shift, pf, bc, s);
+            continue;
+        }
+        const float w = weight ? load_param(weight, pf, c) + p.weight_offset : 1.f;
+        const float f = (which == 2 ? 0.f : 1.f) + (factor ? load_param(factor, pf, bc) : (which == 2 ? 1.f : 0.f));
+        if (dfactor) store_param(dfactor, pf, bc, w * s);
+        if (all) total = fmaf(f, s, total);
+        else part[0] = f * s;
+    }
+    if (all && which != 1 && dweight && lane == 0 && c < p.dim) store_param(dweight, pf, c, total);
+}
+
+// The weights' gradients: sums over the samples of what norm_backward_join left.
 __global__ __launch_bounds__(kCols* kLanes) void norm_backward_weights(NormBackward p, uint32_t parts) {
     __shared__ float lds[kLanes][kCols + 1];
     const uint32_t col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
-    const uint32_t c = blockIdx.x * kCols + col;
-    const size_t plane = static_cast<size_t>(p.batch) * parts * p.dim;
-    for (int which = 0; which < 3; which += 2) {
-        void* out = which == 0 ? p.dnext_weight : p.dweight;
-        if (out == nullptr) continue;
-        float s = 0.f;
-        if (c < p.dim)
-            for (uint32_t b = lane; b < p.batch; b += kLanes)
-                s += p.partial[which * plane + static_cast<size_t>(b) * parts * p.dim + c];
-        __syncthreads();
-        lds[lane][col] = s;
-        __syncthreads();
-        if (lane == 0 && c < p.dim) {
-            s = 0.f;
-            for (int i = 0; i < kLanes; ++i) s += lds[i][col];
-            store_param(out, p.param_f32, c, s);
-        }
-    }
+    const uint32_t c = blockIdx.x * kCols + col, which = blockIdx.z * 2;
+    void* out = which == 0 ? p.dnext_weight : p.dweight;
+    if (out == nullptr) return;
+    float s = 0.f;
+    if (c < p.dim)
+        for (uint32_t b = lane; b < p.batch; b += kLanes)
+            s += p.partial[(static_cast<size_t>(which) * p.batch + b) * parts * p.dim + c];
+    s = lane_sum(s, lds, col, lane);
+    if (lane == 0 && c < p.dim) store_param(out, p.param_f32, c, s);
 }
 
 template <bool F32, int E, bool VEC>
@@ -484,32 +507,33 @@ hipError_t backward_modes(const NormBackward& p, dim3 grid, dim3 block, size_t l
     return hipGetLastError();
 }
 
-// Threads a row and rows a workgroup for a row width: 8 elements a thread up to 8192 columns (the
-// most that 1024 threads then hold), 16 above, and rows side by side up to `threads` threads.
+// Threads a row and rows a workgroup: 8 elements a thread up to 8192 columns (the most that 1024 threads
+// then hold), 16 above; rows side by side up to 512 threads, as long as 512 workgroups are left to do.
+// Two workgroups of 512 threads a compute unit walk down the rows.  More of them at a time are slower,
+// though they hide more: forward, 69360 rows of 2048 bf16, 267 us with 4096 workgroups of 256 threads,
+// 222 with 1024, 212 with 512 of 512; a wavefront a row, without barriers, 207 to 216.  Backward, 36720
+// rows: 234 us with 512 of 1024 threads, 215 with 1024 of 512, 193 with 512 of 512.
 struct Shape {
     bool wide;
     uint32_t T, G;
 };
 
-constexpr uint32_t kForwardWorkgroups = 4096, kBackwardWorkgroups = 512;  // 16 and 2 a compute unit
+constexpr uint32_t kWorkgroups = 512, kThreads = 512;
 
-Shape row_shape(uint32_t dim, uint32_t threads) {
+Shape row_shape(uint32_t batch, uint32_t rows, uint32_t dim) {
     Shape s;
     s.wide = dim > 8192;
     const uint32_t per = s.wide ? 16 : 8;
     s.T = 64 * ((dim + 64 * per - 1) / (64 * per));
-    s.G = s.T >= threads ? 1 : threads / s.T;
+    s.G = s.T >= kThreads ? 1 : kThreads / s.T;
+    while (s.G > 1 && static_cast<uint64_t>(batch) * ((rows + s.G - 1) / s.G) < kWorkgroups) s.G /= 2;
     return s;
 }
 
-uint32_t row_parts(uint32_t batch, uint32_t rows, uint32_t G, uint32_t workgroups) {
+uint32_t row_parts(uint32_t batch, uint32_t rows, uint32_t G) {
     const uint32_t need = (rows + G - 1) / G;
-    const uint32_t most = workgroups / batch;
+    const uint32_t most = kWorkgroups / batch;
     return need < most ? need : (most > 0 ? most : 1);
-}
-
-uint32_t backward_parts(uint32_t batch, uint32_t rows, uint32_t dim) {
-    return row_parts(batch, rows, row_shape(dim, 1024).G, kBackwardWorkgroups);
 }
 
 __global__ __launch_bounds__(256) void norm_zero(void* p, size_t n, bool f32) {
@@ -520,8 +544,8 @@ __global__ __launch_bounds__(256) void norm_zero(void* p, size_t n, bool f32) {
 }  // namespace
 
 hipError_t launch_norm_forward(const NormForward& p, bool f32, bool vec, hipStream_t stream) {
-    const Shape s = row_shape(p.dim, 256);
-    const dim3 block(s.T, s.G), grid(row_parts(p.batch, p.rows, s.G, kForwardWorkgroups), p.batch);
+    const Shape s = row_shape(p.batch, p.rows, p.dim);
+    const dim3 block(s.T, s.G), grid(row_parts(p.batch, p.rows, s.G), p.batch);
     if (f32) {
         if (s.wide) return vec ? forward_modes<true, 16, true>(p, grid, block, stream) : forward_modes<true, 16, false>(p, grid, block, stream);
         return vec ? forward_modes<true, 8, true>(p, grid, block, stream) : forward_modes<true, 8, false>(p, grid, block, stream);
@@ -531,7 +555,7 @@ hipError_t launch_norm_forward(const NormForward& p, bool f32, bool vec, hipStre
 }
 
 size_t norm_backward_workspace(uint32_t batch, uint32_t rows, uint32_t dim) {
-    return size_t(3) * batch * backward_parts(batch, rows, dim) * dim * sizeof(float);
+    return size_t(3) * batch * row_parts(batch, rows, row_shape(batch, rows, dim).G) * dim * sizeof(float);
 }
 
 hipError_t launch_norm_backward(const NormBackward& p, bool f32, bool vec, hipStream_t stream) {
@@ -543,8 +567,8 @@ hipError_t launch_norm_backward(const NormBackward& p, bool f32, bool vec, hipSt
             if (v.first != nullptr && v.second != 0) norm_zero<<<64, 256, 0, stream>>>(v.first, v.second, p.param_f32);
         return hipGetLastError();
     }
-    const Shape s = row_shape(p.dim, 1024);
-    const uint32_t parts = backward_parts(p.batch, p.rows, p.dim);
+    const Shape s = row_shape(p.batch, p.rows, p.dim);
+    const uint32_t parts = row_parts(p.batch, p.rows, s.G);
     const dim3 block(s.T, s.G), grid(parts, p.batch);
     const size_t lds = size_t(s.G - 1) * p.dim * sizeof(float);
     hipError_t e;
@@ -557,10 +581,11 @@ hipError_t launch_norm_backward(const NormBackward& p, bool f32, bool vec, hipSt
     }
     if (e != hipSuccess || p.partial == nullptr) return e;
     const uint32_t cols = (p.dim + kCols - 1) / kCols;
-    norm_backward_samples<<<dim3(cols, p.batch), kCols * kLanes, 0, stream>>>(p, parts);
+    const bool few = p.batch <= 4;
+    norm_backward_join<<<dim3(cols, few ? 1 : p.batch, 3), kCols * kLanes, 0, stream>>>(p, parts);
     e = hipGetLastError();
-    if (e != hipSuccess || p.batch == 1 || (!p.dnext_weight && !p.dweight)) return e;
-    norm_backward_weights<<<cols, kCols * kLanes, 0, stream>>>(p, parts);
+    if (e != hipSuccess || few || (!p.dnext_weight && !p.dweight)) return e;
+    norm_backward_weights<<<dim3(cols, 1, 2), kCols * kLanes, 0, stream>>>(p, parts);
     return hipGetLastError();
 }
 

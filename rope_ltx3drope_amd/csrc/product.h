@@ -610,21 +610,22 @@ struct TileCost {
 
 // Fitted to products timed on the card, k of 4096 unless stated: bf16 2048 x 2048 47 us with tiles of
 // 128, 49 with 64; 4096 x 2048 65, 94 (88 with 256); 4096 x 16384, k 2048: 239 with 256, 297 with 128;
-// 512 x 4352, k 1536: 16 with 64, 21 with 128; 256 x 1024: 32 with 64, 15 split in four.  fp32 4096 x
+// 512 x 4352, k 1536: 16 with 64, 21 with 128; 256 x 1024: 32 with 64, 15 split in four; with k
+// outermost 4096 x 2048, k 16384: 305 with 128, 247 with 256 split in two.  fp32 4096 x
 // 4096, k 2048: 500 with 128, 507 with 64; 301 x 1152, k 5632: 126 with 64, 45 split in eight.
 template <class Op>
-constexpr TileCost tile_cost(uint32_t tile) {
+constexpr TileCost tile_cost(uint32_t tile, bool outer) {
     if (Op::kElem == 4) return tile == 128 ? TileCost{2.05f, 1.95f, 3.5f} : TileCost{0.69f, 0.49f, 1.5f};
     return tile == 256   ? TileCost{1.6f, 1.6f, 7.0f}
-           : tile == 128 ? TileCost{0.65f, 0.465f, 3.5f}
+           : tile == 128 ? TileCost{0.65f, outer ? 0.55f : 0.465f, 3.5f}
                          : TileCost{0.42f, 0.17f, 1.0f};
 }
 
 // The tile and split with the least time by these costs.  Splitting adds the sums' way through memory
 // and a launch; every part keeps 4 steps of k.
-template <class Op, bool GATED>
+template <class Op, bool GATED, bool OUTER>
 inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct) {
-    const float units = 256.f;
+    const uint32_t units = 256;
     const uint32_t steps = (k * Op::kElem + kRowBytes - 1) / kRowBytes;
     Plan best{};
     float least = 0.f;
@@ -632,12 +633,11 @@ inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct) {
         if (tile == 256 && (Op::kElem == 4 || !direct)) continue;
         const uint32_t bn = GATED ? tile / 2 : tile;
         const uint32_t tiles = ((M + tile - 1) / tile) * ((N + bn - 1) / bn);
-        const TileCost c = tile_cost<Op>(tile);
+        const TileCost c = tile_cost<Op>(tile, OUTER);
         for (uint32_t splits = 1; splits <= 16; splits += splits < 4 ? 1 : 2) {
             if (splits > 1 && (steps / splits < 4 || tiles >= 512)) break;
             const float depth = static_cast<float>((steps + splits - 1) / splits);
-            const float per_unit = static_cast<float>(tiles) * splits / units;
-            const float rounds = tile == 256 ? static_cast<float>((tiles * splits + 255) / 256) : per_unit;
+            const float rounds = static_cast<float>((tiles * splits + units - 1) / units);
             const float one = depth * c.alone + c.ends, many = rounds * (depth * c.full + c.ends);
             float us = one > many ? one : many;
             const size_t bytes = splits > 1 ? size_t(splits) * tiles * tile * tile * 4 : 0;
@@ -670,7 +670,7 @@ inline hipError_t launch_tiles(const Product& p, const Plan& plan, const Done& d
 
 template <class Op, bool GATED, bool A_OUTER, bool B_OUTER, class Done>
 hipError_t launch_product(Product p, bool direct, void* workspace, const Done& done, hipStream_t stream) {
-    const Plan plan = plan_product<Op, GATED>(p.M, p.N, p.k, direct);
+    const Plan plan = plan_product<Op, GATED, A_OUTER || B_OUTER>(p.M, p.N, p.k, direct);
     p.splits = plan.splits;
     p.partial = static_cast<float*>(workspace);
     if constexpr (Op::kElem != 4)

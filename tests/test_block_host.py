@@ -150,8 +150,8 @@ def test_norm_workspace_sizes():
     size = L.ltx3drope_norm_backward_workspace
     assert size(backward_call(dweight=None)) == 0
     assert size(backward_call(rows=0)) == 0
-    assert size(backward_call()) == 3 * 1 * 64 * 4  # 6 rows of one workgroup, no per-sample vector
-    assert size(backward_call(gate=FAKE, dgate=FAKE)) == 3 * 2 * 64 * 4  # one partial row a sample
+    assert size(backward_call()) == 3 * 6 * 64 * 4  # 6 rows, a workgroup each, no per-sample vector
+    assert size(backward_call(gate=FAKE, dgate=FAKE)) == 3 * 2 * 3 * 64 * 4
     assert size(backward_call(batch=1, rows=100000, dim=2048)) == 3 * 512 * 2048 * 4
     assert size(backward_call(eps=0.0)) == _lib.E_INVALID and size(None) == _lib.E_INVALID
 
