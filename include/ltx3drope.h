@@ -455,7 +455,7 @@ int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call)
  * gradients carry no rounding of theirs.
  * `workspace`: ltx3drope_gated_ffn_workspace bytes of device memory, 16-byte
  * aligned, that nothing else uses until the call's work on `stream` has run.  It
- * is 0 (then workspace may be NULL) but where more than 64 tokens meet long sums
+ * is 0 (then workspace may be NULL) but where more than 16 tokens meet long sums
  * and few outputs: the sums are then split over the chip and their parts lie there.
  * tokens = 0 or hidden = 0 is an empty call: OK, nothing launched, no pointer
  * looked at.  E_INVALID: a NULL descriptor, an unknown activation, one of g and u without the other, a workspace that is too small.

@@ -95,48 +95,58 @@ __device__ __forceinline__ float get(const void* p, size_t i) {
     if constexpr (F32) return static_cast<const float*>(p)[i];
     else return static_cast<float>(static_cast<const __bf16*>(p)[i]);
 }
-// dg and du as rows [M][2 * Fp]: dg, zeros up to Fp, du, zeros.  Four columns a thread; bound by the
-// bytes (14 read, 4 written an element in bf16).
+// dg and du as rows [M][2 * Fp]: dg, zeros up to Fp, du, zeros.  Eight columns a thread; bound by the
+// bytes (10 read and 4 written an element in bf16).
 template <bool F32>
 __global__ __launch_bounds__(256) void ffn_slopes(const void* dh, const float* g, const float* u, void* out, uint32_t M,
                                                   uint32_t F, uint32_t Fp, int kind) {
-    const uint32_t per_row = Fp / 4;
+    const uint32_t per_row = Fp / 8;
     const size_t total = static_cast<size_t>(M) * per_row;
     for (size_t t = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; t < total; t += size_t(gridDim.x) * 256) {
-        const uint32_t r = static_cast<uint32_t>(t / per_row), c = static_cast<uint32_t>(t % per_row) * 4;
+        const uint32_t r = static_cast<uint32_t>(t / per_row), c = static_cast<uint32_t>(t % per_row) * 8;
         const size_t at = static_cast<size_t>(r) * F + c;
-        f32x4 vg = {0, 0, 0, 0}, vu = {0, 0, 0, 0}, d = {0, 0, 0, 0};
-        if (c + 4 <= F) {
-            __builtin_memcpy(&vg, g + at, 16);
-            __builtin_memcpy(&vu, u + at, 16);
+        float vg[8] = {}, vu[8] = {}, d[8] = {};
+        if (c + 8 <= F) {
+            __builtin_memcpy(vg, g + at, 32);
+            __builtin_memcpy(vu, u + at, 32);
             if constexpr (F32) {
-                __builtin_memcpy(&d, static_cast<const float*>(dh) + at, 16);
+                __builtin_memcpy(d, static_cast<const float*>(dh) + at, 32);
             } else {
-                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                bf16x4 b;
-                __builtin_memcpy(&b, static_cast<const __bf16*>(dh) + at, 8);
-                d = __builtin_convertvector(b, f32x4);
+                bf16x8 h;
+                __builtin_memcpy(&h, static_cast<const __bf16*>(dh) + at, 16);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = static_cast<float>(h[i]);
             }
         } else {
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
                 if (c + i < F) {
                     vg[i] = g[at + i];
                     vu[i] = u[at + i];
                     d[i] = get<F32>(dh, at + i);
                 }
         }
-        f32x4 dg, du;
+        float dg[8], du[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             float slope;
             const float a = act(kind, vg[i], &slope);
-            dg[i] = d[i] * vu[i] * slope;
-            du[i] = d[i] * a;
-            if (c + i >= F) dg[i] = du[i] = 0.f;
+            const bool in = c + i < F;
+            dg[i] = in ? d[i] * vu[i] * slope : 0.f;
+            du[i] = in ? d[i] * a : 0.f;
         }
-        char* row = static_cast<char*>(out) + static_cast<size_t>(r) * 2 * Fp * (F32 ? 4 : 2);
-        store4<F32>(row, c, Fp, dg);
-        store4<F32>(row, Fp + c, 2 * Fp, du);
+        char* row = static_cast<char*>(out) + (static_cast<size_t>(r) * 2 * Fp + c) * (F32 ? 4 : 2);
+        auto put = [](char* to, const float(&v)[8]) {
+            if constexpr (F32) {
+                __builtin_memcpy(__builtin_assume_aligned(to, 16), v, 32);
+            } else {
+                bf16x8 h;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = static_cast<__bf16>(v[i]);
+                __builtin_memcpy(__builtin_assume_aligned(to, 16), &h, 16);
+            }
+        };
+        put(row, dg);
+        put(row + static_cast<size_t>(Fp) * (F32 ? 4 : 2), du);
     }
 }
 
@@ -156,7 +166,8 @@ bool forward_direct(const FfnProblem& p) {
 template <bool F32>
 size_t forward_workspace(const FfnProblem& p) {
     if (p.tokens <= kFewRows) return 0;
-    return plan_product<OpOf<F32>, true, false>(p.tokens, p.hidden, p.dim, forward_direct<F32>(p)).partial_bytes;
+    return plan_product<OpOf<F32>, true, false>(p.tokens, p.hidden, p.dim, forward_direct<F32>(p), p.dim * (F32 ? 4 : 2))
+        .partial_bytes;
 }
 
 template <bool F32>
@@ -190,8 +201,8 @@ BackwardLayout backward_layout(const FfnBackwardProblem& p) {
     l.dx_direct = chunks16(p.w_gate, row, row) && chunks16(p.w_up, row, row);
     l.dw_direct = chunks16(p.x, row, row);
     l.slopes = size_t(p.tokens) * 2 * l.Fp * es;  // whole 128-byte steps
-    const size_t a = p.dx ? plan_product<OpOf<F32>, false, true>(p.tokens, p.dim, 2 * l.Fp, l.dx_direct).partial_bytes : 0;
-    const size_t b = p.dw_gate ? plan_product<OpOf<F32>, false, true>(2 * l.Fp, p.dim, p.tokens, l.dw_direct).partial_bytes : 0;
+    const size_t a = p.dx ? plan_product<OpOf<F32>, false, true>(p.tokens, p.dim, 2 * l.Fp, l.dx_direct, row).partial_bytes : 0;
+    const size_t b = p.dw_gate ? plan_product<OpOf<F32>, false, true>(2 * l.Fp, p.dim, p.tokens, l.dw_direct, row).partial_bytes : 0;
     l.bytes = l.slopes + (a > b ? a : b);
     return l;
 }
@@ -209,7 +220,7 @@ hipError_t backward(const FfnBackwardProblem& p, hipStream_t stream) {
     const BackwardLayout l = backward_layout<F32>(p);
     char* slopes = static_cast<char*>(p.workspace);
     char* partial = slopes + l.slopes;
-    const size_t groups = (size_t(p.tokens) * (l.Fp / 4) + 255) / 256;
+    const size_t groups = (size_t(p.tokens) * (l.Fp / 8) + 255) / 256;
     ffn_slopes<F32><<<static_cast<uint32_t>(groups < 16384 ? groups : 16384), 256, 0, stream>>>(
         p.dh, p.g, p.u, slopes, p.tokens, p.hidden, l.Fp, p.activation);
     hipError_t e = hipGetLastError();

@@ -25,27 +25,51 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 struct OpBf16 {
     using Acc = f32x4;
+    using Sum = float;
     static constexpr int kElem = 2;
     static __device__ __forceinline__ void mac(Acc& c, u32x4 b, u32x4 a) {
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0,
                                                     0, 0);
     }
+    // the eight products of a chunk
+    static __device__ __forceinline__ float dot(u32x4 a, u32x4 b, float s) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = a[j], y = b[j];  // a cast of a[j] itself takes element 0
+            s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), __builtin_bit_cast(bf16x2, y), s, false);
+        }
+        return s;
+    }
 };
 struct OpI8 {
     using Acc = i32x4;
+    using Sum = int;
     static constexpr int kElem = 1;
     static __device__ __forceinline__ void mac(Acc& c, u32x4 b, u32x4 a) {
         c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), c, 0, 0,
                                                   0);
     }
+    static __device__ __forceinline__ int dot(u32x4 a, u32x4 b, int s) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s = __builtin_amdgcn_sdot4(static_cast<int>(a[j]), static_cast<int>(b[j]), s, false);
+        return s;
+    }
 };
 struct OpF32 {
     using Acc = f32x4;
+    using Sum = float;
     static constexpr int kElem = 4;
     static __device__ __forceinline__ void mac(Acc& c, u32x4 b, u32x4 a) {
         const f32x4 fb = __builtin_bit_cast(f32x4, b), fa = __builtin_bit_cast(f32x4, a);
 #pragma unroll
         for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j], fa[j], c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float dot(u32x4 a, u32x4 b, float s) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fmaf(__uint_as_float(a[j]), __uint_as_float(b[j]), s);
+        return s;
     }
 };
 
@@ -108,12 +132,13 @@ __device__ __forceinline__ void wait_and_meet() {
 }
 
 // 16 bytes of a row from byte k on; what lies past `end` is zero.  Without alignment the last chunk is
-// read one element at a time.
-template <class Op, bool ALIGNED>
+// read one element at a time.  STREAM: nobody reads these bytes again soon.
+template <class Op, bool ALIGNED, bool STREAM>
 __device__ __forceinline__ u32x4 load_chunk(const char* row, uint32_t k, uint32_t end) {
     u32x4 v = {0, 0, 0, 0};
     if constexpr (ALIGNED) {
-        if (k < end) v = *reinterpret_cast<const u32x4*>(row + k);
+        const u32x4* at = reinterpret_cast<const u32x4*>(row + k);
+        if (k < end) v = STREAM ? __builtin_nontemporal_load(at) : *at;
     } else {
         if (k + 16 <= end) {
             __builtin_memcpy(&v, row + k, 16);
@@ -197,7 +222,7 @@ struct Side {
 // BM x BN tiles, WM x WN wavefronts, each with (BM / WM) x (BN / WN) of the tile in registers.
 // DIRECT: 16-byte aligned operands go from memory to LDS without passing through registers; otherwise
 // they pass through them (any alignment).  A_OUTER, B_OUTER: k outermost.
-template <class Op, int BM, int BN, int WM, int WN, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
+template <class Op, int BM, int BN, int WM, int WN, bool PIPELINED, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
           class Done>
 __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done done) {
     constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
@@ -208,8 +233,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
     // step's time to land at the least; with the third slot A's have two, and half as many bytes again
     // are on their way at any time, which is what the copies' rate goes by (4096 x 16384 x 2048 in bf16:
     // see the launch rule for both).
-    constexpr bool kPipelined = DIRECT && BM == 256;
-    constexpr int kSlotsA = kPipelined ? 3 : 2, kStepK = SA::kStepK;
+    constexpr int kSlotsA = PIPELINED ? 3 : 2, kStepK = SA::kStepK;
     constexpr int kBytesB = BN * kRowBytes, kAtB = kSlotsA * SA::kBytes;
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies a wavefront makes of each operand
     static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN, "a tile's copies split evenly over the wavefronts");
@@ -307,9 +331,9 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
                 if constexpr (A_OUTER) {
                     const uint32_t k = step * kStepK + line_a[i];
                     if (k < p.k)
-                        held[i] = load_chunk<Op, false>(p.a + k * p.a_pitch, m0 * Op::kElem + byte_a[i], p.M * Op::kElem);
+                        held[i] = load_chunk<Op, false, false>(p.a + k * p.a_pitch, m0 * Op::kElem + byte_a[i], p.M * Op::kElem);
                 } else if (m0 + line_a[i] < p.M) {
-                    held[i] = load_chunk<Op, false>(p.a + (m0 + line_a[i]) * p.a_pitch, step * kRowBytes + byte_a[i],
+                    held[i] = load_chunk<Op, false, false>(p.a + (m0 + line_a[i]) * p.a_pitch, step * kRowBytes + byte_a[i],
                                                     p.k * Op::kElem);
                 }
             }
@@ -321,10 +345,10 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
                     uint32_t k0, rows;
                     const char* base = b_segment(step, k0, rows);
                     if (line_b[i] < rows)
-                        h = load_chunk<Op, false>(base + (k0 + line_b[i]) * p.b_pitch, n0 * Op::kElem + byte_b[i],
+                        h = load_chunk<Op, false, false>(base + (k0 + line_b[i]) * p.b_pitch, n0 * Op::kElem + byte_b[i],
                                                   p.N * Op::kElem);
                 } else if (n0 + line_b[i] < p.N) {
-                    h = load_chunk<Op, false>(p.b[GATED && i >= CB / 2] + (n0 + line_b[i]) * p.b_pitch,
+                    h = load_chunk<Op, false, false>(p.b[GATED && i >= CB / 2] + (n0 + line_b[i]) * p.b_pitch,
                                               step * kRowBytes + byte_b[i], p.k * Op::kElem);
                 }
             }
@@ -394,7 +418,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
         }
     };
 
-    if constexpr (kPipelined) {
+    if constexpr (PIPELINED) {
         // Half a step is multiplied while the next half step's operands are read from LDS.  The step
         // after this one has to be in LDS, and this one's slots are free, once every wavefront has read
         // its second half: they meet between the two multiplications, with operands for the second in
@@ -509,61 +533,109 @@ __global__ __launch_bounds__(WM* WN * 64) void product_join(Product p, Done done
     }
 }
 
-// Few rows of A (at most 16 * MF): B is read once, straight into registers, 16 of its rows a workgroup,
-// and the wavefronts of a workgroup share out k.  Their sums meet in LDS.  Bound by the bytes of B.
-template <class Op, int MF, int NW, bool GATED, bool ALIGNED, class Done>
-__global__ __launch_bounds__(NW * 64) void product_rows(Product p, Done done) {
-    constexpr int NB = GATED ? 2 : 1;
+// The sum over a wavefront, in every lane.
+template <class T>
+__device__ __forceinline__ T lanes_sum(T v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
+// One to four rows of A: a wavefront takes one row of B (of each B), its lanes along k, 4 KB of it at a
+// time, and multiplies it by every row of A in registers.  Bound by the bytes of B, which it reads in
+// whole kilobytes: 2 x 10240 rows of 4096 bf16 in 25 us (6.7 TB/s), where the matrix cores' layout, 16
+// rows a load, takes 37.  The four wavefronts of a workgroup put their sums side by side for `done`.
+template <class Op, int MT, bool GATED, bool ALIGNED, class Done>
+__global__ __launch_bounds__(256) void product_tokens(Product p, Done done) {
+    constexpr int NB = GATED ? 2 : 1, KV = 4;
+    using Sum = typename Op::Sum;
+    __shared__ Sum lds[NB][MT][4];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t n0 = blockIdx.x * 4, n = n0 + wave < p.N ? n0 + wave : p.N - 1;
+    const uint32_t k_bytes = p.k * Op::kElem;
+    const char* rb[NB];
+#pragma unroll
+    for (int q = 0; q < NB; ++q) rb[q] = p.b[q] + n * p.b_pitch;
+    Sum sum[NB][MT] = {};
+    for (uint32_t k0 = 0; k0 < k_bytes; k0 += KV * 1024) {
+        u32x4 b[NB][KV];
+#pragma unroll
+        for (int q = 0; q < NB; ++q)
+#pragma unroll
+            for (int i = 0; i < KV; ++i) b[q][i] = load_chunk<Op, ALIGNED, true>(rb[q], k0 + i * 1024 + lane * 16, k_bytes);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const char* ra = p.a + (m < static_cast<int>(p.M) ? m : 0) * p.a_pitch;
+#pragma unroll
+            for (int i = 0; i < KV; ++i) {
+                const u32x4 a = load_chunk<Op, ALIGNED, false>(ra, k0 + i * 1024 + lane * 16, k_bytes);
+#pragma unroll
+                for (int q = 0; q < NB; ++q) sum[q][m] = Op::dot(a, b[q][i], sum[q][m]);
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < NB; ++q)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const Sum s = lanes_sum(sum[q][m]);
+            if (lane == 0) lds[q][m][wave] = s;
+        }
+    __syncthreads();
+    const uint32_t m = threadIdx.x;
+    if (m < p.M && m < MT) {
+        typename Op::Acc v[NB];
+#pragma unroll
+        for (int q = 0; q < NB; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[q][i] = lds[q][m][i];
+        if constexpr (GATED) done(m, n0, p.N, v[0], v[1]);
+        else done(m, n0, p.N, v[0]);
+    }
+}
+
+// Up to 16 rows of A: B is read once, straight into registers, 16 of its rows a workgroup, and the
+// wavefronts of a workgroup share out k.  Their sums meet in LDS.  Bound by the bytes of B.
+template <class Op, bool GATED, bool ALIGNED, class Done>
+__global__ __launch_bounds__(512) void product_rows(Product p, Done done) {
+    constexpr int NB = GATED ? 2 : 1, NW = 8, U = 4;  // U steps of k in flight: 256 bytes of a row at a time
     using Acc = typename Op::Acc;
-    __shared__ Acc lds[NW][NB * MF][64];
+    __shared__ Acc lds[NW][NB][64];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n0 = blockIdx.x * 16, r = lane & 15;
     const uint32_t n = n0 + r < p.N ? n0 + r : p.N - 1;  // rows past the end repeat the last one
     const char* rb[NB];
 #pragma unroll
     for (int q = 0; q < NB; ++q) rb[q] = p.b[q] + n * p.b_pitch;
-    const char* ra[MF];
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-        const uint32_t m = i * 16 + r < p.M ? i * 16 + r : p.M - 1;
-        ra[i] = p.a + m * p.a_pitch;
-    }
-    Acc acc[NB][MF] = {};
-    const uint32_t k_bytes = p.k * Op::kElem;
-    const uint32_t kl = (lane >> 4) * 16;
-    constexpr int U = MF > 1 ? 2 : 4;  // steps of k in flight; 128 bytes or more of a row at a time
+    const char* ra = p.a + (r < p.M ? r : p.M - 1) * p.a_pitch;
+    const uint32_t k_bytes = p.k * Op::kElem, kl = (lane >> 4) * 16;
+    Acc acc[NB] = {};
     for (uint32_t k0 = wave * 64 * U; k0 < k_bytes; k0 += NW * 64 * U) {
-        u32x4 b[U][NB], a[U][MF];
+        u32x4 b[U][NB], a[U];
 #pragma unroll
         for (int s = 0; s < U; ++s) {
             const uint32_t k = k0 + s * 64 + kl;
 #pragma unroll
-            for (int q = 0; q < NB; ++q) b[s][q] = load_chunk<Op, ALIGNED>(rb[q], k, k_bytes);
-#pragma unroll
-            for (int i = 0; i < MF; ++i) a[s][i] = load_chunk<Op, ALIGNED>(ra[i], k, k_bytes);
+            for (int q = 0; q < NB; ++q) b[s][q] = load_chunk<Op, ALIGNED, false>(rb[q], k, k_bytes);
+            a[s] = load_chunk<Op, ALIGNED, false>(ra, k, k_bytes);
         }
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
-            for (int q = 0; q < NB; ++q)
-#pragma unroll
-                for (int i = 0; i < MF; ++i) Op::mac(acc[q][i], b[s][q], a[s][i]);
+            for (int q = 0; q < NB; ++q) Op::mac(acc[q], b[s][q], a[s]);
     }
 #pragma unroll
-    for (int q = 0; q < NB; ++q)
-#pragma unroll
-        for (int i = 0; i < MF; ++i) lds[wave][q * MF + i][lane] = acc[q][i];
+    for (int q = 0; q < NB; ++q) lds[wave][q][lane] = acc[q];
     __syncthreads();
-    for (uint32_t i = wave; i < MF; i += NW) {
-        Acc sum[NB] = {};
-        for (int w = 0; w < NW; ++w)
+    if (wave != 0) return;
+    Acc sum[NB] = {};
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
-            for (int q = 0; q < NB; ++q) sum[q] += lds[w][q * MF + i][lane];
-        const uint32_t m = i * 16 + r, nn = n0 + (lane >> 4) * 4;
-        if (m < p.M && nn < p.N) {
-            if constexpr (GATED) done(m, nn, p.N, sum[0], sum[1]);
-            else done(m, nn, p.N, sum[0]);
-        }
+        for (int q = 0; q < NB; ++q) sum[q] += lds[w][q][lane];
+    const uint32_t nn = n0 + (lane >> 4) * 4;
+    if (r < p.M && nn < p.N) {
+        if constexpr (GATED) done(r, nn, p.N, sum[0], sum[1]);
+        else done(r, nn, p.N, sum[0]);
     }
 }
 
@@ -593,57 +665,76 @@ __device__ __forceinline__ void store4(void* row, uint32_t n, uint32_t N, f32x4 
 
 inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-constexpr uint32_t kFewRows = 64;  // most rows of A that product_rows takes
+constexpr uint32_t kFewRows = 16;  // most rows of A that the kernels without tiles take
 
-// How a product runs: square tiles of 256, 128 or 64 (gated: half as wide in either B), and over how many
-// workgroups its sums are split.
+// How a product runs: its tile (gated: bn / 2 columns of either B), and over how many workgroups its sums
+// are split.
 struct Plan {
-    uint32_t tile, tiles, splits;
+    uint32_t bm, bn, tiles, splits;
     size_t partial_bytes;
 };
 
-// Microseconds that a tile's workgroup takes: a step of k alone on its compute unit (`alone`), its share
-// of a step when the unit is full (`full`), and a tile's start and end (`ends`).
+// Microseconds that a tile's workgroup takes: a step of k while the chip is nearly empty (`alone`), its
+// share of a step on a full compute unit (`full`; `outer` times that with k outermost, `torn` times
+// where rows of k do not start on 128-byte lines), and a tile's start and end (`ends`).
 struct TileCost {
-    float alone, full, ends;
+    uint32_t bm, bn;
+    float alone, full, outer, torn, ends;
 };
 
-// Fitted to products timed on the card, k of 4096 unless stated: bf16 2048 x 2048 47 us with tiles of
-// 128, 49 with 64; 4096 x 2048 65, 94 (88 with 256); 4096 x 16384, k 2048: 239 with 256, 297 with 128;
-// 512 x 4352, k 1536: 16 with 64, 21 with 128; 256 x 1024: 32 with 64, 15 split in four; with k
-// outermost 4096 x 2048, k 16384: 305 with 128, 247 with 256 split in two.  fp32 4096 x
-// 4096, k 2048: 500 with 128, 507 with 64; 301 x 1152, k 5632: 126 with 64, 45 split in eight.
+// Fitted to products timed on the card, in us, k innermost unless stated:
+//     bf16 (int8 alike, k twice as long)  256x256  256x128  128x128  128x64  64x64
+//     4096 x 16384, k 2048                    239      298      297      -      -
+//     4096 x  2048, k 4096                     88       62       68     88    100
+//     2048 x  2048, k 4096                     89       52       46     41     51
+//     the same, k outermost on both sides       -       60       54     43     57
+//      512 x  8704, k 1536                      -       25       27     26     28
+//      512 x  4352, k 1536                     38       24       21     18     16
+//      128 x  4096, k 4096                      -       48       42     36     26 (15 split in four)
+//      509 x  8662, k 1544: rows off the lines  44       29       29     35     36
+//     4096 x  4096, k 4104: the same           114      138      155    215    275
+//     fp32 4096 x 4096, k 2048                  -        -      500      -    507
+// so 128 x 128 is never the best by much, and is left out.  The wide tiles and the smallest keep a
+// third step of A on its way (product_tiles, PIPELINED); 128 x 64, three of which share a compute unit,
+// is faster without: 2048 x 2048 with k outermost 43 us against 45.
 template <class Op>
-constexpr TileCost tile_cost(uint32_t tile, bool outer) {
-    if (Op::kElem == 4) return tile == 128 ? TileCost{2.05f, 1.95f, 3.5f} : TileCost{0.69f, 0.49f, 1.5f};
-    return tile == 256   ? TileCost{1.6f, 1.6f, 7.0f}
-           : tile == 128 ? TileCost{0.65f, outer ? 0.55f : 0.465f, 3.5f}
-                         : TileCost{0.42f, 0.17f, 1.0f};
-}
+inline constexpr TileCost kTileCosts[4] = {
+    {256, 256, 1.6f, 1.6f, 1.0f, 1.1f, 7.0f},
+    {256, 128, 0.62f, 0.86f, 1.12f, 1.2f, 4.0f},
+    {128, 64, 0.46f, 0.275f, 1.05f, 1.42f, 1.2f},
+    {64, 64, 0.32f, 0.17f, 1.12f, 1.5f, 0.8f},
+};
+template <>
+inline constexpr TileCost kTileCosts<OpF32>[4] = {
+    {0, 0, 0, 0, 0, 0, 0},
+    {0, 0, 0, 0, 0, 0, 0},
+    {128, 64, 1.05f, 0.98f, 1.0f, 1.0f, 1.2f},
+    {64, 64, 0.6f, 0.49f, 1.0f, 1.0f, 0.8f},
+};
 
-// The tile and split with the least time by these costs.  Splitting adds the sums' way through memory
+// The tile and split with the least time by these costs.  pitch: bytes from row to row of B.  Splitting adds the sums' way through memory
 // and a launch; every part keeps 4 steps of k.
 template <class Op, bool GATED, bool OUTER>
-inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct) {
+inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct, uint64_t pitch) {
     const uint32_t units = 256;
     const uint32_t steps = (k * Op::kElem + kRowBytes - 1) / kRowBytes;
     Plan best{};
     float least = 0.f;
-    for (uint32_t tile : {256u, 128u, 64u}) {
-        if (tile == 256 && (Op::kElem == 4 || !direct)) continue;
-        const uint32_t bn = GATED ? tile / 2 : tile;
-        const uint32_t tiles = ((M + tile - 1) / tile) * ((N + bn - 1) / bn);
-        const TileCost c = tile_cost<Op>(tile, OUTER);
+    for (const TileCost& c : kTileCosts<Op>) {
+        if (c.bm == 0 || (c.bm == 256 && !direct)) continue;
+        const uint32_t bn = GATED ? c.bn / 2 : c.bn;
+        const uint32_t tiles = ((M + c.bm - 1) / c.bm) * ((N + bn - 1) / bn);
+        const float full = c.full * (OUTER ? c.outer : pitch % 128 != 0 ? c.torn : 1.f);
         for (uint32_t splits = 1; splits <= 16; splits += splits < 4 ? 1 : 2) {
-            if (splits > 1 && (steps / splits < 4 || tiles >= 512)) break;
+            if (splits > 1 && (steps / splits < 4 || tiles >= 2 * units)) break;
             const float depth = static_cast<float>((steps + splits - 1) / splits);
             const float rounds = static_cast<float>((tiles * splits + units - 1) / units);
-            const float one = depth * c.alone + c.ends, many = rounds * (depth * c.full + c.ends);
+            const float one = depth * c.alone + c.ends, many = rounds * (depth * full + c.ends);
             float us = one > many ? one : many;
-            const size_t bytes = splits > 1 ? size_t(splits) * tiles * tile * tile * 4 : 0;
-            if (splits > 1) us += 4.f + static_cast<float>(bytes) * 2 / 4e6f;
+            const size_t bytes = splits > 1 ? size_t(splits) * tiles * c.bm * c.bn * 4 : 0;
+            if (splits > 1) us += 2.f + static_cast<float>(bytes) * 2 / 5e6f;
             if (best.tiles == 0 || us < least) {
-                best = Plan{tile, tiles, splits, bytes};
+                best = Plan{c.bm, c.bn, tiles, splits, bytes};
                 least = us;
             }
         }
@@ -656,30 +747,34 @@ inline bool chunks16(const void* p, uint64_t pitch, uint64_t row_bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | pitch | row_bytes) & 15) == 0;
 }
 
-template <class Op, int TILE, int WM, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT, class Done>
+template <class Op, int BM, int BN, int WM, bool PIPELINED, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
+          class Done>
 inline hipError_t launch_tiles(const Product& p, const Plan& plan, const Done& done, hipStream_t stream) {
     constexpr int threads = WM * 2 * 64;
-    product_tiles<Op, TILE, TILE, WM, 2, GATED, A_OUTER, B_OUTER, DIRECT, Done>
+    product_tiles<Op, BM, BN, WM, 2, PIPELINED, GATED, A_OUTER, B_OUTER, DIRECT, Done>
         <<<plan.tiles * p.splits, threads, 0, stream>>>(p, done);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    product_join<Op, TILE, TILE, WM, 2, GATED, Done>
-        <<<plan.tiles * (TILE / WM / 16), threads, 0, stream>>>(p, done);
+    product_join<Op, BM, BN, WM, 2, GATED, Done><<<plan.tiles * (BM / WM / 16), threads, 0, stream>>>(p, done);
     return hipGetLastError();
 }
 
 template <class Op, bool GATED, bool A_OUTER, bool B_OUTER, class Done>
 hipError_t launch_product(Product p, bool direct, void* workspace, const Done& done, hipStream_t stream) {
-    const Plan plan = plan_product<Op, GATED, A_OUTER || B_OUTER>(p.M, p.N, p.k, direct);
+    const Plan plan = plan_product<Op, GATED, A_OUTER || B_OUTER>(p.M, p.N, p.k, direct, p.b_pitch);
     p.splits = plan.splits;
     p.partial = static_cast<float*>(workspace);
-    if constexpr (Op::kElem != 4)
-        if (plan.tile == 256) return launch_tiles<Op, 256, 4, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
-    if (plan.tile == 128)
-        return direct ? launch_tiles<Op, 128, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
-                      : launch_tiles<Op, 128, 2, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
-    return direct ? launch_tiles<Op, 64, 2, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
-                  : launch_tiles<Op, 64, 2, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+    if constexpr (Op::kElem != 4) {
+        if (plan.bn == 256)
+            return launch_tiles<Op, 256, 256, 4, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+        if (plan.bn == 128)
+            return launch_tiles<Op, 256, 128, 4, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+    }
+    if (plan.bm == 128)
+        return direct ? launch_tiles<Op, 128, 64, 2, false, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+                      : launch_tiles<Op, 128, 64, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+    return direct ? launch_tiles<Op, 64, 64, 2, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+                  : launch_tiles<Op, 64, 64, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
 }
 
 template <class Op, bool GATED, class Done>
@@ -687,13 +782,16 @@ hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t strea
     const uint64_t bytes = uint64_t(p.k) * Op::kElem;
     const bool al = chunks16(p.a, p.a_pitch, bytes) && chunks16(p.b[0], p.b_pitch, bytes) &&
                     (!GATED || chunks16(p.b[1], p.b_pitch, bytes));
-    const uint32_t groups = (p.N + 15) / 16;
-    if (p.M <= 16) {
-        if (al) product_rows<Op, 1, 8, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
-        else product_rows<Op, 1, 8, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
+    const uint32_t groups = p.M <= 4 ? (p.N + 3) / 4 : (p.N + 15) / 16;
+    if (p.M == 1) {
+        if (al) product_tokens<Op, 1, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
+        else product_tokens<Op, 1, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
+    } else if (p.M <= 4) {
+        if (al) product_tokens<Op, 4, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
+        else product_tokens<Op, 4, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
     } else {
-        if (al) product_rows<Op, 4, 8, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
-        else product_rows<Op, 4, 8, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
+        if (al) product_rows<Op, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
+        else product_rows<Op, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
     }
     return hipGetLastError();
 }

@@ -176,7 +176,7 @@ bool direct(const Q8Problem& p) { return chunks16(p.a, p.dim, p.dim) && chunks16
 
 size_t q8_workspace(const Q8Problem& p) {
     if (p.tokens <= kFewRows) return 0;
-    return plan_product<OpI8, false, false>(p.tokens, p.out, p.dim, direct(p)).partial_bytes;
+    return plan_product<OpI8, false, false>(p.tokens, p.out, p.dim, direct(p), p.dim).partial_bytes;
 }
 
 hipError_t launch_q8(const Q8Problem& p, bool f32, hipStream_t stream) {

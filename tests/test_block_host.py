@@ -167,9 +167,9 @@ def ffn_call(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(activation=3), (_lib.E_INVALID, "OK")), (dict(activation=-1), (_lib.E_INVALID, "OK")),
     (dict(g=FAKE * 5), (_lib.E_INVALID, "OK")),
-    (dict(tokens=65, dim=4096), (_lib.E_INVALID, "OK")),  # sums to be split, no workspace
-    (dict(tokens=65, dim=4096, workspace_bytes=-1), (_lib.E_INVALID, "OK")),
-    (dict(tokens=65, dim=4096, workspace_bytes=1 << 20), (_lib.E_UNSUPPORTED, "NULLPTR")),
+    (dict(tokens=17, dim=4096), (_lib.E_INVALID, "OK")),  # sums to be split, no workspace
+    (dict(tokens=17, dim=4096, workspace_bytes=-1), (_lib.E_INVALID, "OK")),
+    (dict(tokens=17, dim=4096, workspace_bytes=1 << 20), (_lib.E_UNSUPPORTED, "NULLPTR")),
     (dict(dtype=2), (_lib.E_UNSUPPORTED, "DTYPE")), (dict(dim=0), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")),
     (dict(tokens=-1), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")), (dict(dim=1 << 21), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
     (dict(hidden=1 << 20), (_lib.E_UNSUPPORTED, "TOO_LARGE")), (dict(tokens=1 << 21), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
@@ -209,14 +209,14 @@ def test_ffn_backward_refusals(kw, want):
 
 def test_product_workspace_sizes():
     # few tiles and long sums are split; many tiles, short sums and few tokens are not
-    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=64, dim=4096)) == 0
-    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=65)) == 0
-    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=65, dim=4096)) > 0
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=16, dim=4096)) == 0
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=17)) == 0
+    assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=17, dim=4096)) > 0
     assert L.ltx3drope_gated_ffn_workspace(ffn_call(tokens=8192, dim=4096, hidden=8192)) == 0
     assert L.ltx3drope_gated_ffn_backward_workspace(ffn_backward_call(tokens=0)) == 0
     assert L.ltx3drope_gated_ffn_backward_workspace(ffn_backward_call()) > 0
     assert L.ltx3drope_q8_matmul_workspace(q8_call(tokens=65)) == 0
-    assert L.ltx3drope_q8_matmul_workspace(q8_call(tokens=65, dim=4096)) > 0
+    assert L.ltx3drope_q8_matmul_workspace(q8_call(tokens=17, dim=4096)) > 0
     for f in (L.ltx3drope_gated_ffn_workspace, L.ltx3drope_gated_ffn_backward_workspace,
               L.ltx3drope_q8_matmul_workspace):
         assert f(None) == _lib.E_INVALID
@@ -230,7 +230,7 @@ def q8_call(**kw):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(reserved=1), (_lib.E_INVALID, "OK")), (dict(tokens=65, dim=4096), (_lib.E_INVALID, "OK")),
+    (dict(reserved=1), (_lib.E_INVALID, "OK")), (dict(tokens=17, dim=4096), (_lib.E_INVALID, "OK")),
     (dict(dtype=2), (_lib.E_UNSUPPORTED, "DTYPE")), (dict(dim=0), (_lib.E_UNSUPPORTED, "NONPOSITIVE_DIM")),
     (dict(dim=131072), (_lib.E_UNSUPPORTED, "TOO_LARGE")), (dict(out=1 << 26), (_lib.E_UNSUPPORTED, "TOO_LARGE")),
     (dict(tokens=1 << 20, out=1 << 20), (_lib.E_UNSUPPORTED, "TOO_LARGE")),

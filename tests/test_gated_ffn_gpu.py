@@ -93,20 +93,20 @@ def run(M, D, F, dtype, kind, seed):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 65, 100, 127, 128, 129, 257, 300])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 15, 16, 17, 33, 64, 65, 100, 127, 128, 129, 257, 300])
 def test_token_counts(M, dtype):
     run(M, 136, 200, dtype, KINDS[M % 3], M)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M", [3, 20, 77])
+@pytest.mark.parametrize("M", [1, 3, 9, 77])
 @pytest.mark.parametrize("D", [1, 3, 7, 8, 24, 31, 63, 64, 65, 100, 129, 200, 520, 1032])
 def test_widths(D, M, dtype):
     run(M, D, 48, dtype, KINDS[D % 3], 100 + D)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M", [5, 140])
+@pytest.mark.parametrize("M", [1, 4, 5, 140])
 @pytest.mark.parametrize("F", [1, 2, 3, 5, 15, 16, 17, 63, 64, 66, 100, 127, 128, 130, 257])
 def test_hidden_widths(F, M, dtype):
     run(M, 72, F, dtype, KINDS[F % 3], 200 + F)
@@ -114,7 +114,7 @@ def test_hidden_widths(F, M, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,D,F", [(2048, 128, 3200), (2047, 72, 3201), (2300, 2304, 1152), (300, 2056, 700),
-                                   (1025, 4096, 64), (70, 8200, 20), (1700, 640, 65), (90, 1025, 1700)])
+                                   (1025, 4096, 64), (1, 8200, 30), (3, 4104, 257), (12, 5000, 33), (70, 8200, 20), (1700, 640, 65), (90, 1025, 1700)])
 def test_large_tiles(M, D, F, dtype):
     """Enough tiles for the large ones; long sums; odd edges of both."""
     run(M, D, F, dtype, "silu", 300 + M)
@@ -141,7 +141,7 @@ def test_activations_over_their_range(kind, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_unaligned_tensors(dtype):
     """Tensors that start one element past a 16-byte boundary."""
-    for M in (4, 100):
+    for M in (1, 4, 10, 100):
         t = inputs(M, 64, 80, dtype, 9)
 
         def shifted(v):
@@ -172,7 +172,7 @@ def test_leading_dimensions_and_parts_left_out():
 
 
 def test_rows_behind_the_output_are_left_alone():
-    for M in (5, 90):
+    for M in (1, 4, 8, 90):
         t = inputs(M, 64, 100, torch.bfloat16, 4)
         dev = {k: v.to(DEV) for k, v in t.items()}
         big = torch.full((M + 2, 100), 7.0, dtype=torch.bfloat16, device=DEV)
@@ -182,7 +182,7 @@ def test_rows_behind_the_output_are_left_alone():
 
 
 def test_a_row_of_nan_stays_its_own():
-    for M in (6, 130):
+    for M in (3, 6, 130):
         t = inputs(M, 64, 64, torch.bfloat16, 5)
         dev = {k: v.to(DEV) for k, v in t.items()}
         want = rla.gated_ffn(dev["x"], dev["w_gate"], dev["w_up"])

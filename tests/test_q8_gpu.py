@@ -80,18 +80,18 @@ def operands(M, K, N, seed, bias=True):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M", [1, 2, 16, 17, 40, 64, 65, 127, 128, 130, 300])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 16, 17, 40, 64, 65, 127, 128, 130, 300])
 def test_token_counts(M, dtype):
     check_matmul(*operands(M, 272, 140, M, M % 2 == 0), dtype)
 
 
-@pytest.mark.parametrize("M", [1, 30, 100])
+@pytest.mark.parametrize("M", [1, 4, 9, 30, 100])
 @pytest.mark.parametrize("K", [1, 2, 15, 16, 17, 64, 100, 127, 128, 129, 512, 1000, 4100])
 def test_depths(K, M):
     check_matmul(*operands(M, K, 70, K), torch.float32)
 
 
-@pytest.mark.parametrize("M", [1, 30, 100])
+@pytest.mark.parametrize("M", [1, 4, 9, 30, 100])
 @pytest.mark.parametrize("N", [1, 2, 3, 5, 15, 16, 17, 63, 64, 127, 128, 129, 260])
 def test_output_widths(N, M):
     check_matmul(*operands(M, 160, N, N), torch.bfloat16)
@@ -102,7 +102,7 @@ def test_large_tiles():
     check_matmul(*operands(4095, 100, 3329, 2), torch.float32)
 
 
-@pytest.mark.parametrize("M", [1, 65])
+@pytest.mark.parametrize("M", [1, 3, 7, 65])
 def test_longest_sums(M):
     """Every product at its largest over the longest row that is taken: the sums stay within 32 bits."""
     K = 131071
@@ -114,7 +114,7 @@ def test_longest_sums(M):
 
 
 def test_unaligned_operands():
-    for M in (3, 100):
+    for M in (1, 3, 7, 100):
         a, sa, b, sb, bias = operands(M, 256, 64, 8)
         want = check_matmul(a, sa, b, sb, bias, torch.float32)
 
