@@ -71,19 +71,23 @@ def _refused(status: int, reason: ctypes.c_int, what: str):
     return Ltx3dRopeUnsupported(_lib.REASONS.get(reason.value, str(reason.value)), status)
 
 
-def _torch():
-    import torch
+_torch_module = None
+_dtype_codes: dict = {}
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    return -1
+    _torch()
+    return _dtype_codes.get(t.dtype, -1)
 
 
 def _stream_ptr(device, stream=None) -> int:
@@ -425,80 +429,85 @@ def dit_freq_grid(theta: float, dim: int, num_rope_elems: int, double_precision:
     return out
 
 
-class _On:
-    """Allocations for a call on `stream`: memory taken from that stream's pool (its earlier uses are
-    ordered before the call, its later reuse after it), or from the current stream's without one."""
-
-    def __init__(self, stream):
-        self._ctx = None if stream is None else _torch().cuda.stream(stream)
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-
-
-def _block_check(status: int, reason: ctypes.c_int, what: str) -> None:
+def _finish(status: int, reason: ctypes.c_int, what: str) -> None:
+    if status == _lib.OK:
+        return
     if status == _lib.E_UNSUPPORTED:
         raise Ltx3dRopeUnsupported(_lib.REASONS.get(reason.value, str(reason.value)), status)
     _check(status, what)
 
 
+def _operand(t, shape, dtype, device) -> None:
+    """An operand must have this shape, dtype and device and be contiguous."""
+    if t.shape != shape:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    if t.dtype != dtype:
+        raise Ltx3dRopeUnsupported("DTYPE")
+    if t.device != device or not t.is_cuda:
+        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+    if not t.is_contiguous():
+        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+
+
 def _rows_marshal(first, others):
     """(batch, rows, dim) of a [batch, rows, dim] or [rows, dim] row tensor; `others` must match it."""
-    if first.dim() not in (2, 3):
+    shape, dtype, device = first.shape, first.dtype, first.device
+    if len(shape) != 2 and len(shape) != 3:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     if _dtype_code(first) < 0:
         raise Ltx3dRopeUnsupported("DTYPE")
-    if not first.is_cuda:
-        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
-    if not first.is_contiguous():
-        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
-    for t in others:
-        if t is None:
-            continue
-        if t.shape != first.shape:
-            raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-        if t.dtype != first.dtype:
-            raise Ltx3dRopeUnsupported("DTYPE")
-        if t.device != first.device:
-            raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
-        if not t.is_contiguous():
-            raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
-    s = first.shape
-    return (1, s[0], s[1]) if len(s) == 2 else (s[0], s[1], s[2])
+    for t in (first,) + others:
+        if t is not None:
+            _operand(t, shape, dtype, device)
+    return (1, shape[0], shape[1]) if len(shape) == 2 else tuple(shape)
 
 
-def _vectors_marshal(row, batch, dim, weights, per_sample):
-    """The vectors' common dtype: the rows' own or float32."""
-    dtype = None
-    for t, per in [(t, False) for t in weights] + [(t, True) for t in per_sample]:
-        if t is None:
-            continue
-        shape = tuple(t.shape)
-        if shape != ((batch, dim) if per else (dim,)) and not (per and batch == 1 and row.dim() == 2 and shape == (dim,)):
-            raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-        if _dtype_code(t) < 0 or (dtype is not None and t.dtype != dtype):
-            raise Ltx3dRopeUnsupported("DTYPE")
-        dtype = t.dtype
-        if t.device != row.device:
-            raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
-        if not t.is_contiguous():
-            raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
-    return row.dtype if dtype is None else dtype
+def _vectors_marshal(row, size, weights, per_sample):
+    """The code of the vectors' common dtype: the rows' own or float32."""
+    dtype, device, (batch, _, dim) = None, row.device, size
+    for t in weights:
+        if t is not None:
+            dtype = dtype or t.dtype
+            _operand(t, (dim,), dtype, device)
+    for t in per_sample:
+        if t is not None:
+            dtype = dtype or t.dtype
+            flat = batch == 1 and t.dim() == 1 and row.dim() == 2
+            _operand(t, (dim,) if flat else (batch, dim), dtype, device)
+    code = _dtype_codes.get(dtype or row.dtype, -1)
+    if code < 0:
+        raise Ltx3dRopeUnsupported("DTYPE")
+    return code
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
-def _norm_call(cls, row, param_dtype, after, post_norm, next_norm, size, eps, weight_offset, residual_scale, **ptrs):
-    return cls(dtype=_dtype_code(row), param_dtype=DTYPE_F32 if param_dtype == _torch().float32 else DTYPE_BF16,
-               after=after, post_norm=post_norm, next_norm=next_norm, batch=size[0], rows=size[1], dim=size[2],
-               eps=eps, weight_offset=weight_offset, residual_scale=residual_scale, **ptrs)
+def _empty(stream, make):
+    """make() with memory of the pool of `stream`, or of the current stream where that is None: such
+    memory's earlier uses are ordered before the call on that stream, and its later reuse after it."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
+
+
+def _workspace(stream, query, descriptor, device):
+    """A call's workspace (held by the caller until the launch) or None, from the pool of its stream."""
+    n = query(descriptor)
+    if n <= 0:
+        return None, 0
+    return _empty(stream, lambda: _torch().empty(n, dtype=_torch().uint8, device=device)), n
+
+
+def _norm(row, size, pd, after, post_norm, next_norm, eps, weight_offset, residual_scale, stream, what, *tensors):
+    reason = ctypes.c_int(0)
+    _lib.lib()
+    st = _lib.norm(_lib.NORM_BYTES.pack(_dtype_codes[row.dtype], pd, after, post_norm, next_norm, 0, *size, eps,
+                                        weight_offset, residual_scale, *[_ptr(t) for t in tensors]),
+                   _stream_ptr(row.device, stream), ctypes.byref(reason))
+    _finish(st, reason, what)
 
 
 def norm_before(x, weight=None, scale=None, shift=None, *, eps: float = 1e-6, weight_offset: float = 0.0, out=None,
@@ -509,15 +518,11 @@ def norm_before(x, weight=None, scale=None, shift=None, *, eps: float = 1e-6, we
     shift [batch, dim], one row a sample; the vectors float32 or x's dtype, any of them None.  out
     may be x itself."""
     size = _rows_marshal(x, (out,))
-    pd = _vectors_marshal(x, size[0], size[2], (weight,), (scale, shift))
+    pd = _vectors_marshal(x, size, (weight,), (scale, shift))
     if out is None:
-        with _On(stream):
-            out = _torch().empty_like(x)
-    c = _norm_call(_lib.Norm, x, pd, 0, 0, 1, size, eps, weight_offset, 1.0, residual=x.data_ptr(),
-                   next_weight=_ptr(weight), next_scale=_ptr(scale), next_shift=_ptr(shift), n=out.data_ptr())
-    reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_norm(c, _stream_ptr(x.device, stream), reason)
-    _block_check(st, reason, "norm_before")
+        out = _empty(stream, lambda: _torch().empty_like(x))
+    _norm(x, size, pd, 0, 0, 1, eps, weight_offset, 1.0, stream, "norm_before", None, x, None, None, weight, scale,
+          shift, None, out)
     return out
 
 
@@ -532,21 +537,15 @@ def norm_after(y, residual, weight=None, gate=None, *, post_norm: bool = True, r
     next_shift [batch, dim].  n is formed from r before r is rounded to its dtype.  r_out may be
     residual and n_out may be y."""
     size = _rows_marshal(y, (residual, r_out, n_out))
-    pd = _vectors_marshal(y, size[0], size[2], (weight, next_weight), (gate, next_scale, next_shift))
+    pd = _vectors_marshal(y, size, (weight, next_weight), (gate, next_scale, next_shift))
     if not next_norm and any(t is not None for t in (next_weight, next_scale, next_shift, n_out)):
         raise ValueError("next_norm=False takes no vector or output of the next norm")
-    with _On(stream):
-        if r_out is None:
-            r_out = _torch().empty_like(y)
-        if next_norm and n_out is None:
-            n_out = _torch().empty_like(y)
-    c = _norm_call(_lib.Norm, y, pd, 1, bool(post_norm), bool(next_norm), size, eps, weight_offset, residual_scale,
-                   y=y.data_ptr(), residual=residual.data_ptr(), weight=_ptr(weight), gate=_ptr(gate),
-                   next_weight=_ptr(next_weight), next_scale=_ptr(next_scale), next_shift=_ptr(next_shift),
-                   r=r_out.data_ptr(), n=_ptr(n_out))
-    reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_norm(c, _stream_ptr(y.device, stream), reason)
-    _block_check(st, reason, "norm_after")
+    if r_out is None:
+        r_out = _empty(stream, lambda: _torch().empty_like(y))
+    if next_norm and n_out is None:
+        n_out = _empty(stream, lambda: _torch().empty_like(y))
+    _norm(y, size, pd, 1, bool(post_norm), bool(next_norm), eps, weight_offset, residual_scale, stream, "norm_after",
+          y, residual, weight, gate, next_weight, next_scale, next_shift, r_out, n_out)
     return r_out, n_out
 
 
@@ -571,30 +570,25 @@ class NormAfterGrads(NamedTuple):
     dnext_shift: object
 
 
-def _norm_backward(row, pd, after, post_norm, next_norm, size, eps, weight_offset, residual_scale, stream, dr, dn, y, r,
-                   weight, gate, next_weight, next_scale, next_shift):
+def _norm_backward(row, size, pd, after, post_norm, next_norm, eps, weight_offset, residual_scale, stream, what, dr, dn,
+                   y, r, weight, gate, next_weight, next_scale, next_shift):
     torch = _torch()
+    _lib.lib()
 
-    def like(t):
-        return None if t is None else torch.empty_like(t)
+    def outputs():
+        like = [torch.empty_like(row), torch.empty_like(row) if after else None]
+        return like + [None if t is None else torch.empty_like(t) for t in (weight, gate, next_weight, next_scale,
+                                                                            next_shift)]
 
-    with _On(stream):
-        dresidual = torch.empty_like(row)
-        dy = torch.empty_like(row) if after else None
-        dweight, dgate, dnw, dns, dnsh = like(weight), like(gate), like(next_weight), like(next_scale), like(next_shift)
-        c = _norm_call(_lib.NormBackward, row, pd, after, post_norm, next_norm, size, eps, weight_offset, residual_scale,
-                       dr=_ptr(dr), dn=_ptr(dn), y=_ptr(y), r=_ptr(r), weight=_ptr(weight), gate=_ptr(gate),
-                       next_weight=_ptr(next_weight), next_scale=_ptr(next_scale), dresidual=dresidual.data_ptr(),
-                       dy=_ptr(dy), dweight=_ptr(dweight), dgate=_ptr(dgate), dnext_weight=_ptr(dnw),
-                       dnext_scale=_ptr(dns), dnext_shift=_ptr(dnsh))
-        ws_bytes = int(_lib.lib().ltx3drope_norm_backward_workspace(c))
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=row.device) if ws_bytes > 0 else None
-    if workspace is not None:
-        c.workspace, c.workspace_bytes = workspace.data_ptr(), ws_bytes
+    outs = _empty(stream, outputs)
+    head = (_dtype_codes[row.dtype], pd, after, post_norm, next_norm, 0, *size, eps, weight_offset, residual_scale,
+            *[_ptr(t) for t in (dr, dn, y, r, weight, gate, next_weight, next_scale, *outs)])
+    pack = _lib.NORM_BACKWARD_BYTES.pack
+    ws, n = _workspace(stream, _lib.norm_backward_workspace, pack(*head, 0, 0), row.device)
     reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_norm_backward(c, _stream_ptr(row.device, stream), reason)
-    _block_check(st, reason, "norm_backward")
-    return dy, dresidual, dweight, dgate, dnw, dns, dnsh
+    st = _lib.norm_backward(pack(*head, _ptr(ws), n), _stream_ptr(row.device, stream), ctypes.byref(reason))
+    _finish(st, reason, what)
+    return outs
 
 
 def norm_before_backward(dn, x, weight=None, scale=None, shift=None, *, dresidual=None, eps: float = 1e-6,
@@ -602,10 +596,11 @@ def norm_before_backward(dn, x, weight=None, scale=None, shift=None, *, dresidua
     """Gradients of norm_before at x for the output's gradient dn.  dresidual, if given, is what
     reaches x past the block and is added to dx.  shift only asks for its gradient."""
     size = _rows_marshal(dn, (x, dresidual))
-    pd = _vectors_marshal(dn, size[0], size[2], (weight,), (scale, shift))
-    g = _norm_backward(dn, pd, 0, 0, 1, size, eps, weight_offset, 1.0, stream, dresidual, dn, None, x, None, None,
-                       weight, scale, shift)
-    return NormBeforeGrads(g[1], g[4], g[5], g[6])
+    pd = _vectors_marshal(dn, size, (weight,), (scale, shift))
+    dx, _, _, _, dweight, dscale, dshift = _norm_backward(dn, size, pd, 0, 0, 1, eps, weight_offset, 1.0, stream,
+                                                          "norm_before_backward", dresidual, dn, None, x, None, None,
+                                                          weight, scale, shift)
+    return NormBeforeGrads(dx, dweight, dscale, dshift)
 
 
 def norm_after_backward(dr, dn, y, r, weight=None, gate=None, *, post_norm: bool = True, residual_scale: float = 1.0,
@@ -616,24 +611,13 @@ def norm_after_backward(dr, dn, y, r, weight=None, gate=None, *, post_norm: bool
     if (dn is not None) != bool(next_norm):
         raise ValueError("dn belongs to next_norm=True")
     size = _rows_marshal(y, (r, dr, dn))
-    pd = _vectors_marshal(y, size[0], size[2], (weight, next_weight), (gate, next_scale, next_shift))
+    pd = _vectors_marshal(y, size, (weight, next_weight), (gate, next_scale, next_shift))
     if not next_norm and any(t is not None for t in (next_weight, next_scale, next_shift)):
         raise ValueError("next_norm=False takes no vector of the next norm")
-    return NormAfterGrads(*_norm_backward(y, pd, 1, bool(post_norm), bool(next_norm), size, eps, weight_offset,
-                                          residual_scale, stream, dr, dn, y, r, weight, gate, next_weight, next_scale,
-                                          next_shift))
-
-
-def _matrix(t, shape, dtype, device):
-    """Checks of an operand of a product: its shape, dtype and device, contiguous."""
-    if tuple(t.shape) != tuple(shape):
-        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    if t.dtype != dtype:
-        raise Ltx3dRopeUnsupported("DTYPE")
-    if not t.is_cuda or t.device != device:
-        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
-    if not t.is_contiguous():
-        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    dresidual, dy, *rest = _norm_backward(y, size, pd, 1, bool(post_norm), bool(next_norm), eps, weight_offset,
+                                          residual_scale, stream, "norm_after_backward", dr, dn, y, r, weight, gate,
+                                          next_weight, next_scale, next_shift)
+    return NormAfterGrads(dy, dresidual, *rest)
 
 
 def _activation(name: str) -> int:
@@ -641,16 +625,6 @@ def _activation(name: str) -> int:
         return _lib.ACTIVATIONS[name]
     except KeyError:
         raise ValueError(f"activation must be one of {sorted(_lib.ACTIVATIONS)}") from None
-
-
-def _with_workspace(call, query, device):
-    """Gives a call the workspace that it asks for; returns the tensor, to be held until the launch."""
-    n = int(query(call))
-    if n <= 0:
-        return None
-    ws = _torch().empty(n, dtype=_torch().uint8, device=device)
-    call.workspace, call.workspace_bytes = ws.data_ptr(), n
-    return ws
 
 
 def gated_ffn(x, w_gate, w_up, activation: str = "silu", *, save: bool = False, out=None, stream=None):
@@ -661,26 +635,34 @@ def gated_ffn(x, w_gate, w_up, activation: str = "silu", *, save: bool = False, 
     projections for gated_ffn_backward, in float32 whatever x's dtype."""
     torch = _torch()
     act = _activation(activation)
-    if x.dim() < 1 or w_gate.dim() != 2:
+    xs, dtype, device = x.shape, x.dtype, x.device
+    if len(xs) < 1 or w_gate.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    dim, hidden = int(x.shape[-1]), int(w_gate.shape[0])
-    shape = tuple(x.shape[:-1]) + (hidden,)
-    _matrix(x, x.shape, x.dtype, x.device)
-    for w in (w_gate, w_up):
-        _matrix(w, (hidden, dim), x.dtype, x.device)
+    dim, hidden = xs[-1], w_gate.shape[0]
+    shape = xs[:-1] + (hidden,)
+    _operand(x, xs, dtype, device)
+    _operand(w_gate, (hidden, dim), dtype, device)
+    _operand(w_up, (hidden, dim), dtype, device)
     if out is not None:
-        _matrix(out, shape, x.dtype, x.device)
-    with _On(stream):
-        h = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
-        g, u = (torch.empty(shape, dtype=torch.float32, device=x.device) for _ in range(2)) if save else (None, None)
-        c = _lib.GatedFfn(dtype=_dtype_code(x), activation=act, tokens=x.numel() // dim if dim else 0, dim=dim,
-                          hidden=hidden, x=x.data_ptr(), w_gate=w_gate.data_ptr(), w_up=w_up.data_ptr(),
-                          h=h.data_ptr(), g=_ptr(g), u=_ptr(u))
-        ws = _with_workspace(c, _lib.lib().ltx3drope_gated_ffn_workspace, x.device)
+        _operand(out, shape, dtype, device)
+
+    def outputs():
+        h = torch.empty(shape, dtype=dtype, device=device) if out is None else out
+        if not save:
+            return h, None, None
+        return h, *(torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2))
+
+    h, g, u = _empty(stream, outputs)
+    _lib.lib()
+    pack = _lib.FFN_BYTES.pack
+    head = (_dtype_code(x), act, x.numel() // dim if dim else 0, dim, hidden, x.data_ptr(), w_gate.data_ptr(),
+            w_up.data_ptr(), h.data_ptr(), _ptr(g), _ptr(u))
+    descriptor = pack(*head, 0, 0)
+    ws, n = _workspace(stream, _lib.gated_ffn_workspace, descriptor, device)
     reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_gated_ffn(c, _stream_ptr(x.device, stream), reason)
-    del ws
-    _block_check(st, reason, "gated_ffn")
+    st = _lib.gated_ffn(descriptor if ws is None else pack(*head, ws.data_ptr(), n), _stream_ptr(device, stream),
+                        ctypes.byref(reason))
+    _finish(st, reason, "gated_ffn")
     return (h, g, u) if save else h
 
 
@@ -690,26 +672,28 @@ def gated_ffn_backward(dh, x, w_gate, w_up, g, u, activation: str = "silu", *, n
     need_dx=False or need_dw=False leaves those out (None)."""
     torch = _torch()
     act = _activation(activation)
-    if x.dim() < 1 or w_gate.dim() != 2:
+    xs, dtype, device = x.shape, x.dtype, x.device
+    if len(xs) < 1 or w_gate.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    dim, hidden = int(x.shape[-1]), int(w_gate.shape[0])
-    _matrix(x, x.shape, x.dtype, x.device)
-    for w in (w_gate, w_up):
-        _matrix(w, (hidden, dim), x.dtype, x.device)
-    for t, dtype in ((dh, x.dtype), (g, torch.float32), (u, torch.float32)):
-        _matrix(t, tuple(x.shape[:-1]) + (hidden,), dtype, x.device)
-    with _On(stream):
-        dx = torch.empty_like(x) if need_dx else None
-        dwg, dwu = (torch.empty_like(w_gate), torch.empty_like(w_up)) if need_dw else (None, None)
-        c = _lib.GatedFfnBackward(dtype=_dtype_code(x), activation=act, tokens=x.numel() // dim if dim else 0, dim=dim,
-                                  hidden=hidden, dh=dh.data_ptr(), x=x.data_ptr(), w_gate=w_gate.data_ptr(),
-                                  w_up=w_up.data_ptr(), g=g.data_ptr(), u=u.data_ptr(), dx=_ptr(dx),
-                                  dw_gate=_ptr(dwg), dw_up=_ptr(dwu))
-        ws = _with_workspace(c, _lib.lib().ltx3drope_gated_ffn_backward_workspace, x.device)
+    dim, hidden = xs[-1], w_gate.shape[0]
+    shape = xs[:-1] + (hidden,)
+    _operand(x, xs, dtype, device)
+    _operand(w_gate, (hidden, dim), dtype, device)
+    _operand(w_up, (hidden, dim), dtype, device)
+    _operand(dh, shape, dtype, device)
+    _operand(g, shape, torch.float32, device)
+    _operand(u, shape, torch.float32, device)
+    dx, dwg, dwu = _empty(stream, lambda: (torch.empty_like(x) if need_dx else None,
+                                           torch.empty_like(w_gate) if need_dw else None,
+                                           torch.empty_like(w_up) if need_dw else None))
+    _lib.lib()
+    pack = _lib.FFN_BACKWARD_BYTES.pack
+    head = (_dtype_code(x), act, x.numel() // dim if dim else 0, dim, hidden,
+            *[_ptr(t) for t in (dh, x, w_gate, w_up, g, u, dx, dwg, dwu)])
+    ws, n = _workspace(stream, _lib.gated_ffn_backward_workspace, pack(*head, 0, 0), device)
     reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_gated_ffn_backward(c, _stream_ptr(x.device, stream), reason)
-    del ws
-    _block_check(st, reason, "gated_ffn_backward")
+    st = _lib.gated_ffn_backward(pack(*head, _ptr(ws), n), _stream_ptr(device, stream), ctypes.byref(reason))
+    _finish(st, reason, "gated_ffn_backward")
     return dx, dwg, dwu
 
 
@@ -717,19 +701,23 @@ def q8_quantize(x, *, q_out=None, scale_out=None, stream=None):
     """Rows to 8-bit integers: (q int8 like x, scale float32 [...]) with scale = max |row| * (1/127) and
     q = round(x / scale).  x [..., dim], float32 or bfloat16."""
     torch = _torch()
-    if x.dim() < 1:
+    xs, device = x.shape, x.device
+    if len(xs) < 1:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    _matrix(x, x.shape, x.dtype, x.device)
-    dim = int(x.shape[-1])
-    with _On(stream):
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device) if q_out is None else q_out
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if scale_out is None else scale_out
-    _matrix(q, x.shape, torch.int8, x.device)
-    _matrix(scale, x.shape[:-1], torch.float32, x.device)
+    _operand(x, xs, x.dtype, device)
+    q, scale = q_out, scale_out
+    if q is None:
+        q = _empty(stream, lambda: torch.empty_like(x, dtype=torch.int8))
+    else:
+        _operand(q, xs, torch.int8, device)
+    if scale is None:
+        scale = _empty(stream, lambda: torch.empty(xs[:-1], dtype=torch.float32, device=device))
+    else:
+        _operand(scale, xs[:-1], torch.float32, device)
     reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_q8_quantize(_dtype_code(x), scale.numel(), dim, x.data_ptr(), q.data_ptr(),
-                                          scale.data_ptr(), _stream_ptr(x.device, stream), reason)
-    _block_check(st, reason, "q8_quantize")
+    st = _lib.lib().ltx3drope_q8_quantize(_dtype_code(x), scale.numel(), xs[-1], x.data_ptr(), q.data_ptr(),
+                                          scale.data_ptr(), _stream_ptr(device, stream), reason)
+    _finish(st, reason, "q8_quantize")
     return q, scale
 
 
@@ -740,30 +728,34 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
     [out, dim] with b_scale float32 [out] (one a channel); bias float32 [out] or None; dtype of the
     result: bfloat16 (default) or float32."""
     torch = _torch()
-    if a.dim() < 1 or b.dim() != 2:
+    shape, device = a.shape, a.device
+    if len(shape) < 1 or b.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    dim, n = int(a.shape[-1]), int(b.shape[0])
-    _matrix(a, a.shape, torch.int8, a.device)
-    _matrix(b, (n, dim), torch.int8, a.device)
-    _matrix(a_scale, a.shape[:-1], torch.float32, a.device)
-    _matrix(b_scale, (n,), torch.float32, a.device)
+    dim, n = shape[-1], b.shape[0]
+    _operand(a, shape, torch.int8, device)
+    _operand(b, (n, dim), torch.int8, device)
+    _operand(a_scale, shape[:-1], torch.float32, device)
+    _operand(b_scale, (n,), torch.float32, device)
     if bias is not None:
-        _matrix(bias, (n,), torch.float32, a.device)
+        _operand(bias, (n,), torch.float32, device)
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
-    shape = tuple(a.shape[:-1]) + (n,)
-    if out is not None:
-        _matrix(out, shape, dtype, a.device)
-    with _On(stream):
-        y = torch.empty(shape, dtype=dtype, device=a.device) if out is None else out
-        c = _lib.Q8Matmul(dtype=_dtype_code(y), tokens=a_scale.numel(), dim=dim, out=n, a=a.data_ptr(), b=b.data_ptr(),
-                          a_scale=a_scale.data_ptr(), b_scale=b_scale.data_ptr(), bias=_ptr(bias), y=y.data_ptr())
-        ws = _with_workspace(c, _lib.lib().ltx3drope_q8_matmul_workspace, a.device)
+    shape = shape[:-1] + (n,)
+    if out is None:
+        out = _empty(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+    else:
+        _operand(out, shape, dtype, device)
+    _lib.lib()
+    pack = _lib.Q8_BYTES.pack
+    head = (_dtype_code(out), 0, a_scale.numel(), dim, n, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(),
+            b_scale.data_ptr(), _ptr(bias), out.data_ptr())
+    descriptor = pack(*head, 0, 0)
+    ws, size = _workspace(stream, _lib.q8_matmul_workspace, descriptor, device)
     reason = ctypes.c_int(0)
-    st = _lib.lib().ltx3drope_q8_matmul(c, _stream_ptr(a.device, stream), reason)
-    del ws
-    _block_check(st, reason, "q8_matmul")
-    return y
+    st = _lib.q8_matmul(descriptor if ws is None else pack(*head, ws.data_ptr(), size), _stream_ptr(device, stream),
+                        ctypes.byref(reason))
+    _finish(st, reason, "q8_matmul")
+    return out
 
 
 def kernel_choice(q, k, tabs: Tables, q_out=None, k_out=None) -> str:

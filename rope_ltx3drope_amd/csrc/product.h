@@ -541,28 +541,37 @@ __device__ __forceinline__ T lanes_sum(T v) {
     return v;
 }
 
-// One to four rows of A: a wavefront takes one row of B (of each B), its lanes along k, 4 KB of it at a
+// One to four rows of A: a wavefront takes one row of B (of each B; two for more than one row of A, so
+// that they share its loads), its lanes along k, 4 KB of it at a
 // time, and multiplies it by every row of A in registers.  Bound by the bytes of B, which it reads in
 // whole kilobytes: 2 x 10240 rows of 4096 bf16 in 25 us (6.7 TB/s), where the matrix cores' layout, 16
 // rows a load, takes 37.  The four wavefronts of a workgroup put their sums side by side for `done`.
 template <class Op, int MT, bool GATED, bool ALIGNED, class Done>
 __global__ __launch_bounds__(256) void product_tokens(Product p, Done done) {
-    constexpr int NB = GATED ? 2 : 1, KV = 4;
+    constexpr int NB = GATED ? 2 : 1, KV = 4, RW = MT > 1 ? 2 : 1;  // rows of B a wavefront
     using Sum = typename Op::Sum;
-    __shared__ Sum lds[NB][MT][4];
+    __shared__ Sum lds[NB][MT][4 * RW];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t n0 = blockIdx.x * 4, n = n0 + wave < p.N ? n0 + wave : p.N - 1;
+    const uint32_t n0 = blockIdx.x * 4 * RW;
     const uint32_t k_bytes = p.k * Op::kElem;
-    const char* rb[NB];
+    const char* rb[NB][RW];
 #pragma unroll
-    for (int q = 0; q < NB; ++q) rb[q] = p.b[q] + n * p.b_pitch;
-    Sum sum[NB][MT] = {};
+    for (int q = 0; q < NB; ++q)
+#pragma unroll
+        for (int w = 0; w < RW; ++w) {
+            const uint32_t n = n0 + wave * RW + w;
+            rb[q][w] = p.b[q] + (n < p.N ? n : p.N - 1) * p.b_pitch;
+        }
+    Sum sum[NB][RW][MT] = {};
     for (uint32_t k0 = 0; k0 < k_bytes; k0 += KV * 1024) {
-        u32x4 b[NB][KV];
+        u32x4 b[NB][RW][KV];
 #pragma unroll
         for (int q = 0; q < NB; ++q)
 #pragma unroll
-            for (int i = 0; i < KV; ++i) b[q][i] = load_chunk<Op, ALIGNED, true>(rb[q], k0 + i * 1024 + lane * 16, k_bytes);
+            for (int w = 0; w < RW; ++w)
+#pragma unroll
+                for (int i = 0; i < KV; ++i)
+                    b[q][w][i] = load_chunk<Op, ALIGNED, true>(rb[q][w], k0 + i * 1024 + lane * 16, k_bytes);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const char* ra = p.a + (m < static_cast<int>(p.M) ? m : 0) * p.a_pitch;
@@ -570,27 +579,31 @@ __global__ __launch_bounds__(256) void product_tokens(Product p, Done done) {
             for (int i = 0; i < KV; ++i) {
                 const u32x4 a = load_chunk<Op, ALIGNED, false>(ra, k0 + i * 1024 + lane * 16, k_bytes);
 #pragma unroll
-                for (int q = 0; q < NB; ++q) sum[q][m] = Op::dot(a, b[q][i], sum[q][m]);
+                for (int q = 0; q < NB; ++q)
+#pragma unroll
+                    for (int w = 0; w < RW; ++w) sum[q][w][m] = Op::dot(a, b[q][w][i], sum[q][w][m]);
             }
         }
     }
 #pragma unroll
     for (int q = 0; q < NB; ++q)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const Sum s = lanes_sum(sum[q][m]);
-            if (lane == 0) lds[q][m][wave] = s;
-        }
+        for (int w = 0; w < RW; ++w)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const Sum s = lanes_sum(sum[q][w][m]);
+                if (lane == 0) lds[q][m][wave * RW + w] = s;
+            }
     __syncthreads();
-    const uint32_t m = threadIdx.x;
-    if (m < p.M && m < MT) {
+    const uint32_t m = threadIdx.x % MT, four = threadIdx.x / MT, n = n0 + four * 4;
+    if (four < RW && m < p.M && n < p.N) {
         typename Op::Acc v[NB];
 #pragma unroll
         for (int q = 0; q < NB; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[q][i] = lds[q][m][i];
-        if constexpr (GATED) done(m, n0, p.N, v[0], v[1]);
-        else done(m, n0, p.N, v[0]);
+            for (int i = 0; i < 4; ++i) v[q][i] = lds[q][m][four * 4 + i];
+        if constexpr (GATED) done(m, n, p.N, v[0], v[1]);
+        else done(m, n, p.N, v[0]);
     }
 }
 
@@ -782,7 +795,7 @@ hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t strea
     const uint64_t bytes = uint64_t(p.k) * Op::kElem;
     const bool al = chunks16(p.a, p.a_pitch, bytes) && chunks16(p.b[0], p.b_pitch, bytes) &&
                     (!GATED || chunks16(p.b[1], p.b_pitch, bytes));
-    const uint32_t groups = p.M <= 4 ? (p.N + 3) / 4 : (p.N + 15) / 16;
+    const uint32_t groups = p.M == 1 ? (p.N + 3) / 4 : p.M <= 4 ? (p.N + 7) / 8 : (p.N + 15) / 16;
     if (p.M == 1) {
         if (al) product_tokens<Op, 1, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
         else product_tokens<Op, 1, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
