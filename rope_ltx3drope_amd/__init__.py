@@ -437,21 +437,25 @@ def _finish(status: int, reason: ctypes.c_int, what: str) -> None:
     _check(status, what)
 
 
-def _operand(t, shape, dtype, device) -> None:
-    """An operand must have this shape, dtype and device and be contiguous."""
+def _operand(t, shape, dtype, device: int) -> None:
+    """An operand must have this shape and dtype, be on the GPU of this index and contiguous."""
     if t.shape != shape:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     if t.dtype != dtype:
         raise Ltx3dRopeUnsupported("DTYPE")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != device or not t.is_cuda:
         raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
     if not t.is_contiguous():
         raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
 
 
+def _raw_stream(device: int, stream) -> int:
+    return _stream_ptr(device, stream) if stream is not None else _torch()._C._cuda_getCurrentRawStream(device)
+
+
 def _rows_marshal(first, others):
     """(batch, rows, dim) of a [batch, rows, dim] or [rows, dim] row tensor; `others` must match it."""
-    shape, dtype, device = first.shape, first.dtype, first.device
+    shape, dtype, device = first.shape, first.dtype, first.get_device()
     if len(shape) != 2 and len(shape) != 3:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     if _dtype_code(first) < 0:
@@ -464,7 +468,7 @@ def _rows_marshal(first, others):
 
 def _vectors_marshal(row, size, weights, per_sample):
     """The code of the vectors' common dtype: the rows' own or float32."""
-    dtype, device, (batch, _, dim) = None, row.device, size
+    dtype, device, (batch, _, dim) = None, row.get_device(), size
     for t in weights:
         if t is not None:
             dtype = dtype or t.dtype
@@ -505,8 +509,9 @@ def _norm(row, size, pd, after, post_norm, next_norm, eps, weight_offset, residu
     reason = ctypes.c_int(0)
     _lib.lib()
     st = _lib.norm(_lib.NORM_BYTES.pack(_dtype_codes[row.dtype], pd, after, post_norm, next_norm, 0, *size, eps,
-                                        weight_offset, residual_scale, *[_ptr(t) for t in tensors]),
-                   _stream_ptr(row.device, stream), ctypes.byref(reason))
+                                        weight_offset, residual_scale,
+                                        *[0 if t is None else t.data_ptr() for t in tensors]),
+                   _raw_stream(row.get_device(), stream), ctypes.byref(reason))
     _finish(st, reason, what)
 
 
@@ -541,9 +546,9 @@ def norm_after(y, residual, weight=None, gate=None, *, post_norm: bool = True, r
     if not next_norm and any(t is not None for t in (next_weight, next_scale, next_shift, n_out)):
         raise ValueError("next_norm=False takes no vector or output of the next norm")
     if r_out is None:
-        r_out = _empty(stream, lambda: _torch().empty_like(y))
+        r_out = _torch().empty_like(y) if stream is None else _empty(stream, lambda: _torch().empty_like(y))
     if next_norm and n_out is None:
-        n_out = _empty(stream, lambda: _torch().empty_like(y))
+        n_out = _torch().empty_like(y) if stream is None else _empty(stream, lambda: _torch().empty_like(y))
     _norm(y, size, pd, 1, bool(post_norm), bool(next_norm), eps, weight_offset, residual_scale, stream, "norm_after",
           y, residual, weight, gate, next_weight, next_scale, next_shift, r_out, n_out)
     return r_out, n_out
@@ -586,7 +591,7 @@ def _norm_backward(row, size, pd, after, post_norm, next_norm, eps, weight_offse
     pack = _lib.NORM_BACKWARD_BYTES.pack
     ws, n = _workspace(stream, _lib.norm_backward_workspace, pack(*head, 0, 0), row.device)
     reason = ctypes.c_int(0)
-    st = _lib.norm_backward(pack(*head, _ptr(ws), n), _stream_ptr(row.device, stream), ctypes.byref(reason))
+    st = _lib.norm_backward(pack(*head, _ptr(ws), n), _raw_stream(row.get_device(), stream), ctypes.byref(reason))
     _finish(st, reason, what)
     return outs
 
@@ -635,16 +640,16 @@ def gated_ffn(x, w_gate, w_up, activation: str = "silu", *, save: bool = False, 
     projections for gated_ffn_backward, in float32 whatever x's dtype."""
     torch = _torch()
     act = _activation(activation)
-    xs, dtype, device = x.shape, x.dtype, x.device
+    xs, dtype, device, index = x.shape, x.dtype, x.device, x.get_device()
     if len(xs) < 1 or w_gate.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim, hidden = xs[-1], w_gate.shape[0]
     shape = xs[:-1] + (hidden,)
-    _operand(x, xs, dtype, device)
-    _operand(w_gate, (hidden, dim), dtype, device)
-    _operand(w_up, (hidden, dim), dtype, device)
+    _operand(x, xs, dtype, index)
+    _operand(w_gate, (hidden, dim), dtype, index)
+    _operand(w_up, (hidden, dim), dtype, index)
     if out is not None:
-        _operand(out, shape, dtype, device)
+        _operand(out, shape, dtype, index)
 
     def outputs():
         h = torch.empty(shape, dtype=dtype, device=device) if out is None else out
@@ -660,7 +665,7 @@ def gated_ffn(x, w_gate, w_up, activation: str = "silu", *, save: bool = False, 
     descriptor = pack(*head, 0, 0)
     ws, n = _workspace(stream, _lib.gated_ffn_workspace, descriptor, device)
     reason = ctypes.c_int(0)
-    st = _lib.gated_ffn(descriptor if ws is None else pack(*head, ws.data_ptr(), n), _stream_ptr(device, stream),
+    st = _lib.gated_ffn(descriptor if ws is None else pack(*head, ws.data_ptr(), n), _raw_stream(index, stream),
                         ctypes.byref(reason))
     _finish(st, reason, "gated_ffn")
     return (h, g, u) if save else h
@@ -672,17 +677,17 @@ def gated_ffn_backward(dh, x, w_gate, w_up, g, u, activation: str = "silu", *, n
     need_dx=False or need_dw=False leaves those out (None)."""
     torch = _torch()
     act = _activation(activation)
-    xs, dtype, device = x.shape, x.dtype, x.device
+    xs, dtype, device, index = x.shape, x.dtype, x.device, x.get_device()
     if len(xs) < 1 or w_gate.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim, hidden = xs[-1], w_gate.shape[0]
     shape = xs[:-1] + (hidden,)
-    _operand(x, xs, dtype, device)
-    _operand(w_gate, (hidden, dim), dtype, device)
-    _operand(w_up, (hidden, dim), dtype, device)
-    _operand(dh, shape, dtype, device)
-    _operand(g, shape, torch.float32, device)
-    _operand(u, shape, torch.float32, device)
+    _operand(x, xs, dtype, index)
+    _operand(w_gate, (hidden, dim), dtype, index)
+    _operand(w_up, (hidden, dim), dtype, index)
+    _operand(dh, shape, dtype, index)
+    _operand(g, shape, torch.float32, index)
+    _operand(u, shape, torch.float32, index)
     dx, dwg, dwu = _empty(stream, lambda: (torch.empty_like(x) if need_dx else None,
                                            torch.empty_like(w_gate) if need_dw else None,
                                            torch.empty_like(w_up) if need_dw else None))
@@ -692,7 +697,7 @@ def gated_ffn_backward(dh, x, w_gate, w_up, g, u, activation: str = "silu", *, n
             *[_ptr(t) for t in (dh, x, w_gate, w_up, g, u, dx, dwg, dwu)])
     ws, n = _workspace(stream, _lib.gated_ffn_backward_workspace, pack(*head, 0, 0), device)
     reason = ctypes.c_int(0)
-    st = _lib.gated_ffn_backward(pack(*head, _ptr(ws), n), _stream_ptr(device, stream), ctypes.byref(reason))
+    st = _lib.gated_ffn_backward(pack(*head, _ptr(ws), n), _raw_stream(index, stream), ctypes.byref(reason))
     _finish(st, reason, "gated_ffn_backward")
     return dx, dwg, dwu
 
@@ -701,22 +706,22 @@ def q8_quantize(x, *, q_out=None, scale_out=None, stream=None):
     """Rows to 8-bit integers: (q int8 like x, scale float32 [...]) with scale = max |row| * (1/127) and
     q = round(x / scale).  x [..., dim], float32 or bfloat16."""
     torch = _torch()
-    xs, device = x.shape, x.device
+    xs, device, index = x.shape, x.device, x.get_device()
     if len(xs) < 1:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    _operand(x, xs, x.dtype, device)
+    _operand(x, xs, x.dtype, index)
     q, scale = q_out, scale_out
     if q is None:
         q = _empty(stream, lambda: torch.empty_like(x, dtype=torch.int8))
     else:
-        _operand(q, xs, torch.int8, device)
+        _operand(q, xs, torch.int8, index)
     if scale is None:
         scale = _empty(stream, lambda: torch.empty(xs[:-1], dtype=torch.float32, device=device))
     else:
-        _operand(scale, xs[:-1], torch.float32, device)
+        _operand(scale, xs[:-1], torch.float32, index)
     reason = ctypes.c_int(0)
     st = _lib.lib().ltx3drope_q8_quantize(_dtype_code(x), scale.numel(), xs[-1], x.data_ptr(), q.data_ptr(),
-                                          scale.data_ptr(), _stream_ptr(device, stream), reason)
+                                          scale.data_ptr(), _raw_stream(index, stream), reason)
     _finish(st, reason, "q8_quantize")
     return q, scale
 
@@ -728,23 +733,23 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
     [out, dim] with b_scale float32 [out] (one a channel); bias float32 [out] or None; dtype of the
     result: bfloat16 (default) or float32."""
     torch = _torch()
-    shape, device = a.shape, a.device
+    shape, device, index = a.shape, a.device, a.get_device()
     if len(shape) < 1 or b.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim, n = shape[-1], b.shape[0]
-    _operand(a, shape, torch.int8, device)
-    _operand(b, (n, dim), torch.int8, device)
-    _operand(a_scale, shape[:-1], torch.float32, device)
-    _operand(b_scale, (n,), torch.float32, device)
+    _operand(a, shape, torch.int8, index)
+    _operand(b, (n, dim), torch.int8, index)
+    _operand(a_scale, shape[:-1], torch.float32, index)
+    _operand(b_scale, (n,), torch.float32, index)
     if bias is not None:
-        _operand(bias, (n,), torch.float32, device)
+        _operand(bias, (n,), torch.float32, index)
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     shape = shape[:-1] + (n,)
     if out is None:
         out = _empty(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
     else:
-        _operand(out, shape, dtype, device)
+        _operand(out, shape, dtype, index)
     _lib.lib()
     pack = _lib.Q8_BYTES.pack
     head = (_dtype_code(out), 0, a_scale.numel(), dim, n, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(),
@@ -752,7 +757,7 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
     descriptor = pack(*head, 0, 0)
     ws, size = _workspace(stream, _lib.q8_matmul_workspace, descriptor, device)
     reason = ctypes.c_int(0)
-    st = _lib.q8_matmul(descriptor if ws is None else pack(*head, ws.data_ptr(), size), _stream_ptr(device, stream),
+    st = _lib.q8_matmul(descriptor if ws is None else pack(*head, ws.data_ptr(), size), _raw_stream(index, stream),
                         ctypes.byref(reason))
     _finish(st, reason, "q8_matmul")
     return out

@@ -95,6 +95,17 @@ __device__ __forceinline__ float get(const void* p, size_t i) {
     if constexpr (F32) return static_cast<const float*>(p)[i];
     else return static_cast<float>(static_cast<const __bf16*>(p)[i]);
 }
+// Eight floats of any alignment that nobody reads again.
+__device__ __forceinline__ void load8(float (&v)[8], const float* p) {
+    typedef float any_f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const any_f32x4*>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * i + k] = q[k];
+    }
+}
+
 // dg and du as rows [M][2 * Fp]: dg, zeros up to Fp, du, zeros.  Eight columns a thread; bound by the
 // bytes (10 read and 4 written an element in bf16).
 template <bool F32>
@@ -107,13 +118,14 @@ __global__ __launch_bounds__(256) void ffn_slopes(const void* dh, const float* g
         const size_t at = static_cast<size_t>(r) * F + c;
         float vg[8] = {}, vu[8] = {}, d[8] = {};
         if (c + 8 <= F) {
-            __builtin_memcpy(vg, g + at, 32);
-            __builtin_memcpy(vu, u + at, 32);
+            load8(vg, g + at);
+            load8(vu, u + at);
             if constexpr (F32) {
-                __builtin_memcpy(d, static_cast<const float*>(dh) + at, 32);
+                load8(d, static_cast<const float*>(dh) + at);
             } else {
-                bf16x8 h;
-                __builtin_memcpy(&h, static_cast<const __bf16*>(dh) + at, 16);
+                typedef __bf16 any_bf16x8 __attribute__((ext_vector_type(8), aligned(2)));
+                const bf16x8 h = __builtin_nontemporal_load(
+                    reinterpret_cast<const any_bf16x8*>(static_cast<const __bf16*>(dh) + at));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[i] = static_cast<float>(h[i]);
             }
