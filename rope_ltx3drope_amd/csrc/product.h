@@ -294,20 +294,25 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
     };
     // a step past this workgroup's last one brings zeros without touching memory
     const uint32_t k_end = last * kRowBytes < p.k * Op::kElem ? last * kRowBytes : p.k * Op::kElem;
-    auto fetch_a = [&](uint32_t step, uint32_t slot) {
+    auto aim_a = [&](uint32_t step) {
         const uint32_t k = step * kRowBytes;
         if constexpr (A_OUTER) {
             const uint32_t k0 = step * kStepK;
             const uint32_t rows = step >= last ? 0 : (p.k - k0 < kStepK ? p.k - k0 : kStepK);
             ra = buffer_of(p.a + k0 * p.a_pitch + m0 * Op::kElem, p.a_pitch, rows, (p.M - m0) * Op::kElem);
         }
-#pragma unroll
-        for (int i = 0; i < CA; ++i) {
-            const bool past = !A_OUTER && k + byte_a[i] >= k_end;
-            lds_copy16(ra, lds + slot * SA::kBytes + (i * NW + wave) * 1024, past ? kOutOfRange : va[i], A_OUTER ? 0 : k);
-        }
+        return k;
     };
-    auto fetch_b = [&](uint32_t step, uint32_t slot) {
+    auto copy_a = [&](uint32_t k, uint32_t slot, int i) {
+        const bool past = !A_OUTER && k + byte_a[i] >= k_end;
+        lds_copy16(ra, lds + slot * SA::kBytes + (i * NW + wave) * 1024, past ? kOutOfRange : va[i], A_OUTER ? 0 : k);
+    };
+    auto fetch_a = [&](uint32_t step, uint32_t slot) {
+        const uint32_t k = aim_a(step);
+#pragma unroll
+        for (int i = 0; i < CA; ++i) copy_a(k, slot, i);
+    };
+    auto aim_b = [&](uint32_t step) {
         const uint32_t k = step * kRowBytes;
         if constexpr (B_OUTER) {
             uint32_t k0, rows;
@@ -315,12 +320,17 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
             rb0 = buffer_of(base + k0 * p.b_pitch + n0 * Op::kElem, p.b_pitch, step >= last ? 0 : rows,
                             (p.N - n0) * Op::kElem);
         }
+        return k;
+    };
+    auto copy_b = [&](uint32_t k, uint32_t slot, int i) {
+        const bool past = !B_OUTER && k + byte_b[i] >= k_end;
+        lds_copy16(GATED && i >= CB / 2 ? rb1 : rb0, lds + kAtB + slot * kBytesB + (i * NW + wave) * 1024,
+                   past ? kOutOfRange : vb[i], B_OUTER ? 0 : k);
+    };
+    auto fetch_b = [&](uint32_t step, uint32_t slot) {
+        const uint32_t k = aim_b(step);
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            const bool past = !B_OUTER && k + byte_b[i] >= k_end;
-            lds_copy16(GATED && i >= CB / 2 ? rb1 : rb0, lds + kAtB + slot * kBytesB + (i * NW + wave) * 1024,
-                       past ? kOutOfRange : vb[i], B_OUTER ? 0 : k);
-        }
+        for (int i = 0; i < CB; ++i) copy_b(k, slot, i);
     };
     u32x4 held[DIRECT ? 1 : CA + CB];
     auto hold = [&](uint32_t step) {
@@ -387,18 +397,19 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
         for (int kk = 0; kk < 2; ++kk) base_b[kk] = kAtB + SB::lane_base(lane, kk);
     }
     u32x4 fa[2][FM], fb[2][FN];
+    // operand block n of a half step: B's blocks, then A's
+    auto read_one = [&](const char* at_a, const char* at_b, int kk, int n) {
+        if (n < FN) {
+            if constexpr (B_OUTER) fb[kk][n] = SB::outer_frag(at_b, base_b[n], kk);
+            else fb[kk][n] = *reinterpret_cast<const u32x4*>(at_b + base_b[kk] + b_block(n) * 16 * kRowBytes);
+        } else {
+            if constexpr (A_OUTER) fa[kk][n - FN] = SA::outer_frag(at_a, base_a[n - FN], kk);
+            else fa[kk][n - FN] = *reinterpret_cast<const u32x4*>(at_a + base_a[kk] + (n - FN) * 16 * kRowBytes);
+        }
+    };
     auto read = [&](uint32_t slot_a, uint32_t slot_b, int kk) {
-        const char *at_a = lds + slot_a * SA::kBytes, *at_b = lds + slot_b * kBytesB;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            if constexpr (B_OUTER) fb[kk][j] = SB::outer_frag(at_b, base_b[j], kk);
-            else fb[kk][j] = *reinterpret_cast<const u32x4*>(at_b + base_b[kk] + b_block(j) * 16 * kRowBytes);
-        }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            if constexpr (A_OUTER) fa[kk][i] = SA::outer_frag(at_a, base_a[i], kk);
-            else fa[kk][i] = *reinterpret_cast<const u32x4*>(at_a + base_a[kk] + i * 16 * kRowBytes);
-        }
+        for (int n = 0; n < FN + FM; ++n) read_one(lds + slot_a * SA::kBytes, lds + slot_b * kBytesB, kk, n);
     };
     auto multiply = [&](int kk) {
 #pragma unroll
@@ -406,15 +417,19 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
 #pragma unroll
             for (int j = 0; j < FN; ++j) Op::mac(acc[i][j], fb[kk][j], fa[kk][i]);
     };
-    // a few LDS reads, a few products, and so on, instead of all of one and then all of the other
-    auto interleave = [&]() {
-        constexpr int reads = (FM * (A_OUTER ? (Op::kElem == 4 ? 4 : 2) : 1) + FN * (B_OUTER ? (Op::kElem == 4 ? 4 : 2) : 1));
-        constexpr int macs = FM * FN * (Op::kElem == 4 ? 4 : 1);
-        constexpr int per = macs / reads > 0 ? macs / reads : 1;
+    // One row of blocks is multiplied while some of the operands of half step kk of the given slots are
+    // read; `between` says what else goes there.  Pinned in this order: left alone, the compiler puts all
+    // reads (and copies) first, and the matrix cores wait for them.
+    auto multiply_and_read = [&](int kk, uint32_t slot_a, uint32_t slot_b, auto between) {
+        const char *at_a = lds + slot_a * SA::kBytes, *at_b = lds + slot_b * kBytesB;
 #pragma unroll
-        for (int r = 0; r < reads; ++r) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, per, 0);
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int n = i * (FN + FM) / FM; n < (i + 1) * (FN + FM) / FM; ++n) read_one(at_a, at_b, kk ^ 1, n);
+            between(i);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) Op::mac(acc[i][j], fb[kk][j], fa[kk][i]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
@@ -433,15 +448,18 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
         uint32_t sa = 0, sb = 0;  // the step's slots
         for (uint32_t s = first; s + 1 < last; ++s) {
             const uint32_t next = sa == 2 ? 0 : sa + 1;
-            read(sa, sb, 1);
-            multiply(0);
-            interleave();
+            __builtin_amdgcn_s_setprio(1);  // whoever still multiplies goes first
+            multiply_and_read(0, sa, sb, [](int) {});
+            __builtin_amdgcn_s_setprio(0);
             wait_and_meet<CA>();  // all but A's copies for the step after the next
-            fetch_b(s + 2, sb);
-            fetch_a(s + 3, sa);
-            read(next, sb ^ 1, 0);
-            multiply(1);
-            interleave();
+            const uint32_t kb = aim_b(s + 2), ka = aim_a(s + 3);
+            multiply_and_read(1, next, sb ^ 1, [&](int i) {
+#pragma unroll
+                for (int c = i * (CA + CB) / FM; c < (i + 1) * (CA + CB) / FM; ++c) {
+                    if (c < CB) copy_b(kb, sb, c);
+                    else copy_a(ka, sa, c - CB);
+                }
+            });
             sa = next;
             sb ^= 1;
         }
@@ -760,15 +778,15 @@ inline bool chunks16(const void* p, uint64_t pitch, uint64_t row_bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | pitch | row_bytes) & 15) == 0;
 }
 
-template <class Op, int BM, int BN, int WM, bool PIPELINED, bool GATED, bool A_OUTER, bool B_OUTER, bool DIRECT,
-          class Done>
+template <class Op, int BM, int BN, int WM, int WN, bool PIPELINED, bool GATED, bool A_OUTER, bool B_OUTER,
+          bool DIRECT, class Done>
 inline hipError_t launch_tiles(const Product& p, const Plan& plan, const Done& done, hipStream_t stream) {
-    constexpr int threads = WM * 2 * 64;
-    product_tiles<Op, BM, BN, WM, 2, PIPELINED, GATED, A_OUTER, B_OUTER, DIRECT, Done>
+    constexpr int threads = WM * WN * 64;
+    product_tiles<Op, BM, BN, WM, WN, PIPELINED, GATED, A_OUTER, B_OUTER, DIRECT, Done>
         <<<plan.tiles * p.splits, threads, 0, stream>>>(p, done);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    product_join<Op, BM, BN, WM, 2, GATED, Done><<<plan.tiles * (BM / WM / 16), threads, 0, stream>>>(p, done);
+    product_join<Op, BM, BN, WM, WN, GATED, Done><<<plan.tiles * (BM / WM / 16), threads, 0, stream>>>(p, done);
     return hipGetLastError();
 }
 
@@ -779,15 +797,15 @@ hipError_t launch_product(Product p, bool direct, void* workspace, const Done& d
     p.partial = static_cast<float*>(workspace);
     if constexpr (Op::kElem != 4) {
         if (plan.bn == 256)
-            return launch_tiles<Op, 256, 256, 4, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+            return launch_tiles<Op, 256, 256, 2, 4, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
         if (plan.bn == 128)
-            return launch_tiles<Op, 256, 128, 4, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+            return launch_tiles<Op, 256, 128, 4, 2, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
     }
     if (plan.bm == 128)
-        return direct ? launch_tiles<Op, 128, 64, 2, false, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
-                      : launch_tiles<Op, 128, 64, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
-    return direct ? launch_tiles<Op, 64, 64, 2, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
-                  : launch_tiles<Op, 64, 64, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+        return direct ? launch_tiles<Op, 128, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+                      : launch_tiles<Op, 128, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
+    return direct ? launch_tiles<Op, 64, 64, 2, 2, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+                  : launch_tiles<Op, 64, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
 }
 
 template <class Op, bool GATED, class Done>
