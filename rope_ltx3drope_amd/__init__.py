@@ -437,15 +437,19 @@ def _finish(status: int, reason: ctypes.c_int, what: str) -> None:
     _check(status, what)
 
 
-def _operand(t, shape, dtype, device: int) -> None:
-    """An operand must have this shape and dtype, be on the GPU of this index and contiguous."""
-    if t.shape != shape:
-        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    if t.dtype != dtype:
-        raise Ltx3dRopeUnsupported("DTYPE")
-    if t.get_device() != device or not t.is_cuda:
-        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
-    if not t.is_contiguous():
+def _operands(device: int, *operands) -> None:
+    """Each (tensor, shape, dtype) must be as stated, on the GPU of this index and contiguous."""
+    for t, shape, dtype in operands:
+        if t is None:
+            continue
+        if t.shape == shape and t.dtype == dtype and t.get_device() == device >= 0 and t.is_contiguous():
+            continue
+        if t.shape != shape:
+            raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+        if t.dtype != dtype:
+            raise Ltx3dRopeUnsupported("DTYPE")
+        if t.get_device() != device or device < 0:
+            raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
         raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
 
 
@@ -460,9 +464,7 @@ def _rows_marshal(first, others):
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     if _dtype_code(first) < 0:
         raise Ltx3dRopeUnsupported("DTYPE")
-    for t in (first,) + others:
-        if t is not None:
-            _operand(t, shape, dtype, device)
+    _operands(device, (first, shape, dtype), *[(t, shape, dtype) for t in others if t is not None])
     return (1, shape[0], shape[1]) if len(shape) == 2 else tuple(shape)
 
 
@@ -472,12 +474,12 @@ def _vectors_marshal(row, size, weights, per_sample):
     for t in weights:
         if t is not None:
             dtype = dtype or t.dtype
-            _operand(t, (dim,), dtype, device)
+            _operands(device, (t, (dim,), dtype))
     for t in per_sample:
         if t is not None:
             dtype = dtype or t.dtype
             flat = batch == 1 and t.dim() == 1 and row.dim() == 2
-            _operand(t, (dim,) if flat else (batch, dim), dtype, device)
+            _operands(device, (t, (dim,) if flat else (batch, dim), dtype))
     code = _dtype_codes.get(dtype or row.dtype, -1)
     if code < 0:
         raise Ltx3dRopeUnsupported("DTYPE")
@@ -645,19 +647,13 @@ def gated_ffn(x, w_gate, w_up, activation: str = "silu", *, save: bool = False, 
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim, hidden = xs[-1], w_gate.shape[0]
     shape = xs[:-1] + (hidden,)
-    _operand(x, xs, dtype, index)
-    _operand(w_gate, (hidden, dim), dtype, index)
-    _operand(w_up, (hidden, dim), dtype, index)
-    if out is not None:
-        _operand(out, shape, dtype, index)
-
-    def outputs():
-        h = torch.empty(shape, dtype=dtype, device=device) if out is None else out
-        if not save:
-            return h, None, None
-        return h, *(torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2))
-
-    h, g, u = _empty(stream, outputs)
+    weight = (hidden, dim)
+    _operands(index, (x, xs, dtype), (w_gate, weight, dtype), (w_up, weight, dtype), (out, shape, dtype))
+    h, g, u = out, None, None
+    if h is None:
+        h = x.new_empty(shape) if stream is None else _empty(stream, lambda: x.new_empty(shape))
+    if save:
+        g, u = _empty(stream, lambda: [torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2)])
     _lib.lib()
     pack = _lib.FFN_BYTES.pack
     head = (_dtype_code(x), act, x.numel() // dim if dim else 0, dim, hidden, x.data_ptr(), w_gate.data_ptr(),
@@ -682,12 +678,9 @@ def gated_ffn_backward(dh, x, w_gate, w_up, g, u, activation: str = "silu", *, n
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim, hidden = xs[-1], w_gate.shape[0]
     shape = xs[:-1] + (hidden,)
-    _operand(x, xs, dtype, index)
-    _operand(w_gate, (hidden, dim), dtype, index)
-    _operand(w_up, (hidden, dim), dtype, index)
-    _operand(dh, shape, dtype, index)
-    _operand(g, shape, torch.float32, index)
-    _operand(u, shape, torch.float32, index)
+    weight = (hidden, dim)
+    _operands(index, (x, xs, dtype), (w_gate, weight, dtype), (w_up, weight, dtype), (dh, shape, dtype),
+              (g, shape, torch.float32), (u, shape, torch.float32))
     dx, dwg, dwu = _empty(stream, lambda: (torch.empty_like(x) if need_dx else None,
                                            torch.empty_like(w_gate) if need_dw else None,
                                            torch.empty_like(w_up) if need_dw else None))
@@ -706,19 +699,17 @@ def q8_quantize(x, *, q_out=None, scale_out=None, stream=None):
     """Rows to 8-bit integers: (q int8 like x, scale float32 [...]) with scale = max |row| * (1/127) and
     q = round(x / scale).  x [..., dim], float32 or bfloat16."""
     torch = _torch()
-    xs, device, index = x.shape, x.device, x.get_device()
+    xs, index = x.shape, x.get_device()
     if len(xs) < 1:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
-    _operand(x, xs, x.dtype, index)
-    q, scale = q_out, scale_out
-    if q is None:
-        q = _empty(stream, lambda: torch.empty_like(x, dtype=torch.int8))
-    else:
-        _operand(q, xs, torch.int8, index)
-    if scale is None:
-        scale = _empty(stream, lambda: torch.empty(xs[:-1], dtype=torch.float32, device=device))
-    else:
-        _operand(scale, xs[:-1], torch.float32, index)
+    rows = xs[:-1]
+    _operands(index, (x, xs, x.dtype), (q_out, xs, torch.int8), (scale_out, rows, torch.float32))
+
+    def outputs():
+        return (torch.empty_like(x, dtype=torch.int8) if q_out is None else q_out,
+                x.new_empty(rows, dtype=torch.float32) if scale_out is None else scale_out)
+
+    q, scale = outputs() if stream is None else _empty(stream, outputs)
     reason = ctypes.c_int(0)
     st = _lib.lib().ltx3drope_q8_quantize(_dtype_code(x), scale.numel(), xs[-1], x.data_ptr(), q.data_ptr(),
                                           scale.data_ptr(), _raw_stream(index, stream), reason)
@@ -737,19 +728,15 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
     if len(shape) < 1 or b.dim() != 2:
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim, n = shape[-1], b.shape[0]
-    _operand(a, shape, torch.int8, index)
-    _operand(b, (n, dim), torch.int8, index)
-    _operand(a_scale, shape[:-1], torch.float32, index)
-    _operand(b_scale, (n,), torch.float32, index)
-    if bias is not None:
-        _operand(bias, (n,), torch.float32, index)
+    rows, channels = shape[:-1], (n,)
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
-    shape = shape[:-1] + (n,)
+    _operands(index, (a, shape, torch.int8), (b, (n, dim), torch.int8), (a_scale, rows, torch.float32),
+              (b_scale, channels, torch.float32), (bias, channels, torch.float32), (out, rows + channels, dtype))
     if out is None:
-        out = _empty(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
-    else:
-        _operand(out, shape, dtype, index)
+        shape = rows + channels
+        out = (a_scale.new_empty(shape, dtype=dtype) if stream is None
+               else _empty(stream, lambda: a_scale.new_empty(shape, dtype=dtype)))
     _lib.lib()
     pack = _lib.Q8_BYTES.pack
     head = (_dtype_code(out), 0, a_scale.numel(), dim, n, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(),

@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace ltx3drope {
 
@@ -131,25 +132,49 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// 16 bytes of a row from byte k on; what lies past `end` is zero.  Without alignment the last chunk is
-// read one element at a time.  STREAM: nobody reads these bytes again soon.
+// v without its first d bytes, moved down, zeros behind.
+__device__ __forceinline__ u32x4 drop_bytes(u32x4 v, uint32_t d) {
+    const uint32_t n = d < 16 ? d : 16;
+    uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+    const uint32_t bits = (n & 7) * 8;
+    if (n >= 8) {
+        lo = hi;
+        hi = 0;
+    }
+    lo = bits ? lo >> bits | hi << (64 - bits) : lo;
+    hi >>= bits;
+    if (n == 16) lo = 0;
+    return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                 static_cast<uint32_t>(hi >> 32)};
+}
+
+// This wavefront's LDS reads and writes are done, and so are every other wavefront's; loads on their way
+// into registers stay there.
+__device__ __forceinline__ void wait_for_lds_and_meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// 16 bytes of a row from byte k on; what lies past `end` is zero.  Without alignment a chunk that reaches
+// past the end is read from the row's last 16 bytes, so that every lane makes one load; only rows
+// shorter than that are read one element at a time.  STREAM: nobody reads these bytes again soon.
 template <class Op, bool ALIGNED, bool STREAM>
 __device__ __forceinline__ u32x4 load_chunk(const char* row, uint32_t k, uint32_t end) {
     u32x4 v = {0, 0, 0, 0};
     if constexpr (ALIGNED) {
         const u32x4* at = reinterpret_cast<const u32x4*>(row + k);
         if (k < end) v = STREAM ? __builtin_nontemporal_load(at) : *at;
+    } else if (end >= 16) {
+        typedef u32x4 any_u32x4 __attribute__((aligned(1)));
+        const uint32_t at = k + 16 <= end ? k : end - 16;
+        v = *reinterpret_cast<const any_u32x4*>(row + at);
+        if (k != at) v = drop_bytes(v, k - at);
     } else {
-        if (k + 16 <= end) {
-            __builtin_memcpy(&v, row + k, 16);
-        } else if (k < end) {
-            for (uint32_t i = 0; i < end - k; i += Op::kElem) {
-                uint32_t e = 0;
-                __builtin_memcpy(&e, row + k + i, Op::kElem);
+        for (uint32_t i = 0; k + i < end; i += Op::kElem) {
+            uint32_t e = 0;
+            __builtin_memcpy(&e, row + k + i, Op::kElem);
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (i / 4 == static_cast<uint32_t>(w)) v[w] |= e << (8 * (i % 4));
-            }
+            for (int w = 0; w < 4; ++w)
+                if (i / 4 == static_cast<uint32_t>(w)) v[w] |= e << (8 * (i % 4));
         }
     }
     return v;
@@ -332,46 +357,52 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
 #pragma unroll
         for (int i = 0; i < CB; ++i) copy_b(k, slot, i);
     };
-    u32x4 held[DIRECT ? 1 : CA + CB];
-    auto hold = [&](uint32_t step) {
+    struct Held {
+        u32x4 v[DIRECT ? 1 : CA + CB];
+    };
+    // rows past the output's end repeat the last one (their sums are dropped); rows of k past the end are zero
+    auto hold = [&](Held& to, uint32_t step) {
         if constexpr (!DIRECT) {
+            const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < CA; ++i) {
-                held[i] = u32x4{0, 0, 0, 0};
                 if constexpr (A_OUTER) {
-                    const uint32_t k = step * kStepK + line_a[i];
-                    if (k < p.k)
-                        held[i] = load_chunk<Op, false, false>(p.a + k * p.a_pitch, m0 * Op::kElem + byte_a[i], p.M * Op::kElem);
-                } else if (m0 + line_a[i] < p.M) {
-                    held[i] = load_chunk<Op, false, false>(p.a + (m0 + line_a[i]) * p.a_pitch, step * kRowBytes + byte_a[i],
-                                                    p.k * Op::kElem);
+                    const uint32_t k = step * kStepK + line_a[i], last_k = p.k - 1;
+                    to.v[i] = load_chunk<Op, false, false>(p.a + (k < last_k ? k : last_k) * p.a_pitch,
+                                                           m0 * Op::kElem + byte_a[i], p.M * Op::kElem);
+                    if (k > last_k) to.v[i] = zero;
+                } else {
+                    const uint32_t m = m0 + line_a[i] < p.M ? m0 + line_a[i] : p.M - 1;
+                    to.v[i] = load_chunk<Op, false, false>(p.a + m * p.a_pitch, step * kRowBytes + byte_a[i],
+                                                           p.k * Op::kElem);
                 }
             }
 #pragma unroll
             for (int i = 0; i < CB; ++i) {
-                u32x4& h = held[CA + i];
-                h = u32x4{0, 0, 0, 0};
+                u32x4& h = to.v[CA + i];
                 if constexpr (B_OUTER) {
                     uint32_t k0, rows;
                     const char* base = b_segment(step, k0, rows);
-                    if (line_b[i] < rows)
-                        h = load_chunk<Op, false, false>(base + (k0 + line_b[i]) * p.b_pitch, n0 * Op::kElem + byte_b[i],
-                                                  p.N * Op::kElem);
-                } else if (n0 + line_b[i] < p.N) {
-                    h = load_chunk<Op, false, false>(p.b[GATED && i >= CB / 2] + (n0 + line_b[i]) * p.b_pitch,
-                                              step * kRowBytes + byte_b[i], p.k * Op::kElem);
+                    const uint32_t row = rows == 0 ? 0 : k0 + (line_b[i] < rows ? line_b[i] : rows - 1);
+                    h = load_chunk<Op, false, false>(base + row * p.b_pitch, n0 * Op::kElem + byte_b[i],
+                                                     p.N * Op::kElem);
+                    if (line_b[i] >= rows) h = zero;
+                } else {
+                    const uint32_t n = n0 + line_b[i] < p.N ? n0 + line_b[i] : p.N - 1;
+                    h = load_chunk<Op, false, false>(p.b[GATED && i >= CB / 2] + n * p.b_pitch,
+                                                     step * kRowBytes + byte_b[i], p.k * Op::kElem);
                 }
             }
         }
     };
-    auto put_held = [&](uint32_t slot) {
+    auto put_held = [&](const Held& from, uint32_t slot) {
         if constexpr (!DIRECT) {
             char* at = lds + wave * 1024 + lane * 16;
 #pragma unroll
-            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(at + slot * SA::kBytes + i * NW * 1024) = held[i];
+            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(at + slot * SA::kBytes + i * NW * 1024) = from.v[i];
 #pragma unroll
             for (int i = 0; i < CB; ++i)
-                *reinterpret_cast<u32x4*>(at + kAtB + slot * kBytesB + i * NW * 1024) = held[CA + i];
+                *reinterpret_cast<u32x4*>(at + kAtB + slot * kBytesB + i * NW * 1024) = from.v[CA + i];
         }
     };
 
@@ -485,17 +516,24 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
             }
         }
     } else {
-        hold(first);
-        put_held(0);
-        for (uint32_t s = first; s < last; ++s) {
+        // two steps ahead in registers: a load has two steps' time to arrive
+        Held even, odd;
+        auto turn = [&](uint32_t s, Held& next, Held& after) {
             const uint32_t slot = (s - first) & 1;
-            wait_and_meet<0>();
-            if (s + 1 < last) hold(s + 1);
+            wait_for_lds_and_meet();
+            if (s + 2 < last) hold(after, s + 2);
             read(slot, slot, 0);
             read(slot, slot, 1);
             multiply(0);
             multiply(1);
-            if (s + 1 < last) put_held(slot ^ 1);
+            if (s + 1 < last) put_held(next, slot ^ 1);
+        };
+        hold(even, first);
+        if (first + 1 < last) hold(odd, first + 1);
+        put_held(even, 0);
+        for (uint32_t s = first; s < last; s += 2) {
+            turn(s, odd, even);
+            if (s + 1 < last) turn(s + 1, even, odd);
         }
     }
 
@@ -673,28 +711,19 @@ __global__ __launch_bounds__(512) void product_rows(Product p, Done done) {
 // Four consecutive outputs from column n on, those below N, in fp32 or rounded once to bf16.
 template <bool F32>
 __device__ __forceinline__ void store4(void* row, uint32_t n, uint32_t N, f32x4 v) {
-    if constexpr (F32) {
-        float* o = static_cast<float*>(row) + n;
-        if (n + 4 <= N) {
-            __builtin_memcpy(o, &v, 16);
-        } else {
-            for (int i = 0; i < 4; ++i)
-                if (n + i < N) o[i] = v[i];
-        }
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    using Elem = typename std::conditional<F32, float, __bf16>::type;
+    using Four = typename std::conditional<F32, f32x4, bf16x4>::type;
+    typedef Four AnyFour __attribute__((aligned(F32 ? 4 : 2)));
+    const Four b = __builtin_convertvector(v, Four);
+    Elem* o = static_cast<Elem*>(row) + n;
+    if (n + 4 <= N) {
+        *reinterpret_cast<AnyFour*>(o) = b;
     } else {
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        const bf16x4 b = __builtin_convertvector(v, bf16x4);
-        __bf16* o = static_cast<__bf16*>(row) + n;
-        if (n + 4 <= N) {
-            __builtin_memcpy(o, &b, 8);
-        } else {
-            for (int i = 0; i < 4; ++i)
-                if (n + i < N) o[i] = b[i];
-        }
+        for (int i = 0; i < 4; ++i)
+            if (n + i < N) o[i] = b[i];
     }
 }
-
-inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 constexpr uint32_t kFewRows = 16;  // most rows of A that the kernels without tiles take
 
@@ -743,6 +772,7 @@ inline constexpr TileCost kTileCosts<OpF32>[4] = {
     {64, 64, 0.6f, 0.49f, 1.0f, 1.0f, 0.8f},
 };
 
+// (through registers a step takes 0.9 us with tiles of 64 on a nearly empty chip).
 // The tile and split with the least time by these costs.  pitch: bytes from row to row of B.  Splitting adds the sums' way through memory
 // and a launch; every part keeps 4 steps of k.
 template <class Op, bool GATED, bool OUTER>
@@ -760,7 +790,7 @@ inline Plan plan_product(uint32_t M, uint32_t N, uint32_t k, bool direct, uint64
             if (splits > 1 && (steps / splits < 4 || tiles >= 2 * units)) break;
             const float depth = static_cast<float>((steps + splits - 1) / splits);
             const float rounds = static_cast<float>((tiles * splits + units - 1) / units);
-            const float one = depth * c.alone + c.ends, many = rounds * (depth * full + c.ends);
+            const float one = depth * c.alone * (direct ? 1.f : 2.2f) + c.ends, many = rounds * (depth * full + c.ends);
             float us = one > many ? one : many;
             const size_t bytes = splits > 1 ? size_t(splits) * tiles * c.bm * c.bn * 4 : 0;
             if (splits > 1) us += 2.f + static_cast<float>(bytes) * 2 / 5e6f;
