@@ -1,7 +1,8 @@
-// Matrix products C[m][n] = sum_k A[m][k] * B[n][k] on the matrix cores (device code; both operands
-// row-major with k innermost), with a functor for what happens to a finished tile.
+// Matrix products C[m][n] = sum_k A[m][k] * B[n][k] with a functor for what happens to finished sums:
+// product_tiles on the matrix cores for many rows of A, product_rows for up to 16, product_tokens for up
+// to 4.  Kernels, and the rules that choose among them.
 //
-// The products treat a row of k as bytes: a 16-byte chunk holds 8 bf16, 16 int8 or 4 fp32 numbers,
+// The matrix cores' products treat a row of k as bytes: a 16-byte chunk holds 8 bf16, 16 int8 or 4 fp32 numbers,
 // and one step of a wavefront multiplies 16 rows of A by 16 rows of B over 4 chunks.  Lane l holds
 // chunk l / 16 of row l % 16 of either operand.  The order of k inside a step is the same on both
 // sides, so any order gives the same sum of products.  B goes in as the instruction's first operand
@@ -27,7 +28,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 struct OpBf16 {
     using Acc = f32x4;
     using Sum = float;
-    static constexpr int kElem = 2;
+    static constexpr int kElem = 2, kTokens = 4;  // most rows of A for product_tokens
     static __device__ __forceinline__ void mac(Acc& c, u32x4 b, u32x4 a) {
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0,
                                                     0, 0);
@@ -46,7 +47,7 @@ struct OpBf16 {
 struct OpI8 {
     using Acc = i32x4;
     using Sum = int;
-    static constexpr int kElem = 1;
+    static constexpr int kElem = 1, kTokens = 1;
     static __device__ __forceinline__ void mac(Acc& c, u32x4 b, u32x4 a) {
         c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), c, 0, 0,
                                                   0);
@@ -61,7 +62,7 @@ struct OpI8 {
 struct OpF32 {
     using Acc = f32x4;
     using Sum = float;
-    static constexpr int kElem = 4;
+    static constexpr int kElem = 4, kTokens = 8;
     static __device__ __forceinline__ void mac(Acc& c, u32x4 b, u32x4 a) {
         const f32x4 fb = __builtin_bit_cast(f32x4, b), fa = __builtin_bit_cast(f32x4, a);
 #pragma unroll
@@ -75,7 +76,7 @@ struct OpF32 {
 };
 
 // One product, C[m][n] = sum_k A[m][k] * B[n][k].  An operand is stored with k innermost (rows of the
-// output's index, k_bytes bytes of k each) or with k outermost (rows of k, the output's index along
+// output's index, the k of one after the other) or with k outermost (rows of k, the output's index along
 // them).  Sizes are 32-bit; the host keeps what a tile addresses (256 rows of an operand with k
 // innermost, 64 of one with k outermost) within 2^31 bytes.
 struct Product {
@@ -116,9 +117,9 @@ __device__ __forceinline__ u32x4 buffer_of(const char* base, uint64_t pitch, uin
 
 // Sends 16 bytes a lane from the buffer to LDS, lane l's to lds + 16 * l.  The instruction is written out
 // because the compiler, which cannot tell which LDS bytes a builtin copy fills, waits for all copies
-// before every turning read of another slot (4096 x 2048 x 16384 with k outermost: 308 us with the
-// builtin).  It leaves no register behind but m0, which
-// nothing else in these kernels uses; its arrival is awaited by wait_and_meet.
+// before every turning read of another slot (16384 x 2048, k 4096 outermost on both sides: 308 us with
+// the builtin, 252 so).  It leaves no register behind but m0, which nothing else in these kernels uses;
+// its arrival is awaited by wait_and_meet.
 __device__ __forceinline__ void lds_copy16(u32x4 buffer, char* lds, uint32_t voffset, uint32_t soffset) {
     const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voffset),
@@ -256,8 +257,8 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
     using SB = Side<Op, BNB, B_OUTER>;
     // LDS: rings of kSlotsA steps of A and 2 of B (160 KB for 256 x 256: all there is).  The copies have a
     // step's time to land at the least; with the third slot A's have two, and half as many bytes again
-    // are on their way at any time, which is what the copies' rate goes by (4096 x 16384 x 2048 in bf16:
-    // see the launch rule for both).
+    // are on their way at any time, which is what the copies' rate goes by (8192 x 8192 x 8192 in bf16:
+    // 887 us with two slots each, 848 so; copies alone 743, and 587 with two whole steps on their way).
     constexpr int kSlotsA = PIPELINED ? 3 : 2, kStepK = SA::kStepK;
     constexpr int kBytesB = BN * kRowBytes, kAtB = kSlotsA * SA::kBytes;
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies a wavefront makes of each operand
@@ -597,14 +598,17 @@ __device__ __forceinline__ T lanes_sum(T v) {
     return v;
 }
 
-// One to four rows of A: a wavefront takes one row of B (of each B; two for more than one row of A, so
-// that they share its loads), its lanes along k, 4 KB of it at a
-// time, and multiplies it by every row of A in registers.  Bound by the bytes of B, which it reads in
-// whole kilobytes: 2 x 10240 rows of 4096 bf16 in 25 us (6.7 TB/s), where the matrix cores' layout, 16
-// rows a load, takes 37.  The four wavefronts of a workgroup put their sums side by side for `done`.
+// A few rows of A (bf16 1 to 4, fp32 1 to 8, int8 one: Op::kTokens): a wavefront takes one row of B (of
+// each B; two for more than one row of A, so that they share its loads), its lanes along k, some KB of it
+// at a time, and multiplies it by every row of A in registers.  Bound by the bytes of B, which it reads
+// in whole kilobytes.  2 x 10240 rows of 4096 bf16: 26 us for one row of A (6.4 TB/s), 35 for four; the
+// matrix cores' layout, 16 rows of B a load (product_rows), takes 37 and 40, and 41 against 50 for eight.
+// fp32: 51, 58 for four and 73 for eight, against 91 for nine there.  int8, 4096 rows of 10240: 10 us
+// for any number up to eight there.  The four wavefronts of a workgroup put their sums side by side for
+// `done`.
 template <class Op, int MT, bool GATED, bool ALIGNED, class Done>
 __global__ __launch_bounds__(256) void product_tokens(Product p, Done done) {
-    constexpr int NB = GATED ? 2 : 1, KV = 4, RW = MT > 1 ? 2 : 1;  // rows of B a wavefront
+    constexpr int NB = GATED ? 2 : 1, KV = MT > 4 ? 2 : 4, RW = MT > 1 ? 2 : 1;  // rows of B a wavefront
     using Sum = typename Op::Sum;
     __shared__ Sum lds[NB][MT][4 * RW];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -663,7 +667,7 @@ __global__ __launch_bounds__(256) void product_tokens(Product p, Done done) {
     }
 }
 
-// Up to 16 rows of A: B is read once, straight into registers, 16 of its rows a workgroup, and the
+// Up to 16 rows of A, where product_tokens is not better: B is read once, straight into registers, 16 of its rows a workgroup, and the
 // wavefronts of a workgroup share out k.  Their sums meet in LDS.  Bound by the bytes of B.
 template <class Op, bool GATED, bool ALIGNED, class Done>
 __global__ __launch_bounds__(512) void product_rows(Product p, Done done) {
@@ -843,14 +847,23 @@ hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t strea
     const uint64_t bytes = uint64_t(p.k) * Op::kElem;
     const bool al = chunks16(p.a, p.a_pitch, bytes) && chunks16(p.b[0], p.b_pitch, bytes) &&
                     (!GATED || chunks16(p.b[1], p.b_pitch, bytes));
-    const uint32_t groups = p.M == 1 ? (p.N + 3) / 4 : p.M <= 4 ? (p.N + 7) / 8 : (p.N + 15) / 16;
     if (p.M == 1) {
+        const uint32_t groups = (p.N + 3) / 4;
         if (al) product_tokens<Op, 1, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
         else product_tokens<Op, 1, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
-    } else if (p.M <= 4) {
-        if (al) product_tokens<Op, 4, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
-        else product_tokens<Op, 4, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
+    } else if (p.M <= Op::kTokens) {
+        if constexpr (Op::kTokens > 1) {
+            const uint32_t groups = (p.N + 7) / 8;
+            if (Op::kTokens == 4 || p.M <= 4) {
+                if (al) product_tokens<Op, 4, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
+                else product_tokens<Op, 4, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
+            } else if constexpr (Op::kTokens == 8) {
+                if (al) product_tokens<Op, 8, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
+                else product_tokens<Op, 8, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
+            }
+        }
     } else {
+        const uint32_t groups = (p.N + 15) / 16;
         if (al) product_rows<Op, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);
         else product_rows<Op, GATED, false, Done><<<groups, 512, 0, stream>>>(p, done);
     }

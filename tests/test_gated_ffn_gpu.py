@@ -93,13 +93,13 @@ def run(M, D, F, dtype, kind, seed):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 15, 16, 17, 33, 64, 65, 100, 127, 128, 129, 257, 300])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 33, 64, 65, 100, 127, 128, 129, 257, 300])
 def test_token_counts(M, dtype):
     run(M, 136, 200, dtype, KINDS[M % 3], M)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M", [1, 3, 9, 77])
+@pytest.mark.parametrize("M", [1, 3, 7, 11, 77])
 @pytest.mark.parametrize("D", [1, 3, 7, 8, 24, 31, 63, 64, 65, 100, 129, 200, 520, 1032])
 def test_widths(D, M, dtype):
     run(M, D, 48, dtype, KINDS[D % 3], 100 + D)
