@@ -118,7 +118,7 @@ int check_ffn(const Call& c, int* why) {
         *why = LTX3DROPE_REASON_NONPOSITIVE_DIM;
         return LTX3DROPE_E_UNSUPPORTED;
     }
-    if (c.tokens >= kFfnMaxSize || c.dim >= kFfnMaxSize || 2 * c.hidden >= kFfnMaxSize ||
+    if (c.tokens >= kFfnMaxSize || c.dim >= kFfnMaxSize || c.hidden >= kFfnMaxSize / 2 ||
         too_many_tiles(c.tokens, c.hidden) || too_many_tiles(c.tokens, c.dim) || too_many_tiles(2 * c.hidden, c.dim)) {
         *why = LTX3DROPE_REASON_TOO_LARGE;
         return LTX3DROPE_E_UNSUPPORTED;

@@ -274,3 +274,19 @@ def test_host_tensors_are_refused(call):
     with pytest.raises(rla.Ltx3dRopeUnsupported) as e:
         call()
     assert e.value.reason == "NOT_DEVICE_PTR"
+
+
+@pytest.mark.parametrize("tokens", [0, 3, 4032, 1 << 20, 1 << 62])
+@pytest.mark.parametrize("hidden", [1 << 61, 1 << 62, (1 << 62) + (1 << 20), (1 << 63) - 32, (1 << 63) - 1])
+def test_sizes_whose_products_pass_64_bits_are_refused(tokens, hidden):
+    reason = ctypes.c_int(-1)
+    for call, size, make in ((L.ltx3drope_gated_ffn, L.ltx3drope_gated_ffn_workspace, ffn_call),
+                             (L.ltx3drope_gated_ffn_backward, L.ltx3drope_gated_ffn_backward_workspace,
+                              ffn_backward_call)):
+        for kw in (dict(tokens=tokens, hidden=hidden), dict(tokens=hidden, dim=hidden)):
+            assert call(make(**kw), None, reason) == _lib.E_UNSUPPORTED
+            assert _lib.REASONS[reason.value] == "TOO_LARGE"
+            assert size(make(**kw)) == _lib.E_UNSUPPORTED
+    for kw in (dict(tokens=tokens, out=hidden), dict(tokens=hidden, dim=hidden)):
+        assert L.ltx3drope_q8_matmul(q8_call(**kw), None, reason) == _lib.E_UNSUPPORTED
+        assert _lib.REASONS[reason.value] == "TOO_LARGE"
