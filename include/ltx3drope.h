@@ -36,6 +36,12 @@
  * named q, k, q_out, k_out are device pointers owned by the caller.  Table
  * handles are owned by the library and reference counted.  A "stream" is a
  * hipStream_t passed as void* (NULL = the device's null stream).
+ *
+ * Beside it stand the operations around the rotation: a shard of the grid,
+ * the rotate-half form, patchify, the DiT frequency grid, and the rest of a
+ * transformer block: norms before and after it with gate, scaled residual and
+ * the next modulated norm, the gated feed-forward block, and the linear layer
+ * in 8-bit integers.  Each is documented at its declaration.
  */
 #ifndef LTX3DROPE_H
 #define LTX3DROPE_H
@@ -491,9 +497,8 @@ int64_t ltx3drope_gated_ffn_workspace(const ltx3drope_gated_ffn_t* call);
  * the sums are held in fp32 and each output rounded once.  dx may be NULL, and
  * so may dw_gate and dw_up together; what is NULL is not computed.  Sums are
  * added in a fixed order: equal inputs give equal bits.  An empty call
- * (tokens = 0 or hidden = 0) writes zeros into what it is given.  Workspace,
- * statuses and reasons as above; the
- * workspace is needed by every call that is not empty.
+ * (tokens = 0 or hidden = 0) writes zeros into what it is given.  Statuses and
+ * reasons as above; every call that is not empty needs a workspace.
  */
 typedef struct {
     int32_t dtype, activation;
@@ -505,6 +510,8 @@ typedef struct {
     int64_t workspace_bytes;
 } ltx3drope_gated_ffn_backward_t;
 int ltx3drope_gated_ffn_backward(const ltx3drope_gated_ffn_backward_t* call, void* stream, int* reason);
+/* Bytes of workspace for a call (its sizes, the alignment of the operands, and which outputs are not
+   NULL), or a negative status for a malformed descriptor. */
 int64_t ltx3drope_gated_ffn_backward_workspace(const ltx3drope_gated_ffn_backward_t* call);
 
 /*

@@ -16,6 +16,9 @@ checked: the pages print no table values.
 
 oracle.neox: the rotate-half RoPE with a gathered cos/sin cache (pins in
 tests/test_neox_oracle_pins.py).
+oracle.block: norms, gated feed-forward block and 8-bit linear layer of a
+transformer block in float64, forward and backward (pins in
+tests/test_block_host.py: the gradients against differences).
 """
 from . import dit_freqs, neox, patchify  # noqa: F401
 from .rope import (  # noqa: F401

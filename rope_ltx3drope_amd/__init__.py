@@ -11,6 +11,10 @@ Names follow the sglang PR #35698 page ("Implementation breakdown", steps 1-4;
 "Key source snippets"): tables() is the cached per-axis table lookup,
 can_use() the precheck, apply_qk() the fused one-launch rotation of Q and K and
 forward_pair() the decoder-side entry that ties them together.
+
+Of the transformer block around it: norm_before(), norm_after() and their
+backward passes, gated_ffn() and its backward pass, q8_quantize() and
+q8_matmul().
 """
 from __future__ import annotations
 
