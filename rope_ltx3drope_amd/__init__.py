@@ -468,8 +468,11 @@ def _rows_marshal(first, others):
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     if _dtype_code(first) < 0:
         raise Ltx3dRopeUnsupported("DTYPE")
-    _operands(device, (first, shape, dtype), *[(t, shape, dtype) for t in others if t is not None])
-    return (1, shape[0], shape[1]) if len(shape) == 2 else tuple(shape)
+    for t in (first, *others):
+        if t is not None and not (t.dtype is dtype and t.get_device() == device >= 0 and t.is_contiguous()
+                                  and t.shape == shape):
+            _operands(device, (t, shape, dtype))
+    return (1, *shape) if len(shape) == 2 else tuple(shape)
 
 
 def _vectors_marshal(row, size, weights, per_sample):
@@ -478,7 +481,8 @@ def _vectors_marshal(row, size, weights, per_sample):
     for t in weights:
         if t is not None:
             dtype = dtype or t.dtype
-            _operands(device, (t, (dim,), dtype))
+            if not (t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.shape == (dim,)):
+                _operands(device, (t, (dim,), dtype))
     for t in per_sample:
         if t is not None:
             dtype = dtype or t.dtype

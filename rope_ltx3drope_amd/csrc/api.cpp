@@ -140,26 +140,37 @@ bool ranges_overlap(const void* a, size_t an, const void* b, size_t bn) {
     return a0 < b0 + bn && b0 < a0 + an;
 }
 
+// The allocation that holds p; false where that is not device memory.
+bool device_range(const void* p, DeviceRange* out) {
+    hipPointerAttribute_t attr;
+    std::memset(&attr, 0, sizeof(attr));
+    void* base = nullptr;
+    if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    if (attr.type != hipMemoryTypeDevice) return false;
+    out->device = attr.device;
+    if (hipMemGetAddressRange(&base, &out->size, const_cast<void*>(p)) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    out->base = reinterpret_cast<uintptr_t>(base);
+    return true;
+}
+
+int check_range(const DeviceRange& a, const void* p, size_t bytes, int device) {
+    if (a.device != device) return LTX3DROPE_REASON_TABLE_DEVICE;
+    const uintptr_t q = reinterpret_cast<uintptr_t>(p);
+    if (q < a.base || q + bytes > a.base + a.size) return LTX3DROPE_REASON_EXTENT;
+    return LTX3DROPE_REASON_OK;
+}
+
 // Is p device memory of `device` inside an allocation that holds [p, p + bytes)?
 // Returns NOT_DEVICE_PTR, TABLE_DEVICE (memory of another device), EXTENT or OK.
 int check_device_ptr(const void* p, size_t bytes, int device) {
-    hipPointerAttribute_t attr;
-    std::memset(&attr, 0, sizeof(attr));
-    if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
-        (void)hipGetLastError();
-        return LTX3DROPE_REASON_NOT_DEVICE_PTR;
-    }
-    if (attr.type != hipMemoryTypeDevice) return LTX3DROPE_REASON_NOT_DEVICE_PTR;
-    if (attr.device != device) return LTX3DROPE_REASON_TABLE_DEVICE;
-    void* base = nullptr;
-    size_t size = 0;
-    if (hipMemGetAddressRange(&base, &size, const_cast<void*>(p)) != hipSuccess) {
-        (void)hipGetLastError();
-        return LTX3DROPE_REASON_NOT_DEVICE_PTR;
-    }
-    const uintptr_t b = reinterpret_cast<uintptr_t>(base), q = reinterpret_cast<uintptr_t>(p);
-    if (q < b || q + bytes > b + size) return LTX3DROPE_REASON_EXTENT;
-    return LTX3DROPE_REASON_OK;
+    DeviceRange a;
+    return device_range(p, &a) ? check_range(a, p, bytes, device) : LTX3DROPE_REASON_NOT_DEVICE_PTR;
 }
 
 namespace {

@@ -40,17 +40,28 @@ int check_spans(const Spans& t, int* device) {
             if (!own_row) return LTX3DROPE_REASON_OVERLAP;
         }
     }
-    hipPointerAttribute_t a;
-    std::memset(&a, 0, sizeof(a));
-    if (t.n == 0 || hipPointerGetAttributes(&a, t.s[0].p) != hipSuccess || a.type != hipMemoryTypeDevice) {
-        (void)hipGetLastError();
-        return LTX3DROPE_REASON_NOT_DEVICE_PTR;
-    }
+    // Tensors of one allocation (an allocator's blocks, a model's buffers) are asked for once: a range
+    // inside one that this call has found is device memory of the same GPU.
+    constexpr int kAllocations = 4;
+    uintptr_t from[kAllocations], to[kAllocations];
+    int known = 0, on = -1;
     for (int i = 0; i < t.n; ++i) {
-        const int r = check_device_ptr(t.s[i].p, t.s[i].bytes, a.device);
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t.s[i].p);
+        bool inside = false;
+        for (int j = 0; j < known; ++j) inside = inside || (p >= from[j] && p < to[j] && t.s[i].bytes <= to[j] - p);
+        if (inside) continue;
+        DeviceRange a;
+        if (!device_range(t.s[i].p, &a)) return LTX3DROPE_REASON_NOT_DEVICE_PTR;
+        if (on < 0) on = a.device;
+        const int r = check_range(a, t.s[i].p, t.s[i].bytes, on);
         if (r != LTX3DROPE_REASON_OK) return r;
+        if (known < kAllocations) {
+            from[known] = a.base;
+            to[known++] = a.base + a.size;
+        }
     }
-    *device = a.device;
+    if (on < 0) return LTX3DROPE_REASON_NOT_DEVICE_PTR;
+    *device = on;
     return LTX3DROPE_REASON_OK;
 }
 

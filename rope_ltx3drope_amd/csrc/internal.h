@@ -108,6 +108,13 @@ int64_t option(int which);
 
 // Argument checks and bookkeeping that every entry point shares (api.cpp).
 bool ranges_overlap(const void* a, size_t an, const void* b, size_t bn);
+struct DeviceRange {  // an allocation in device memory
+    uintptr_t base = 0;
+    size_t size = 0;
+    int device = -1;
+};
+bool device_range(const void* p, DeviceRange* out);
+int check_range(const DeviceRange& a, const void* p, size_t bytes, int device);
 int check_device_ptr(const void* p, size_t bytes, int device);
 int device_cu_count(int device, int* out);  // a status; the device must be the current one
 void count_launch();

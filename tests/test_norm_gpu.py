@@ -389,3 +389,27 @@ def test_refusals_on_the_device():
 def overlap():
     buf = torch.zeros(7 * 64, device=DEV)
     rla.norm_before(buf[:384].view(2, 3, 64), out=buf[64:448].view(2, 3, 64))
+
+
+def test_ranges_past_an_allocation_are_refused():
+    import ctypes
+
+    L, reason = _lib.lib(), ctypes.c_int(-1)
+    x = torch.zeros(1024, device=DEV)
+    # rows of half a terabyte, in place
+    call = _lib.Norm(dtype=_lib.DTYPE_F32, param_dtype=_lib.DTYPE_F32, after=0, post_norm=0, next_norm=1, batch=1,
+                     rows=1 << 27, dim=1024, eps=1e-6, weight_offset=0.0, residual_scale=1.0, residual=x.data_ptr(),
+                     n=x.data_ptr())
+    assert L.ltx3drope_norm(call, None, reason) == _lib.E_UNSUPPORTED
+    assert _lib.REASONS[reason.value] == "EXTENT"
+    # output and input inside an allocation, weights that begin in it and pass its end
+    hidden, dim = 1 << 19, 1 << 13
+    buf = torch.zeros(hidden + 2 * dim, device=DEV)
+    at = buf.data_ptr()
+    call = _lib.GatedFfn(dtype=_lib.DTYPE_F32, activation=0, tokens=1, dim=dim, hidden=hidden, x=at + 4 * hidden,
+                         w_gate=at + 4 * (hidden + dim), w_up=at + 4 * (hidden + dim), h=at)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    assert L.ltx3drope_gated_ffn(call, None, reason) == _lib.E_UNSUPPORTED
+    assert _lib.REASONS[reason.value] == "EXTENT"
+    assert rla.stats()["fast_launches"] == 0
