@@ -7,7 +7,7 @@
 // roundings come on top of those of dg and du and of the gradients themselves (measured: gradients
 // within 0.0030 of 64 bits in the 2-norm, 0.0024 with fp32 projections, 0.0017 the output's rounding
 // alone).  The round trip through memory costs a ninth of a training step (4096 tokens, 2048 -> 8192
-// bf16: 90 of 797 us; half of that in bf16), where recomputing the projections would cost 220 us:
+// bf16: 90 of 791 us; half of that in bf16), where recomputing the projections would cost 220 us:
 //     dg = dh * u * act'(g),  du = dh * act(g)          in fp32, rounded once for the matrix cores
 //     dx = [dg du] [Wg; Wu],  dWg = dg^T x,  dWu = du^T x
 // dg and du lie side by side, [M][2 Fp], so that dx is one product over k = 2F and dWg, dWu together
