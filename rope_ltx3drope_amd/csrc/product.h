@@ -1,6 +1,6 @@
 // Matrix products C[m][n] = sum_k A[m][k] * B[n][k] with a functor for what happens to finished sums:
 // product_tiles on the matrix cores for many rows of A, product_rows for up to 16, product_tokens for up
-// to 4.  Kernels, and the rules that choose among them.
+// to 8.  Kernels, and the rules that choose among them.
 //
 // The matrix cores' products treat a row of k as bytes: a 16-byte chunk holds 8 bf16, 16 int8 or 4 fp32 numbers,
 // and one step of a wavefront multiplies 16 rows of A by 16 rows of B over 4 chunks.  Lane l holds
@@ -255,16 +255,17 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
     constexpr int BNB = GATED ? BN / 2 : BN;  // rows of each B in a tile
     using SA = Side<Op, BM, A_OUTER>;
     using SB = Side<Op, BNB, B_OUTER>;
-    // LDS: rings of kSlotsA steps of A and 2 of B (160 KB for 256 x 256: all there is).  The copies have a
+    // LDS: rings of kSlotsA steps of A and kSlotsB of B (256 x 256: 3 and 2, all 160 KB).  The copies have a
     // step's time to land at the least; with the third slot A's have two, and half as many bytes again
     // are on their way at any time, which is what the copies' rate goes by (8192 x 8192 x 8192 in bf16:
     // 887 us with two slots each, 848 so; copies alone 743, and 587 with two whole steps on their way).
-    constexpr int kSlotsA = PIPELINED ? 3 : 2, kStepK = SA::kStepK;
+    constexpr int kRing = DIRECT && BM == 64 ? 3 : 2;  // not PIPELINED: slots of either
+    constexpr int kSlotsA = PIPELINED ? 3 : kRing, kSlotsB = PIPELINED ? 2 : kRing, kStepK = SA::kStepK;
     constexpr int kBytesB = BN * kRowBytes, kAtB = kSlotsA * SA::kBytes;
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies a wavefront makes of each operand
     static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN, "a tile's copies split evenly over the wavefronts");
     static_assert(!GATED || (CB % 2 == 0 && FN % 2 == 0 && !B_OUTER), "both halves of B in every wavefront");
-    __shared__ __align__(1024) char lds[kAtB + 2 * kBytesB];
+    __shared__ __align__(1024) char lds[kAtB + kSlotsB * kBytesB];
 
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -500,22 +501,25 @@ __global__ __launch_bounds__(WM* WN * 64) void product_tiles(Product p, Done don
         multiply(1);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives its workgroup
     } else if constexpr (DIRECT) {
-        // two workgroups share a compute unit and fill each other's waits
-        fetch_a(first, 0);
-        fetch_b(first, 0);
+        // several workgroups share a compute unit and fill each other's waits
+        for (int i = 0; i < kRing - 1; ++i) {
+            fetch_a(first + i, i);
+            fetch_b(first + i, i);
+        }
+        uint32_t slot = 0, free = kRing - 1;
         for (uint32_t s = first; s < last; ++s) {
-            const uint32_t slot = (s - first) & 1;
-            wait_and_meet<0>();
-            if (s + 1 < last) {
-                fetch_a(s + 1, slot ^ 1);
-                fetch_b(s + 1, slot ^ 1);
-            }
+            wait_and_meet<(kRing - 2) * (CA + CB)>();
+            fetch_a(s + kRing - 1, free);
+            fetch_b(s + kRing - 1, free);
+            free = slot;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 read(slot, slot, kk);
                 multiply(kk);
             }
+            slot = slot + 1 == kRing ? 0 : slot + 1;
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives its workgroup
     } else {
         // two steps ahead in registers: a load has two steps' time to arrive
         Held even, odd;
@@ -824,6 +828,12 @@ inline hipError_t launch_tiles(const Product& p, const Plan& plan, const Done& d
     return hipGetLastError();
 }
 
+// Tiles of 64 with k innermost: whole steps with three slots for both operands (not PIPELINED) keep more of
+// B on its way, half steps (PIPELINED) keep the matrix cores busier.  32 x 20480, k 4096 in bf16 (B from
+// memory): 38 us and 50; 64 rows 45 and 53; 128 rows 60 and 59; 512 x 4352, k 1536: 17 and 16.  int8
+// 128 x 10240, k 4096: 14 and 17; fp32 301 x 5568, k 1104: 42 and 44.  Five or eight slots are slower than three.
+constexpr uint32_t kStreamedRows = 128;
+
 template <class Op, bool GATED, bool A_OUTER, bool B_OUTER, class Done>
 hipError_t launch_product(Product p, bool direct, void* workspace, const Done& done, hipStream_t stream) {
     const Plan plan = plan_product<Op, GATED, A_OUTER || B_OUTER>(p.M, p.N, p.k, direct, p.b_pitch);
@@ -838,7 +848,12 @@ hipError_t launch_product(Product p, bool direct, void* workspace, const Done& d
     if (plan.bm == 128)
         return direct ? launch_tiles<Op, 128, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
                       : launch_tiles<Op, 128, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
-    return direct ? launch_tiles<Op, 64, 64, 2, 2, true, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
+    if constexpr (!A_OUTER && !B_OUTER) {
+        if (direct && (Op::kElem != 2 || p.M <= kStreamedRows))
+            return launch_tiles<Op, 64, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream);
+    }
+    constexpr bool halves = Op::kElem == 2 || A_OUTER || B_OUTER;
+    return direct ? launch_tiles<Op, 64, 64, 2, 2, halves, GATED, A_OUTER, B_OUTER, true>(p, plan, done, stream)
                   : launch_tiles<Op, 64, 64, 2, 2, false, GATED, A_OUTER, B_OUTER, false>(p, plan, done, stream);
 }
 
@@ -862,6 +877,15 @@ hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t strea
                 else product_tokens<Op, 8, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
             }
         }
+    } else if (const uint32_t tiles = (p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64);
+               Op::kElem == 2 && al && tiles >= 256) {
+        // A tile a compute unit or more: copies to LDS carry the weights faster than registers.  2 x 10240
+        // rows of 4096 bf16: 38 us for 5 to 16 rows, product_rows 41 to 47; 2 x 16384 of 1024: 12 and 13 to
+        // 15.  fp32 is the other way: 139 and 101 for 16 rows; int8 gives no tile a compute unit at usual sizes, and splits need a workspace.
+        Product q = p;
+        q.splits = 1;
+        return launch_tiles<Op, 64, 64, 2, 2, false, GATED, false, false, true>(q, Plan{64, 64, tiles, 1, 0}, done,
+                                                                                stream);
     } else {
         const uint32_t groups = (p.N + 15) / 16;
         if (al) product_rows<Op, GATED, true, Done><<<groups, 512, 0, stream>>>(p, done);

@@ -290,3 +290,21 @@ def test_refusals_on_the_device():
     with pytest.raises(ValueError):
         rla.gated_ffn(x, w, w, "relu")
     assert rla.stats()["fast_launches"] == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,D,F", [(5, 8, 8161), (5, 200, 8200), (8, 64, 8192), (9, 72, 8192), (15, 136, 8200), (16, 520, 8161),
+                                   (16, 128, 16391), (17, 200, 8200), (33, 392, 8200), (64, 136, 8161), (100, 264, 8200),
+                                   (128, 320, 4100), (129, 264, 8200)])
+def test_few_tokens_of_wide_blocks(M, D, F, dtype):
+    """Tiles with three steps on their way, sums of one step to some, where they begin and end."""
+    run(M, D, F, dtype, "silu", M * F + D)
+
+
+def test_few_tokens_repeat_their_bits():
+    t = {k: v.to(DEV) for k, v in inputs(16, 1024, 8200, torch.bfloat16, 5).items()}
+    first = rla.gated_ffn(t["x"], t["w_gate"], t["w_up"])
+    for i in range(20):
+        assert torch.equal(rla.gated_ffn(t["x"], t["w_gate"], t["w_up"]), first), i
+    for m in (5, 9, 15):  # rows do not depend on their neighbours
+        assert torch.equal(rla.gated_ffn(t["x"][:m], t["w_gate"], t["w_up"]), first[:m]), m
