@@ -385,7 +385,8 @@ int ltx3drope_dit_freq_grid(double theta, int64_t dim, int64_t num_rope_elems, i
  *     n      = hat(r) * (next_weight + weight_offset) * (1 + next_scale_b) + next_shift_b
  * each output rounded once to `dtype` (n is formed from the unrounded r).
  * weight_offset counts only where its weight is given.  mean(v^2) has to be
- * finite in fp32: a row whose squares pass it gives zeros or NaN.
+ * finite in fp32 (with an eps below 2^-110 the sum of the squares): a row whose
+ * squares pass it gives zeros or NaN.
  *
  * after = 1: y, residual and r are required; next_norm = 1 also writes n.
  * after = 0 is the norm before a block alone: n from `residual`; y, weight,

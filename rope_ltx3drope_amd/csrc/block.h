@@ -17,6 +17,7 @@ struct NormForward {
     void *r, *n;
     uint32_t batch, rows, dim;
     float eps, weight_offset, residual_scale;
+    float square_scale;  // norm_square_scale(eps)
     bool has_y, post_norm, next_norm, param_f32;
     bool chunks;  // the vectors, and each sample's part of them, start on 16 bytes
 };
@@ -27,10 +28,18 @@ struct NormBackward {
     float* partial;  // [3][batch][parts][dim], NULL when no vector's gradient is asked for
     uint32_t batch, rows, dim;
     float eps, weight_offset, residual_scale;
+    float square_scale;
     bool has_y, post_norm, next_norm, param_f32, chunks;
 };
 
 constexpr int64_t kNormMaxDim = 16384;    // 1024 threads of 16 elements hold one row
+
+// A row's squares are added up times this power of two: 1 / kNormMaxDim, so that their sum stays in fp32's
+// range wherever their mean does.  It is exact but where a scaled square falls below 2^-126; those are off
+// by 2^-150 each, 2^-136 in the mean, which is less than fp32 resolves beside an eps of 2^-110 or more.
+// Below that the squares are added up as they are.
+inline float norm_square_scale(float eps) { return eps >= 0x1p-110f ? 0x1p-14f : 1.f; }
+static_assert(kNormMaxDim == 1 << 14, "norm_square_scale takes a row's length out of its sum");
 constexpr int64_t kNormMaxBatch = 65535;  // one grid row a sample
 
 // vec: every row pointer is 16-byte aligned and a row is whole 16-byte vectors.

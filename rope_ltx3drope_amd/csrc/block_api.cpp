@@ -265,6 +265,7 @@ int ltx3drope_norm(const ltx3drope_norm_t* call, void* stream, int* reason) {
     p.eps = c.eps;
     p.weight_offset = c.weight_offset;
     p.residual_scale = c.residual_scale;
+    p.square_scale = norm_square_scale(c.eps);
     p.has_y = c.after != 0;
     p.post_norm = c.post_norm != 0;
     p.next_norm = c.next_norm != 0;
@@ -354,6 +355,7 @@ int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream,
     p.eps = c.eps;
     p.weight_offset = c.weight_offset;
     p.residual_scale = c.residual_scale;
+    p.square_scale = norm_square_scale(c.eps);
     p.has_y = c.after != 0;
     p.post_norm = c.post_norm != 0;
     p.next_norm = c.next_norm != 0;

@@ -221,7 +221,7 @@ __global__ __launch_bounds__(1024) void norm_forward(NormForward p) {
     __shared__ float lds[2][2][kMaxWaves];
     const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
     const uint32_t D = p.dim, b = blockIdx.y;
-    const float inv_d = 1.0f / static_cast<float>(D);
+    const float sq = p.square_scale, inv_sq = 1.0f / static_cast<float>(D) / sq;  // sq: a power of two
 
     constexpr size_t es = F32 ? 4 : 2;
     const uint32_t step = gridDim.x * G;
@@ -258,9 +258,9 @@ __global__ __launch_bounds__(1024) void norm_forward(NormForward p) {
             if (p.post_norm) {
                 float ss[1] = {0.f};
 #pragma unroll
-                for (int k = 0; k < E; ++k) ss[0] = fmaf(y[k], y[k], ss[0]);
+                for (int k = 0; k < E; ++k) ss[0] = fmaf(y[k] * sq, y[k], ss[0]);
                 row_sum(ss, lds[phase][0], t, T, g);
-                rstd = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+                rstd = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
             }
 #pragma unroll
             for (int k = 0; k < E; ++k) r[k] = fmaf(y[k] * rstd, fy[k], p.residual_scale * r[k]);
@@ -269,9 +269,9 @@ __global__ __launch_bounds__(1024) void norm_forward(NormForward p) {
         if constexpr (NEXT) {
             float ss[1] = {0.f};
 #pragma unroll
-            for (int k = 0; k < E; ++k) ss[0] = fmaf(r[k], r[k], ss[0]);
+            for (int k = 0; k < E; ++k) ss[0] = fmaf(r[k] * sq, r[k], ss[0]);
             row_sum(ss, lds[phase][1], t, T, g);
-            const float rstd = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+            const float rstd = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
 #pragma unroll
             for (int k = 0; k < E; ++k) r[k] = fmaf(r[k] * rstd, fn[k], sh[k]);
             if (live) store_row<F32, E, VEC>(static_cast<char*>(p.n) + off, r, t, T, D);
@@ -286,6 +286,7 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
     const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
     const uint32_t D = p.dim, b = blockIdx.y;
     const float inv_d = 1.0f / static_cast<float>(D);
+    const float sq = p.square_scale, inv_sq = inv_d / sq;  // sq: a power of two
 
     float fy[HAS_Y ? E : 1], fn[NEXT ? E : 1];
     float p1[NEXT ? E : 1] = {}, p2[NEXT ? E : 1] = {}, p3[HAS_Y ? E : 1] = {};
@@ -314,18 +315,18 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
         }
         float rstd_y = 1.f;
         if constexpr (NEXT) {
-            float ss[3] = {0.f, 0.f, 0.f};  // r.r, (dn fn).r, y.y
+            float ss[3] = {0.f, 0.f, 0.f};  // r.r sq, (dn fn).r, y.y sq
 #pragma unroll
             for (int k = 0; k < E; ++k) {
-                ss[0] = fmaf(r[k], r[k], ss[0]);
+                ss[0] = fmaf(r[k] * sq, r[k], ss[0]);
                 ss[1] = fmaf(dn[k] * fn[k], r[k], ss[1]);
-                if constexpr (HAS_Y) ss[2] = fmaf(y[k], y[k], ss[2]);
+                if constexpr (HAS_Y) ss[2] = fmaf(y[k] * sq, y[k], ss[2]);
             }
             row_sum(ss, lds[phase][0], t, T, g);
-            const float rstd = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+            const float rstd = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
             const float proj = ss[1] * rstd * inv_d;  // mean(v * hat(r))
             if constexpr (HAS_Y)
-                if (p.post_norm) rstd_y = rsqrtf(fmaf(ss[2], inv_d, p.eps));
+                if (p.post_norm) rstd_y = rsqrtf(fmaf(ss[2], inv_sq, p.eps));
 #pragma unroll
             for (int k = 0; k < E; ++k) {
                 const float hat = r[k] * rstd;
@@ -337,9 +338,9 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
             if (p.post_norm) {
                 float ss[1] = {0.f};
 #pragma unroll
-                for (int k = 0; k < E; ++k) ss[0] = fmaf(y[k], y[k], ss[0]);
+                for (int k = 0; k < E; ++k) ss[0] = fmaf(y[k] * sq, y[k], ss[0]);
                 row_sum(ss, lds[phase][0], t, T, g);
-                rstd_y = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+                rstd_y = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
             }
         }
         if (live) {

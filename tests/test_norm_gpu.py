@@ -413,3 +413,30 @@ def test_ranges_past_an_allocation_are_refused():
     assert L.ltx3drope_gated_ffn(call, None, reason) == _lib.E_UNSUPPORTED
     assert _lib.REASONS[reason.value] == "EXTENT"
     assert rla.stats()["fast_launches"] == 0
+
+
+@pytest.mark.parametrize("dtype,pdtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 2053, 4096, 16384])
+@pytest.mark.parametrize("scale", [2.0 ** 55, 2.0 ** 61])
+def test_rows_whose_squares_add_up_past_fp32(scale, dim, dtype, pdtype):
+    """mean(v^2) is finite in fp32 (around 2e37 for the larger scale) where the sum of the squares, or one of
+    them alone, is not; and the same rows as far below 1.  The scaling is exact, so the bounds are those of any row."""
+    for post in (True, False):
+        for s in (scale, 1.0 / scale):
+            c = Case(2, 5, dim, dtype, pdtype, dim + 1, post=post)
+            c.y, c.residual = c.y * s, c.residual * s
+            run_all(c)
+
+
+@pytest.mark.parametrize("eps", [1e-30, 2e-33, 1e-36])
+def test_smallest_eps(eps):
+    """Rows around sqrt(eps): the squares lie close to fp32's smallest normal number."""
+    g = torch.Generator().manual_seed(6)
+    x = randn(g, 3, 4096) * float(torch.tensor(eps).sqrt())
+    got = rla.norm_before(x.to(DEV), eps=eps)
+    eps32 = float(torch.tensor(eps))  # as the call takes it
+    # squares under the smallest normal number are off by 2^-150 each, with an eps of 2^-110 or more after
+    # they were scaled by 2^-14
+    want = ob.norm_before(d(x)[None], None, None, None, eps32, 0.0)[0]
+    under = 2.0 ** (-136 if eps >= 2.0 ** -110 else -150) / (d(x) ** 2).mean(-1, keepdim=True).clamp_min(eps32)
+    assert_within(got, want, (K_ROW * U + under) * want.abs() + tiny(torch.float32), "n")
