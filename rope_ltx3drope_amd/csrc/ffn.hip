@@ -38,8 +38,10 @@ __device__ __forceinline__ float act(int kind, float g, float* slope) {
         if (slope) *slope = fmaf(g * s, 1.0f - s, s);
         return g * s;
     }
-    if (kind == 1) {  // gelu
-        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+    if (kind == 1) {
+        // gelu, by the complement: 1 + erf would cancel on the negative side (0 from -5.5 on).  It costs up
+        // to 4 % of a forward call (4096 tokens, 2048 -> 8192 bf16: 241 us, 232 with 1 + erf).
+        const float c = 0.5f * erfcf(g * -0.70710678118654752f);
         if (slope) *slope = fmaf(g * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g), c);
         return g * c;
     }

@@ -308,3 +308,57 @@ def test_few_tokens_repeat_their_bits():
         assert torch.equal(rla.gated_ffn(t["x"], t["w_gate"], t["w_up"]), first), i
     for m in (5, 9, 15):  # rows do not depend on their neighbours
         assert torch.equal(rla.gated_ffn(t["x"][:m], t["w_gate"], t["w_up"]), first[:m]), m
+
+
+def act64(v, kind):
+    """act(v) and its slope in 64 bits, to full relative precision on both sides."""
+    if kind == "gelu":
+        c, phi = torch.erfc(-v / math.sqrt(2.0)) / 2.0, torch.exp(-0.5 * v * v) / math.sqrt(2.0 * math.pi)
+        return v * c, c + v * phi, c.abs(), (v * phi).abs()
+    k, cubic = (1.0, 0.0) if kind == "silu" else (math.sqrt(8.0 / math.pi), 0.044715)
+    s = torch.sigmoid(k * (v + cubic * v ** 3))
+    inner = torch.where((s == 0) | (s == 1), torch.zeros_like(s), k * (1.0 + 3 * cubic * v * v))
+    t = torch.sigmoid(-k * (v + cubic * v ** 3))  # 1 - s
+    return v * s, s + v * s * t * inner, s, (v * s * t * inner).abs()
+
+
+def act_bounds(v, kind):
+    """What act(v) and its slope in fp32 may be off by.
+
+    gelu: the argument is off by 2 u relative (constant, product), which moves erfc(x) by (2 x^2 + 1) times
+    as much, and erfcf itself is within 16 ulp; the density's exponent g^2 / 2 by 3 u relative.
+    The others: z by 6 u (gelu_tanh) and z log2(e) by 2 u relative, exp2, 1 + and the reciprocal by 5 u:
+    k |z| u + 8 u, the first weighed with 1 - s as e^-z is in 1 + e^-z.  Below 2^-126 the reciprocal may be 0."""
+    a, slope, s, rest = act64(v, kind)
+    if kind == "gelu":
+        c_tol = (2 * v * v + 40) * U * s
+        return v.abs() * c_tol + 2 * U * a.abs(), c_tol + rest * (2 * v * v + 8) * U + 2 * U * (s + rest)
+    per, z = (2, v.abs()) if kind == "silu" else (8, 1.6 * v.abs() + 0.0715 * v.abs() ** 3)
+    inner = 1.0 if kind == "silu" else 1.6 * (1.0 + 0.135 * v * v)
+    t = (1.0 - s).clamp_min(0)
+    s_tol = s * (t * (per * z + 2) + 8) * U + 2.0 ** -126
+    away = t * s_tol + s * (s_tol + U)
+    away = torch.where((s == 0) | (s == 1), torch.zeros_like(s), v.abs() * inner * away)
+    return v.abs() * s_tol + 2 * U * a.abs(), s_tol + away + 10 * U * (s + rest)
+
+
+def check_act(values, kind, dtype):
+    """h = act(v) and its slope through one hidden unit: g = v and u = 1 exactly."""
+    x = torch.stack([values, torch.ones_like(values)], 1).to(DEV)
+    wg, wu = torch.tensor([[1.0, 0.0]], dtype=dtype, device=DEV), torch.tensor([[0.0, 1.0]], dtype=dtype, device=DEV)
+    h, g, u = rla.gated_ffn(x, wg, wu, kind, save=True)
+    assert torch.equal(g[:, 0].cpu(), values.float()) and bool((u == 1).all())
+    dx, _, _ = rla.gated_ffn_backward(torch.ones_like(h), x, wg, wu, g, u, kind, need_dw=False)
+    a, slope, _, _ = act64(d(values), kind)
+    a_tol, slope_tol = act_bounds(d(values), kind)
+    hs = half_step(dtype)
+    for got, want, tol, what in ((h[:, 0], a, a_tol, "act"), (dx[:, 0], slope, slope_tol, "slope"),
+                                 (dx[:, 1], a, a_tol, "act in dx")):
+        assert_within(got, want, tol + hs * (want.abs() + tol) + tiny(dtype), what)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [3, 16, 1500])
+@pytest.mark.parametrize("kind,low,high", [("silu", -80.0, 20.0), ("gelu", -12.5, 8.0), ("gelu_tanh", -9.5, 8.0)])
+def test_activation_tails_relative_to_their_values(kind, low, high, M, dtype):
+    check_act(torch.linspace(low, high, M).to(dtype), kind, dtype)
