@@ -48,7 +48,11 @@ __device__ __forceinline__ float act(int kind, float g, float* slope) {
     // gelu by its tanh formula: (1 + tanh z) / 2 is the logistic function of 2z
     const float z2 = 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
     const float s = logistic(z2);
-    if (slope) *slope = fmaf(g * s * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
+    if (slope) {
+        // s or 1 - s is 0 long before g^2 passes 2^100: held there, so that 0 is not multiplied by infinity
+        const float g2 = fminf(g * g, 0x1p100f);
+        *slope = fmaf(g * s * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f, g2, 1.0f), s);
+    }
     return g * s;
 }
 

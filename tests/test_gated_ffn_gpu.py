@@ -362,3 +362,11 @@ def check_act(values, kind, dtype):
 @pytest.mark.parametrize("kind,low,high", [("silu", -80.0, 20.0), ("gelu", -12.5, 8.0), ("gelu_tanh", -9.5, 8.0)])
 def test_activation_tails_relative_to_their_values(kind, low, high, M, dtype):
     check_act(torch.linspace(low, high, M).to(dtype), kind, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", KINDS)
+def test_activations_of_huge_projections(kind, dtype):
+    """Far out act(v) is v or 0 and its slope 1 or 0, also where v^2 and v^3 pass fp32's range."""
+    v = torch.tensor([1e3, 1e6, 1e13, 1e15, 5e18, 3e19, 1e20, 1e30, 3e38])
+    check_act(torch.cat([v, -v]).to(dtype), kind, dtype)
