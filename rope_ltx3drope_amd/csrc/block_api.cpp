@@ -114,7 +114,8 @@ size_t norm_workspace(const ltx3drope_norm_backward_t& c) {
                                    static_cast<uint32_t>(c.dim));
 }
 
-// A product's launch: 64 x 32 tiles (the smallest) of 256 threads stay below 2^32 threads.
+// A product's launch: 64 x 32 tiles (the smallest) of 256 threads stay below 2^32 threads.  The kernels
+// without tiles take 64 threads an output up to 2^25 outputs a token and 32 above, of fewer than 2^26.
 bool too_many_tiles(int64_t M, int64_t N) { return (M / 64 + 1) * (N / 32 + 1) > kMaxTiles; }
 
 // The feed-forward block's scalars, both directions.

@@ -734,6 +734,9 @@ __device__ __forceinline__ void store4(void* row, uint32_t n, uint32_t N, f32x4 
 }
 
 constexpr uint32_t kFewRows = 16;  // most rows of A that the kernels without tiles take
+// Most outputs that product_tokens takes for one row of A: 64 threads each, and a launch holds fewer than
+// 2^32.  product_rows has 32 an output.
+constexpr uint32_t kTokenOutputs = uint32_t(1) << 25;
 
 // How a product runs: its tile (gated: bn / 2 columns of either B), and over how many workgroups its sums
 // are split.
@@ -862,11 +865,11 @@ hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t strea
     const uint64_t bytes = uint64_t(p.k) * Op::kElem;
     const bool al = chunks16(p.a, p.a_pitch, bytes) && chunks16(p.b[0], p.b_pitch, bytes) &&
                     (!GATED || chunks16(p.b[1], p.b_pitch, bytes));
-    if (p.M == 1) {
+    if (p.M == 1 && p.N <= kTokenOutputs) {
         const uint32_t groups = (p.N + 3) / 4;
         if (al) product_tokens<Op, 1, GATED, true, Done><<<groups, 256, 0, stream>>>(p, done);
         else product_tokens<Op, 1, GATED, false, Done><<<groups, 256, 0, stream>>>(p, done);
-    } else if (p.M <= Op::kTokens) {
+    } else if (p.M > 1 && p.M <= Op::kTokens) {
         if constexpr (Op::kTokens > 1) {
             const uint32_t groups = (p.N + 7) / 8;
             if (Op::kTokens == 4 || p.M <= 4) {

@@ -290,3 +290,13 @@ def test_sizes_whose_products_pass_64_bits_are_refused(tokens, hidden):
     for kw in (dict(tokens=tokens, out=hidden), dict(tokens=hidden, dim=hidden)):
         assert L.ltx3drope_q8_matmul(q8_call(**kw), None, reason) == _lib.E_UNSUPPORTED
         assert _lib.REASONS[reason.value] == "TOO_LARGE"
+
+
+def test_widest_8_bit_layers():
+    """The last width that is taken passes the checks of sizes; the next one does not."""
+    reason = ctypes.c_int(-1)
+    for out, tokens, want in (((1 << 26) - 1, 1, "NOT_DEVICE_PTR"), (1 << 26, 1, "TOO_LARGE"),
+                              ((1 << 26) - 1, 64, "NOT_DEVICE_PTR"), ((1 << 26) - 1, 256, "TOO_LARGE")):
+        far = dict(a=FAKE, a_scale=FAKE * 2, b=FAKE << 8, b_scale=FAKE << 16, y=FAKE << 20)
+        assert L.ltx3drope_q8_matmul(q8_call(tokens=tokens, dim=16, out=out, **far), None, reason) == _lib.E_UNSUPPORTED
+        assert _lib.REASONS[reason.value] == want, (out, tokens)

@@ -75,3 +75,17 @@ def test_gated_ffn():
         t = dict(x=rows(x, at).cpu(), w_gate=wg.cpu(), w_up=wu.cpu(), dh=rows(dh, at).cpu())
         check_forward(t, "gelu_tanh", rows(h, at), rows(g, at), rows(u, at))
         check_backward(t, "gelu_tanh", rows(g, at), rows(u, at), rows(dx, at), None, None)
+
+
+@pytest.mark.parametrize("tokens", [1, 2])
+@pytest.mark.parametrize("out", [1 << 25, (1 << 25) + 1, (1 << 26) - 4, (1 << 26) - 3, (1 << 26) - 1])
+def test_q8_matmul_of_the_most_outputs(out, tokens):
+    """Every width that is taken, up to the last: sums below 2^24 and two roundings, so bit for bit."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    a = torch.randint(-127, 128, (tokens, 16), generator=gen, device=DEV, dtype=torch.int8)
+    b = torch.randint(-128, 128, (out, 16), generator=gen, device=DEV, dtype=torch.int8)
+    sa, sb = torch.rand(tokens, generator=gen, device=DEV), torch.rand(out, generator=gen, device=DEV)
+    y = rla.q8_matmul(a, sa, b, sb, dtype=torch.float32)
+    for m in range(tokens):
+        want = (b.float() * a[m].float()).sum(1) * sa[m] * sb
+        assert torch.equal(y[m], want)
