@@ -466,7 +466,7 @@ int ltx3drope_q8_quantize(int dtype, int64_t rows, int64_t dim, const void* x, v
     if (dtype != LTX3DROPE_DTYPE_F32 && dtype != LTX3DROPE_DTYPE_BF16) return refuse(LTX3DROPE_REASON_DTYPE, reason);
     if (dim <= 0 || rows < 0) return refuse(LTX3DROPE_REASON_NONPOSITIVE_DIM, reason);
     const int64_t lim = int64_t(1) << 31;
-    if (dim >= lim || rows >= lim || (rows != 0 && dim > (int64_t(1) << 48) / rows))
+    if (dim >= lim || rows >= lim || (rows != 0 && dim > ((int64_t(1) << 48) - 1) / rows))
         return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
     if (rows == 0) return LTX3DROPE_OK;
     if (!x || !q || !scale) return refuse(LTX3DROPE_REASON_NULLPTR, reason);

@@ -300,3 +300,13 @@ def test_widest_8_bit_layers():
         far = dict(a=FAKE, a_scale=FAKE * 2, b=FAKE << 8, b_scale=FAKE << 16, y=FAKE << 20)
         assert L.ltx3drope_q8_matmul(q8_call(tokens=tokens, dim=16, out=out, **far), None, reason) == _lib.E_UNSUPPORTED
         assert _lib.REASONS[reason.value] == want, (out, tokens)
+
+
+@pytest.mark.parametrize("rows,dim", [(1 << 24, 1 << 24), (1 << 18, 1 << 30), (1 << 30, 1 << 18)])
+def test_quantiser_of_2_to_the_48_elements_is_refused(rows, dim):
+    reason = ctypes.c_int(-1)
+    args = (FAKE, 1 << 58, 1 << 60, None, reason)  # apart from each other at any of these sizes
+    assert L.ltx3drope_q8_quantize(0, rows, dim, *args) == _lib.E_UNSUPPORTED
+    assert _lib.REASONS[reason.value] == "TOO_LARGE"
+    assert L.ltx3drope_q8_quantize(0, rows - 1, dim, *args) == _lib.E_UNSUPPORTED
+    assert _lib.REASONS[reason.value] == "NOT_DEVICE_PTR"
