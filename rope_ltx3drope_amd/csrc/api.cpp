@@ -380,13 +380,6 @@ int verify_fast(const Problem& p, hipStream_t stream, int device, bool noalloc, 
 void count_launch() { stats().fast.fetch_add(1); }
 void count_rejected() { stats().rejected.fetch_add(1); }
 
-int device_cu_count(int device, int* out) {
-    DeviceRes* res = nullptr;
-    const int st = device_res(device, &res);
-    if (st == LTX3DROPE_OK) *out = res->cu_count;
-    return st;
-}
-
 int64_t option(int which) {
     switch (which) {
         case LTX3DROPE_OPT_PATH: return opts().path.load();

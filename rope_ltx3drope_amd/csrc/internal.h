@@ -116,7 +116,6 @@ struct DeviceRange {  // an allocation in device memory
 bool device_range(const void* p, DeviceRange* out);
 int check_range(const DeviceRange& a, const void* p, size_t bytes, int device);
 int check_device_ptr(const void* p, size_t bytes, int device);
-int device_cu_count(int device, int* out);  // a status; the device must be the current one
 void count_launch();
 void count_rejected();
 
