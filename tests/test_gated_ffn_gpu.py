@@ -326,12 +326,13 @@ def act_bounds(v, kind):
     """What act(v) and its slope in fp32 may be off by.
 
     gelu: the argument is off by 2 u relative (constant, product), which moves erfc(x) by (2 x^2 + 1) times
-    as much, and erfcf itself is within 16 ulp; the density's exponent g^2 / 2 by 3 u relative.
+    as much, and erfcf itself is within 16 ulp; the density's exponent g^2 / 2 by 3 u relative.  Below 2^-126
+    an ulp is 2^-149 whatever the value: half of 16 of those, and half of one for the halving, is below 2^-145.
     The others: z by 6 u (gelu_tanh) and z log2(e) by 2 u relative, exp2, 1 + and the reciprocal by 5 u:
     k |z| u + 8 u, the first weighed with 1 - s as e^-z is in 1 + e^-z.  Below 2^-126 the reciprocal may be 0."""
     a, slope, s, rest = act64(v, kind)
     if kind == "gelu":
-        c_tol = (2 * v * v + 40) * U * s
+        c_tol = (2 * v * v + 40) * U * s + 2.0 ** -145
         return v.abs() * c_tol + 2 * U * a.abs(), c_tol + rest * (2 * v * v + 8) * U + 2 * U * (s + rest)
     per, z = (2, v.abs()) if kind == "silu" else (8, 1.6 * v.abs() + 0.0715 * v.abs() ** 3)
     inner = 1.0 if kind == "silu" else 1.6 * (1.0 + 0.135 * v * v)
