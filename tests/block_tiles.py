@@ -27,6 +27,10 @@ Q8 = [
     (2105, 834, 1709), (2110, 944, 3925), (2159, 925, 81), (2743, 966, 1235), (3423, 1120, 3030),
     (4130, 1008, 1084), (4382, 7312, 44), (4389, 912, 213), (4686, 816, 996), (4957, 3035, 221),
     (2532, 8256, 1625), (1628, 7920, 2497)]
+# Up to 16 tokens: kernels without tiles, or one round of tiles of 64 (bf16 from five tokens on, 8161 and more
+# hidden columns), on 16 bytes and off them, rows shorter and longer than a wavefront's kilobytes.
+FEW = [(tokens, dim, hidden) for tokens in (1, 2, 4, 5, 8, 9, 16)
+       for dim, hidden in ((8, 3), (520, 8161), (1001, 77), (4104, 8200), (6152, 33))]
 
 FFN = {"bf16": FFN_BF16, "f32": FFN_F32}
 STEP = {"bf16": 64, "f32": 32, "int8": 128}  # k of a step of 128 bytes

@@ -89,3 +89,68 @@ def test_q8_matmul_of_the_most_outputs(out, tokens):
     for m in range(tokens):
         want = (b.float() * a[m].float()).sum(1) * sa[m] * sb
         assert torch.equal(y[m], want)
+
+
+def test_norm_vector_gradients():
+    """The vectors' gradients over all rows, against 64 bits a few thousand rows at a time."""
+    x, dn = (workloads.generate_bf16_bits((ROWS, DIM), seed, DEV) for seed in (6, 7))
+    w = torch.linspace(0.5, 1.5, DIM, device=DEV)
+    gate = torch.linspace(-1.0, 1.0, DIM, device=DEV)[None]
+    b = rla.norm_before_backward(dn[None], x[None], w, gate, gate)
+    dweight, dscale, dshift = (t.double() for t in b[1:])
+    a = rla.norm_after_backward(dn[None], None, x[None], None, w, gate, next_norm=False)
+    want, p2, terms, terms2 = (torch.zeros(DIM, dtype=torch.float64, device=DEV) for _ in range(4))
+    for at in range(0, ROWS, 1 << 16):
+        r, v = x[at:at + (1 << 16)].double(), dn[at:at + (1 << 16)].double()
+        hat = r * torch.rsqrt((r * r).mean(-1, keepdim=True) + 1e-6)
+        want += (v * hat).sum(0)
+        terms += (v * hat).abs().sum(0)
+        p2 += v.sum(0)
+        terms2 += v.abs().sum(0)
+    # a thread's walk adds its row of 512 workgroups' (DIM / 8 threads a row, one row a workgroup at a time),
+    # the join 512 parts; 40 operations for a term, and a few for the factors
+    steps = (ROWS / 512 + 512 + 48) * 2.0 ** -24
+    w, gate = w.double(), gate[0].double()
+    for got, value, size in ((dweight, (1 + gate) * want, (1 + gate).abs() * terms), (dscale[0], w * want, w * terms),
+                             (dshift[0], p2, terms2), (a.dweight.double(), gate * want, gate.abs() * terms),
+                             (a.dgate[0].double(), w * want, w * terms)):
+        assert bool(((got - value).abs() <= steps * size).all()), float(((got - value).abs() / size).max())
+
+
+def test_gated_ffn_weight_gradients():
+    """A weight's gradient over slopes of more than 2^32 elements: integers below 2^24, so exact."""
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randint(-1, 2, (ROWS, 48), generator=gen, device=DEV).bfloat16()
+    wg = torch.zeros(DIM, 48, dtype=torch.bfloat16, device=DEV)
+    g = torch.randint(0, 2, (ROWS, DIM), generator=gen, device=DEV, dtype=torch.int8).float() * 1088.0 - 1024.0
+    u = torch.ones_like(g)  # silu of 64 is 64 and its slope 1, of -1024 both are 0
+    dh = torch.randint(-1, 2, (ROWS, DIM), generator=gen, device=DEV, dtype=torch.int8).bfloat16()
+    _, dwg, dwu = rla.gated_ffn_backward(dh, x, wg, wg, g, u, "silu", need_dx=False)
+    want = torch.zeros(DIM, 48, dtype=torch.float64, device=DEV)
+    for at in range(0, ROWS, 1 << 16):
+        dg = dh[at:at + (1 << 16)].double() * (g[at:at + (1 << 16)] > 0)
+        want += dg.T.contiguous() @ x[at:at + (1 << 16)].double()
+    assert torch.equal(dwg, want.bfloat16()) and torch.equal(dwu, (64 * want).bfloat16())
+
+
+def test_norm_backward_of_the_most_samples():
+    """65535 samples of the widest rows: one partial row each, 13 GB of them."""
+    batch, dim = 65535, 16384
+    x, dn = (workloads.generate_bf16_bits((batch, 1, dim), seed, DEV) for seed in (9, 10))
+    w = torch.linspace(0.5, 1.5, dim, device=DEV)
+    scale = workloads.generate_bf16_bits((batch, dim), 11, DEV).float()
+    g = rla.norm_before_backward(dn, x, w, scale, scale)
+    torch.cuda.synchronize()
+    want, size = (torch.zeros(dim, dtype=torch.float64, device=DEV) for _ in range(2))
+    for at in range(0, batch, 2048):
+        part = slice(at, min(at + 2048, batch))
+        one = rla.norm_before_backward(dn[part], x[part], w, scale[part], scale[part])
+        assert torch.equal(g.dx[part], one.dx)
+        assert torch.equal(g.dscale[part], one.dscale) and torch.equal(g.dshift[part], one.dshift)
+        r, v = x[part, 0].double(), dn[part, 0].double()
+        t = v * r * torch.rsqrt((r * r).mean(-1, keepdim=True) + 1e-6) * (1 + scale[part].double())
+        want += t.sum(0)
+        size += t.abs().sum(0)
+    # 64 lanes down 65535 samples, then 16 sums; 48 operations for a term
+    steps = (65536 / 64 + 16 + 48) * 2.0 ** -24
+    assert bool(((g.dweight.double() - want).abs() <= steps * size).all())

@@ -1,4 +1,4 @@
-"""Every tile kernel of the block's matrix products on the GPU, at the sizes of tests/block_tiles.py.
+"""Every kernel of the block's matrix products on the GPU, at the sizes of tests/block_tiles.py.
 
 The inputs are small integers, so that every sum is exact in fp32 whatever its order: each element of the
 projections, of dx and of the weights' gradients has one right value, and one step of k left out, taken twice or
@@ -48,7 +48,7 @@ def assert_same(got, want, what):
                              f"first at {at}: {float(got[at])} for {float(want[at])}")
 
 
-@pytest.mark.parametrize("kind,tokens,dim,hidden", [(k, *s) for k, sizes in bt.FFN.items() for s in sizes])
+@pytest.mark.parametrize("kind,tokens,dim,hidden", [(k, *s) for k, sizes in bt.FFN.items() for s in sizes + bt.FEW])
 def test_feed_forward(kind, tokens, dim, hidden):
     dtype = DTYPES[kind]
     gen = torch.Generator(device=DEV).manual_seed(tokens * hidden + dim)
@@ -83,7 +83,7 @@ def test_feed_forward(kind, tokens, dim, hidden):
     assert_same(dwu, product(du.T, x), "dw_up")
 
 
-@pytest.mark.parametrize("tokens,dim,out", bt.Q8)
+@pytest.mark.parametrize("tokens,dim,out", bt.Q8 + bt.FEW)
 def test_8_bit_layer(tokens, dim, out):
     gen = torch.Generator(device=DEV).manual_seed(tokens * out + dim)
     a, b = integers(gen, -128, 127, tokens, dim).to(torch.int8), integers(gen, -128, 127, out, dim).to(torch.int8)
@@ -99,7 +99,7 @@ def test_the_integers_stay_exact():
     """The largest sums of the tests above stay within fp32's 2^24 (dx: F of 3 * 2 * 2 and of 2 * 128 * 2; dw: M of
     6 * 3 and of 256 * 3), so that no order of them rounds; dg and du (at most 6 and 256) fit bf16's 8 bits."""
     for sizes in bt.FFN.values():
-        for tokens, dim, hidden in sizes:
+        for tokens, dim, hidden in sizes + bt.FEW:
             assert dim * 3 * 2 < 2 ** 24
             assert hidden * (3 * 2 * 2 + 2 * 128 * 2) < 2 ** 24
             assert tokens * 256 * 3 < 2 ** 24

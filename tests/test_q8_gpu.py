@@ -261,3 +261,15 @@ def test_block_in_a_row():
             for a, b in zip(eager, outs):
                 assert torch.equal(a, b)
             check(x, outs)
+
+
+@pytest.mark.parametrize("dtype,dim", [(torch.bfloat16, 16384), (torch.bfloat16, 16392), (torch.bfloat16, 20480),
+                                       (torch.bfloat16, 32768), (torch.bfloat16, 32776), (torch.float32, 8192),
+                                       (torch.float32, 8196), (torch.float32, 16384), (torch.float32, 16388)])
+def test_quantize_wide_rows(dtype, dim):
+    """Two vectors a thread, four, and rows that are read twice; the largest magnitude in the last column too."""
+    x = randn(torch.Generator().manual_seed(dim), 5, dim, dtype=dtype)
+    x[1, -1] = 40.0
+    x[2] = 0
+    x[3, dim // 2] = float("inf")
+    check_quantize(x)
