@@ -191,6 +191,25 @@ __device__ __forceinline__ float wave_sum(float v) {
            (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
 }
 
+// The sum of a thread's squares times sq (norm_square_scale), in two chains of additions.  The sums are scaled
+// as a whole, unless one of the wavefront's passes fp32's range: scaling every square costs a multiplication
+// an element (2 x 34680 rows of 2048 bf16 after a block: 215 us, 213 so, 211 without scaling).
+template <int E>
+__device__ __forceinline__ float square_sum(const float (&v)[E], float sq) {
+    float even = 0.f, odd = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+        even = fmaf(v[k], v[k], even);
+        odd = fmaf(v[k + 1], v[k + 1], odd);
+    }
+    const float s = fmaf(odd, sq, even * sq);
+    if (__builtin_expect(!__any(!(s < __builtin_inff())), 1)) return s;
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) t = fmaf(v[k] * sq, v[k], t);
+    return t;
+}
+
 // Sums of K values over the T threads of each row (T a multiple of 64; row g of the workgroup owns
 // waves [g*T/64, (g+1)*T/64)).  `lds` holds K floats a wave of the workgroup, and successive calls
 // use different parts of it, so that one barrier a call is enough.
@@ -256,9 +275,7 @@ __global__ __launch_bounds__(1024) void norm_forward(NormForward p) {
         if constexpr (HAS_Y) {
             float rstd = 1.f;
             if (p.post_norm) {
-                float ss[1] = {0.f};
-#pragma unroll
-                for (int k = 0; k < E; ++k) ss[0] = fmaf(y[k] * sq, y[k], ss[0]);
+                float ss[1] = {square_sum(y, sq)};
                 row_sum(ss, lds[phase][0], t, T, g);
                 rstd = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
             }
@@ -267,9 +284,7 @@ __global__ __launch_bounds__(1024) void norm_forward(NormForward p) {
             if (live) store_row<F32, E, VEC>(static_cast<char*>(p.r) + off, r, t, T, D);
         }
         if constexpr (NEXT) {
-            float ss[1] = {0.f};
-#pragma unroll
-            for (int k = 0; k < E; ++k) ss[0] = fmaf(r[k] * sq, r[k], ss[0]);
+            float ss[1] = {square_sum(r, sq)};
             row_sum(ss, lds[phase][1], t, T, g);
             const float rstd = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
 #pragma unroll
@@ -315,13 +330,10 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
         }
         float rstd_y = 1.f;
         if constexpr (NEXT) {
-            float ss[3] = {0.f, 0.f, 0.f};  // r.r sq, (dn fn).r, y.y sq
+            float ss[3] = {square_sum(r, sq), 0.f, 0.f};  // r.r sq, (dn fn).r, y.y sq
+            if constexpr (HAS_Y) ss[2] = square_sum(y, sq);
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                ss[0] = fmaf(r[k] * sq, r[k], ss[0]);
-                ss[1] = fmaf(dn[k] * fn[k], r[k], ss[1]);
-                if constexpr (HAS_Y) ss[2] = fmaf(y[k] * sq, y[k], ss[2]);
-            }
+            for (int k = 0; k < E; ++k) ss[1] = fmaf(dn[k] * fn[k], r[k], ss[1]);
             row_sum(ss, lds[phase][0], t, T, g);
             const float rstd = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
             const float proj = ss[1] * rstd * inv_d;  // mean(v * hat(r))
@@ -336,9 +348,7 @@ __global__ __launch_bounds__(1024) void norm_backward(NormBackward p) {
             }
         } else if constexpr (HAS_Y) {
             if (p.post_norm) {
-                float ss[1] = {0.f};
-#pragma unroll
-                for (int k = 0; k < E; ++k) ss[0] = fmaf(y[k] * sq, y[k], ss[0]);
+                float ss[1] = {square_sum(y, sq)};
                 row_sum(ss, lds[phase][0], t, T, g);
                 rstd_y = rsqrtf(fmaf(ss[0], inv_sq, p.eps));
             }
