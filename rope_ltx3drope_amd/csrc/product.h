@@ -607,8 +607,8 @@ __device__ __forceinline__ T lanes_sum(T v) {
 // at a time, and multiplies it by every row of A in registers.  Bound by the bytes of B, which it reads
 // in whole kilobytes.  2 x 10240 rows of 4096 bf16: 26 us for one row of A (6.4 TB/s), 35 for four; the
 // matrix cores' layout, 16 rows of B a load (product_rows), takes 37 and 40, and 41 against 50 for eight.
-// fp32: 51, 58 for four and 73 for eight, against 91 for nine there.  int8, 4096 rows of 10240: 10 us
-// for any number up to eight there.  The four wavefronts of a workgroup put their sums side by side for
+// fp32: 50, 57 for four and 74 for eight, against 88 for nine there.  int8, 4096 rows of 10240: 10 us,
+// and there 11 for two and 13 for eight.  The four wavefronts of a workgroup put their sums side by side for
 // `done`.
 template <class Op, int MT, bool GATED, bool ALIGNED, class Done>
 __global__ __launch_bounds__(256) void product_tokens(Product p, Done done) {
@@ -884,7 +884,8 @@ hipError_t launch_few_rows(const Product& p, const Done& done, hipStream_t strea
                Op::kElem == 2 && al && tiles >= 256) {
         // A tile a compute unit or more: copies to LDS carry the weights faster than registers.  2 x 10240
         // rows of 4096 bf16: 38 us for 5 to 16 rows, product_rows 41 to 47; 2 x 16384 of 1024: 12 and 13 to
-        // 15.  fp32 is the other way: 139 and 101 for 16 rows; int8 gives no tile a compute unit at usual sizes, and splits need a workspace.
+        // 15.  fp32 is the other way: 139 and 96 for 16 rows; int8 gives no tile a compute unit at
+        // usual sizes, and splits need a workspace.
         Product q = p;
         q.splits = 1;
         return launch_tiles<Op, 64, 64, 2, 2, false, GATED, false, false, true>(q, Plan{64, 64, tiles, 1, 0}, done,

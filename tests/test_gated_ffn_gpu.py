@@ -371,3 +371,27 @@ def test_activations_of_huge_projections(kind, dtype):
     """Far out act(v) is v or 0 and its slope 1 or 0, also where v^2 and v^3 pass fp32's range."""
     v = torch.tensor([1e3, 1e6, 1e13, 1e15, 5e18, 3e19, 1e20, 1e30, 3e38])
     check_act(torch.cat([v, -v]).to(dtype), kind, dtype)
+
+
+def test_through_an_autograd_function():
+    """Calls are not recorded; a Function around one and its backward pass gives the leaves their gradients."""
+
+    class Block(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, wg, wu):
+            h, g, u = rla.gated_ffn(x, wg, wu, "gelu", save=True)
+            ctx.save_for_backward(x, wg, wu, g, u)
+            return h
+
+        @staticmethod
+        def backward(ctx, dh):
+            return rla.gated_ffn_backward(dh, *ctx.saved_tensors, "gelu")
+
+    t = inputs(40, 72, 88, torch.bfloat16, 13)
+    leaves = [t[k].to(DEV).requires_grad_() for k in ("x", "w_gate", "w_up")]
+    assert not rla.gated_ffn(*leaves, "gelu").requires_grad
+    h = Block.apply(*leaves)
+    h.backward(t["dh"].to(DEV))
+    _, g, u = rla.gated_ffn(*leaves, "gelu", save=True)
+    check_forward(t, "gelu", h)
+    check_backward(t, "gelu", g, u, *[v.grad for v in leaves])
