@@ -452,6 +452,70 @@ int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream,
 int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call);
 
 /*
+ * Layer norms before and after a transformer block, fused with the block's gate,
+ * the residual and the norm's own weight, bias and per-sample scale and shift.
+ *
+ * Row tensors and vectors as for ltx3drope_norm: weight and bias [dim]; gate,
+ * scale and shift [batch, dim]; any vector may be NULL (its factor is then 1, its
+ * term 0).  With hat(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps), per
+ * row of sample b and all in fp32:
+ *     r = residual + gate_b * y
+ *     n = (hat(r) * weight + bias) * (1 + scale_b) + shift_b
+ * each output rounded once to `dtype` (n is formed from the unrounded r).  The
+ * squares are taken around the mean, whose own rounding is taken out again, so a
+ * mean that is large beside the row's spread costs no precision.  mean(|v|) and
+ * mean((v - mean(v))^2) have to be finite in fp32 (with an eps below 2^-110 the
+ * sum of the squares): other rows give zeros or NaN.
+ *
+ * after = 1: y, residual, r and n are required.  after = 0 is the norm before a
+ * block alone: n from `residual`; y, gate and r must be NULL.
+ *
+ * Outputs over inputs, empty calls, statuses and reasons as for ltx3drope_norm
+ * (E_INVALID: a NULL descriptor, eps not finite or <= 0, `after` other than 0 or
+ * 1, reserved not 0, a pointer that must be NULL).
+ */
+typedef struct {
+    int32_t dtype, param_dtype;
+    int32_t after, reserved; /* reserved must be 0 */
+    int64_t batch, rows, dim;
+    float eps;
+    const void *y, *residual, *gate, *weight, *bias, *scale, *shift;
+    void *r, *n;
+} ltx3drope_layer_norm_t;
+int ltx3drope_layer_norm(const ltx3drope_layer_norm_t* call, void* stream, int* reason);
+
+/*
+ * The gradients of ltx3drope_layer_norm.  `r` is the forward's output r (after =
+ * 1) or its input (after = 0); dr (may be NULL: zero) is the gradient that reaches
+ * r past the norm, dn that of n.  With v = dn * weight * (1 + scale_b):
+ *     dresidual = dr + (v - mean(v) - hat(r) * mean(v * hat(r))) / sqrt(var(r) + eps)
+ *     dy        = gate_b * dresidual       (from the unrounded dresidual)
+ * and the vectors' gradients, sums over rows (weight and bias: over rows and
+ * samples) held in fp32, in param_dtype.  dresidual is required, dy too with
+ * after = 1; the vectors' gradients may each be NULL, and must be where the vector
+ * itself is, but for dshift and dbias, whose vectors' values no gradient but dscale's
+ * (of bias) needs.  y may be NULL where dgate is.
+ * `workspace`: ltx3drope_layer_norm_backward_workspace bytes, as for
+ * ltx3drope_norm_backward.  Sums are added in a fixed order: equal inputs give
+ * equal bits.  Empty calls write zeros into the vectors' gradients.  Aliasing,
+ * statuses and reasons as above; a workspace that is too small is E_INVALID.
+ */
+typedef struct {
+    int32_t dtype, param_dtype;
+    int32_t after, reserved;
+    int64_t batch, rows, dim;
+    float eps;
+    const void *dr, *dn, *y, *r, *gate, *weight, *bias, *scale;
+    void *dresidual, *dy, *dgate, *dweight, *dbias, *dscale, *dshift;
+    void* workspace;
+    int64_t workspace_bytes;
+} ltx3drope_layer_norm_backward_t;
+int ltx3drope_layer_norm_backward(const ltx3drope_layer_norm_backward_t* call, void* stream, int* reason);
+/* Bytes of workspace for a call (its sizes and which gradients are not NULL; no pointer is looked
+   at), or a negative status for a malformed descriptor. */
+int64_t ltx3drope_layer_norm_backward_workspace(const ltx3drope_layer_norm_backward_t* call);
+
+/*
  * The gated feed-forward block: both projections, the activation and the
  * product in one kernel.
  *     g = x Wg^T,  u = x Wu^T,  h = act(g) * u

@@ -128,3 +128,43 @@ def q8_matmul(a, a_scale, b, b_scale, bias):
     """The product in float64 (integer sums below 2^53 are exact)."""
     y = (a.double() @ b.double().T) * a_scale.double()[:, None] * b_scale.double()
     return y if bias is None else y + bias.double()
+
+
+def layer_norm_parts(x, eps):
+    """hat(x) of a layer norm and its reciprocal root of the variance."""
+    c = x - x.mean(-1, keepdim=True)
+    inv = 1.0 / torch.sqrt((c * c).mean(-1, keepdim=True) + eps)
+    return c * inv, inv
+
+
+def layer_norm_before(x, weight, bias, scale, shift, eps):
+    n = layer_norm_parts(x, eps)[0]
+    if weight is not None:
+        n = n * weight
+    if bias is not None:
+        n = n + bias
+    if scale is not None:
+        n = n * (1.0 + _rowwise(scale))
+    return n if shift is None else n + _rowwise(shift)
+
+
+def layer_norm_residual(y, residual, gate):
+    return residual + (y if gate is None else y * _rowwise(gate))
+
+
+def layer_norm_before_backward(dn, x, weight, bias, scale, dresidual, eps):
+    """dx, dweight, dbias, dscale, dshift (the last four whether or not the vector is there)."""
+    hat, inv = layer_norm_parts(x, eps)
+    v = dn * norm_factor(weight, scale, 0.0, x)
+    dx = inv * (v - v.mean(-1, keepdim=True) - hat * (v * hat).mean(-1, keepdim=True))
+    if dresidual is not None:
+        dx = dx + dresidual
+    p1, p2 = (dn * hat).sum(1), dn.sum(1)
+    s = torch.ones_like(p1) if scale is None else 1.0 + scale
+    dscale = (p1 if weight is None else weight * p1) + (0.0 if bias is None else bias * p2)
+    return dx, (s * p1).sum(0), (s * p2).sum(0), dscale, p2
+
+
+def layer_norm_after_backward(dR, y, gate):
+    """dy, dresidual, dgate for the gradient dR of r = residual + gate * y."""
+    return dR if gate is None else dR * _rowwise(gate), dR, None if gate is None else (dR * y).sum(1)

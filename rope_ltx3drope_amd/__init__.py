@@ -12,8 +12,8 @@ Names follow the sglang PR #35698 page ("Implementation breakdown", steps 1-4;
 can_use() the precheck, apply_qk() the fused one-launch rotation of Q and K and
 forward_pair() the decoder-side entry that ties them together.
 
-Of the transformer block around it: norm_before(), norm_after() and their
-backward passes, gated_ffn() and its backward pass, q8_quantize() and
+Of the transformer block around it: norm_before(), norm_after(),
+layer_norm_before(), layer_norm_after() and their backward passes, gated_ffn() and its backward pass, q8_quantize() and
 q8_matmul().
 
 No call here is recorded by autograd: results never require gradients, whatever
@@ -45,7 +45,8 @@ __all__ = [
     "forward_pair", "kernel_choice", "stats", "stats_reset", "set_option", "get_option", "gate_state", "gate_reset",
     "cache_clear", "copy_bytes", "version", "neox_can_use", "neox_apply_qk", "neox_position_errors", "patchify",
     "unpatchify", "dit_freq_grid", "norm_before", "norm_after", "norm_before_backward", "norm_after_backward",
-    "NormBeforeGrads", "NormAfterGrads", "gated_ffn", "gated_ffn_backward", "q8_quantize", "q8_matmul",
+    "NormBeforeGrads", "NormAfterGrads", "layer_norm_before", "layer_norm_after", "layer_norm_before_backward",
+    "layer_norm_after_backward", "LayerNormBeforeGrads", "LayerNormAfterGrads", "gated_ffn", "gated_ffn_backward", "q8_quantize", "q8_matmul",
 ]
 
 
@@ -637,6 +638,111 @@ def norm_after_backward(dr, dn, y, r, weight=None, gate=None, *, post_norm: bool
                                           residual_scale, stream, "norm_after_backward", dr, dn, y, r, weight, gate,
                                           next_weight, next_scale, next_shift)
     return NormAfterGrads(dy, dresidual, *rest)
+
+
+def _layer_norm(row, size, pd, after, eps, stream, what, *tensors):
+    reason = ctypes.c_int(0)
+    _lib.lib()
+    st = _lib.layer_norm(_lib.LAYER_NORM_BYTES.pack(_dtype_codes[row.dtype], pd, after, 0, *size, eps,
+                                                    *[0 if t is None else t.data_ptr() for t in tensors]),
+                         _raw_stream(row.get_device(), stream), ctypes.byref(reason))
+    _finish(st, reason, what)
+
+
+def layer_norm_before(x, weight=None, bias=None, scale=None, shift=None, *, eps: float = 1e-6, out=None, stream=None):
+    """The layer norm before a block: (hat(x) * weight + bias) * (1 + scale) + shift, one pass, with
+    hat(x) = (x - mean(x)) / sqrt(var(x) + eps) a row.
+
+    x [batch, rows, dim] or [rows, dim] (one sample), float32 or bfloat16; weight and bias [dim]; scale
+    and shift [batch, dim], one row a sample; the vectors float32 or x's dtype, any of them None.  out
+    may be x itself."""
+    size = _rows_marshal(x, (out,))
+    pd = _vectors_marshal(x, size, (weight, bias), (scale, shift))
+    if out is None:
+        out = _empty(stream, lambda: _torch().empty_like(x))
+    _layer_norm(x, size, pd, 0, eps, stream, "layer_norm_before", None, x, None, weight, bias, scale, shift, None, out)
+    return out
+
+
+def layer_norm_after(y, residual, gate=None, *, weight=None, bias=None, scale=None, shift=None, eps: float = 1e-6,
+                     r_out=None, n_out=None, stream=None):
+    """After a block, in one pass: (r, n) with r = residual + gate * y and n the next block's
+    layer_norm_before(r, weight, bias, scale, shift), formed from r before r is rounded to its dtype.
+
+    y, residual [batch, rows, dim] or [rows, dim]; weight, bias [dim]; gate, scale, shift [batch, dim].
+    r_out may be residual and n_out may be y."""
+    size = _rows_marshal(y, (residual, r_out, n_out))
+    pd = _vectors_marshal(y, size, (weight, bias), (gate, scale, shift))
+    if r_out is None:
+        r_out = _torch().empty_like(y) if stream is None else _empty(stream, lambda: _torch().empty_like(y))
+    if n_out is None:
+        n_out = _torch().empty_like(y) if stream is None else _empty(stream, lambda: _torch().empty_like(y))
+    _layer_norm(y, size, pd, 1, eps, stream, "layer_norm_after", y, residual, gate, weight, bias, scale, shift, r_out,
+                n_out)
+    return r_out, n_out
+
+
+class LayerNormBeforeGrads(NamedTuple):
+    """Gradients of layer_norm_before; None where the vector was not given."""
+
+    dx: object
+    dweight: object
+    dbias: object
+    dscale: object
+    dshift: object
+
+
+class LayerNormAfterGrads(NamedTuple):
+    """Gradients of layer_norm_after; None where the vector was not given."""
+
+    dy: object
+    dresidual: object
+    dgate: object
+    dweight: object
+    dbias: object
+    dscale: object
+    dshift: object
+
+
+def _layer_norm_backward(row, size, pd, after, eps, stream, what, dr, dn, y, r, gate, weight, bias, scale, shift):
+    torch = _torch()
+    _lib.lib()
+
+    def outputs():
+        like = [torch.empty_like(row), torch.empty_like(row) if after else None]
+        return like + [None if t is None else torch.empty_like(t) for t in (gate, weight, bias, scale, shift)]
+
+    outs = _empty(stream, outputs)
+    head = (_dtype_codes[row.dtype], pd, after, 0, *size, eps,
+            *[_ptr(t) for t in (dr, dn, y, r, gate, weight, bias, scale, *outs)])
+    pack = _lib.LAYER_NORM_BACKWARD_BYTES.pack
+    ws, n = _workspace(stream, _lib.layer_norm_backward_workspace, pack(*head, 0, 0), row.device)
+    reason = ctypes.c_int(0)
+    st = _lib.layer_norm_backward(pack(*head, _ptr(ws), n), _raw_stream(row.get_device(), stream), ctypes.byref(reason))
+    _finish(st, reason, what)
+    return outs
+
+
+def layer_norm_before_backward(dn, x, weight=None, bias=None, scale=None, shift=None, *, dresidual=None,
+                               eps: float = 1e-6, stream=None) -> LayerNormBeforeGrads:
+    """Gradients of layer_norm_before at x for the output's gradient dn.  dresidual, if given, is what
+    reaches x past the block and is added to dx.  shift only asks for its gradient."""
+    size = _rows_marshal(dn, (x, dresidual))
+    pd = _vectors_marshal(dn, size, (weight, bias), (scale, shift))
+    dx, _, _, *rest = _layer_norm_backward(dn, size, pd, 0, eps, stream, "layer_norm_before_backward", dresidual, dn,
+                                           None, x, None, weight, bias, scale, shift)
+    return LayerNormBeforeGrads(dx, *rest)
+
+
+def layer_norm_after_backward(dr, dn, y, r, gate=None, *, weight=None, bias=None, scale=None, shift=None,
+                              eps: float = 1e-6, stream=None) -> LayerNormAfterGrads:
+    """Gradients of layer_norm_after for the gradients dr of r (None: zero) and dn of n; r is the forward's
+    output.  y is needed for the gate's gradient only (None without a gate).  shift only asks for its gradient."""
+    size = _rows_marshal(dn, (dr, y, r))
+    pd = _vectors_marshal(dn, size, (weight, bias), (gate, scale, shift))
+    dresidual, dy, *rest = _layer_norm_backward(dn, size, pd, 1, eps, stream, "layer_norm_after_backward", dr, dn, y, r,
+                                                gate, weight, bias, scale, shift)
+    return LayerNormAfterGrads(dy, dresidual, *rest)
 
 
 def _activation(name: str) -> int:

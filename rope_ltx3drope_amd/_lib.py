@@ -52,6 +52,7 @@ EXPORTS = (
     "ltx3drope_gated_ffn", "ltx3drope_gated_ffn_workspace", "ltx3drope_gated_ffn_backward",
     "ltx3drope_gated_ffn_backward_workspace", "ltx3drope_q8_quantize", "ltx3drope_q8_matmul",
     "ltx3drope_q8_matmul_workspace",
+    "ltx3drope_layer_norm", "ltx3drope_layer_norm_backward", "ltx3drope_layer_norm_backward_workspace",
 )
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -97,6 +98,21 @@ class NormBackward(ctypes.Structure):
         ("workspace_bytes", i64)]
 
 
+_LAYER_NORM_SCALARS = [(n, ctypes.c_int32) for n in ("dtype", "param_dtype", "after", "reserved")] + [
+    (n, i64) for n in ("batch", "rows", "dim")] + [("eps", ctypes.c_float)]
+
+
+class LayerNorm(ctypes.Structure):
+    _fields_ = _LAYER_NORM_SCALARS + [(n, vp) for n in (
+        "y", "residual", "gate", "weight", "bias", "scale", "shift", "r", "n")]
+
+
+class LayerNormBackward(ctypes.Structure):
+    _fields_ = _LAYER_NORM_SCALARS + [(n, vp) for n in (
+        "dr", "dn", "y", "r", "gate", "weight", "bias", "scale",
+        "dresidual", "dy", "dgate", "dweight", "dbias", "dscale", "dshift", "workspace")] + [("workspace_bytes", i64)]
+
+
 _FFN_SIZES = [("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)] + [(n, i64) for n in (
     "tokens", "dim", "hidden")]
 
@@ -121,21 +137,25 @@ class Q8Matmul(ctypes.Structure):
 # tenth of the time of filling a ctypes.Structure by name.
 NORM_BYTES = struct.Struct("@6i3q3f9P")
 NORM_BACKWARD_BYTES = struct.Struct("@6i3q3f16Pq")
+LAYER_NORM_BYTES = struct.Struct("@4i3qf9P")
+LAYER_NORM_BACKWARD_BYTES = struct.Struct("@4i3qf16Pq")
 FFN_BYTES = struct.Struct("@2i3q7Pq")
 FFN_BACKWARD_BYTES = struct.Struct("@2i3q10Pq")
 Q8_BYTES = struct.Struct("@2i3q7Pq")
 
 # entry points that take a descriptor as bytes (bound in lib())
-norm = norm_backward = gated_ffn = gated_ffn_backward = q8_matmul = None
-norm_backward_workspace = gated_ffn_workspace = gated_ffn_backward_workspace = q8_matmul_workspace = None
+norm = norm_backward = layer_norm = layer_norm_backward = gated_ffn = gated_ffn_backward = q8_matmul = None
+norm_backward_workspace = layer_norm_backward_workspace = gated_ffn_workspace = gated_ffn_backward_workspace = None
+q8_matmul_workspace = None
 
 
 def _bind_bytes(L) -> None:
     call = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, vp, vp)
     size = ctypes.CFUNCTYPE(i64, ctypes.c_char_p)
-    for name in ("norm", "norm_backward", "gated_ffn", "gated_ffn_backward", "q8_matmul"):
+    for name in ("norm", "norm_backward", "layer_norm", "layer_norm_backward", "gated_ffn", "gated_ffn_backward",
+                 "q8_matmul"):
         globals()[name] = call(("ltx3drope_" + name, L))
-        if name != "norm":
+        if name not in ("norm", "layer_norm"):
             globals()[name + "_workspace"] = size((f"ltx3drope_{name}_workspace", L))
 
 
@@ -203,6 +223,10 @@ def lib() -> ctypes.CDLL:
             "ltx3drope_norm_backward": (ctypes.c_int, [ctypes.POINTER(NormBackward), vp,
                                                        ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_norm_backward_workspace": (i64, [ctypes.POINTER(NormBackward)]),
+            "ltx3drope_layer_norm": (ctypes.c_int, [ctypes.POINTER(LayerNorm), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_layer_norm_backward": (ctypes.c_int, [ctypes.POINTER(LayerNormBackward), vp,
+                                                             ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_layer_norm_backward_workspace": (i64, [ctypes.POINTER(LayerNormBackward)]),
             "ltx3drope_gated_ffn": (ctypes.c_int, [ctypes.POINTER(GatedFfn), vp, ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_gated_ffn_workspace": (i64, [ctypes.POINTER(GatedFfn)]),
             "ltx3drope_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(GatedFfnBackward), vp,

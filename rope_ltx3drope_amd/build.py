@@ -39,6 +39,7 @@ SOURCES = [  # (file, language, extra flags)
     ("patchify.hip", "hip", DEVICE),
     ("dit_freqs.hip", "hip", DEVICE),
     ("norm.hip", "hip", DEVICE),
+    ("layer_norm.hip", "hip", DEVICE),
     ("ffn.hip", "hip", DEVICE),
     ("q8.hip", "hip", DEVICE),
     ("api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),

@@ -1,5 +1,5 @@
 // The transformer-block operators: what the host side (block_api.cpp) hands to the kernel launchers
-// (norm.hip, ffn.hip, q8.hip).  Sizes fit in 32 bits unless they are size_t; offsets into tensors are formed in 64.
+// (norm.hip, layer_norm.hip, ffn.hip, q8.hip).  Sizes fit in 32 bits unless they are size_t; offsets into tensors are formed in 64.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -46,6 +46,29 @@ constexpr int64_t kNormMaxBatch = 65535;  // one grid row a sample
 hipError_t launch_norm_forward(const NormForward& p, bool f32, bool vec, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackward& p, bool f32, bool vec, hipStream_t stream);
 size_t norm_backward_workspace(uint32_t batch, uint32_t rows, uint32_t dim);
+
+// The layer norms (layer_norm.hip), in the same shapes: r is the norm's input, gate, scale and shift are
+// [batch, dim], weight and bias [dim].
+struct LayerNormForward {
+    const void *y, *residual, *gate, *weight, *bias, *scale, *shift;
+    void *r, *n;
+    uint32_t batch, rows, dim;
+    float eps, square_scale;
+    bool after, param_f32, chunks;
+};
+
+struct LayerNormBackward {
+    const void *dr, *dn, *y, *r, *gate, *weight, *bias, *scale;
+    void *dresidual, *dy, *dgate, *dweight, *dbias, *dscale, *dshift;
+    float* partial;  // [3][batch][parts][dim], NULL when no vector's gradient is asked for
+    uint32_t batch, rows, dim;
+    float eps, square_scale;
+    bool after, param_f32, chunks;
+};
+
+// The backward's workspace is norm_backward_workspace's.
+hipError_t launch_layer_norm_forward(const LayerNormForward& p, bool f32, bool vec, hipStream_t stream);
+hipError_t launch_layer_norm_backward(const LayerNormBackward& p, bool f32, bool vec, hipStream_t stream);
 
 // The gated feed-forward block (ffn.hip).  x [tokens, dim], weights [hidden, dim], h, g, u and dh
 // [tokens, hidden], g and u in fp32.  activation: LTX3DROPE_ACT_*.

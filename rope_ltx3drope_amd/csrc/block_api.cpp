@@ -75,6 +75,20 @@ bool flag(int32_t v) { return v == 0 || v == 1; }
 
 size_t elem(int dtype) { return dtype == LTX3DROPE_DTYPE_F32 ? 4 : 2; }
 
+// The sizes and types that the norms share: OK, or the reason of a refusal.
+template <class Call>
+int check_rows(const Call& c, bool per_sample) {
+    if ((c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) ||
+        (c.param_dtype != LTX3DROPE_DTYPE_F32 && c.param_dtype != c.dtype))
+        return LTX3DROPE_REASON_DTYPE;
+    if (c.dim <= 0 || c.batch < 0 || c.rows < 0) return LTX3DROPE_REASON_NONPOSITIVE_DIM;
+    const int64_t lim = int64_t(1) << 31;
+    if (c.dim > kNormMaxDim || c.batch >= lim || c.rows >= lim || (c.rows != 0 && c.batch > (lim - 1) / c.rows) ||
+        (per_sample && c.batch > kNormMaxBatch))
+        return LTX3DROPE_REASON_TOO_LARGE;
+    return LTX3DROPE_REASON_OK;
+}
+
 // The scalars that both directions of the norm share: a status, and for E_UNSUPPORTED the reason.
 template <class Call>
 int check_norm(const Call& c, bool per_sample, int* why) {
@@ -83,22 +97,8 @@ int check_norm(const Call& c, bool per_sample, int* why) {
         return LTX3DROPE_E_INVALID;
     if (!c.after && (c.post_norm || !c.next_norm || c.residual_scale != 1.f || c.y || c.weight || c.gate))
         return LTX3DROPE_E_INVALID;
-    if ((c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) ||
-        (c.param_dtype != LTX3DROPE_DTYPE_F32 && c.param_dtype != c.dtype)) {
-        *why = LTX3DROPE_REASON_DTYPE;
-        return LTX3DROPE_E_UNSUPPORTED;
-    }
-    if (c.dim <= 0 || c.batch < 0 || c.rows < 0) {
-        *why = LTX3DROPE_REASON_NONPOSITIVE_DIM;
-        return LTX3DROPE_E_UNSUPPORTED;
-    }
-    const int64_t lim = int64_t(1) << 31;
-    if (c.dim > kNormMaxDim || c.batch >= lim || c.rows >= lim || (c.rows != 0 && c.batch > (lim - 1) / c.rows) ||
-        (per_sample && c.batch > kNormMaxBatch)) {
-        *why = LTX3DROPE_REASON_TOO_LARGE;
-        return LTX3DROPE_E_UNSUPPORTED;
-    }
-    return LTX3DROPE_OK;
+    *why = check_rows(c, per_sample);
+    return *why == LTX3DROPE_REASON_OK ? LTX3DROPE_OK : LTX3DROPE_E_UNSUPPORTED;
 }
 
 bool norm_per_sample(const ltx3drope_norm_backward_t& c) {
@@ -109,6 +109,28 @@ size_t norm_workspace(const ltx3drope_norm_backward_t& c) {
     if (!c.dweight && !c.dgate && !c.dnext_weight && !c.dnext_scale && !c.dnext_shift) return 0;
     if (c.batch == 0 || c.rows == 0) return 0;
     const bool per_sample = norm_per_sample(c);
+    return norm_backward_workspace(static_cast<uint32_t>(per_sample ? c.batch : 1),
+                                   static_cast<uint32_t>(per_sample ? c.rows : c.batch * c.rows),
+                                   static_cast<uint32_t>(c.dim));
+}
+
+// The layer norms' scalars, both directions.
+template <class Call>
+int check_layer_norm(const Call& c, bool per_sample, int* why) {
+    if (!flag(c.after) || c.reserved != 0 || !std::isfinite(c.eps) || c.eps <= 0.f) return LTX3DROPE_E_INVALID;
+    if (!c.after && (c.y || c.gate)) return LTX3DROPE_E_INVALID;
+    *why = check_rows(c, per_sample);
+    return *why == LTX3DROPE_REASON_OK ? LTX3DROPE_OK : LTX3DROPE_E_UNSUPPORTED;
+}
+
+bool layer_norm_per_sample(const ltx3drope_layer_norm_backward_t& c) {
+    return c.gate || c.scale || c.dgate || c.dscale || c.dshift;
+}
+
+size_t layer_norm_workspace(const ltx3drope_layer_norm_backward_t& c) {
+    if (!c.dgate && !c.dweight && !c.dbias && !c.dscale && !c.dshift) return 0;
+    if (c.batch == 0 || c.rows == 0) return 0;
+    const bool per_sample = layer_norm_per_sample(c);
     return norm_backward_workspace(static_cast<uint32_t>(per_sample ? c.batch : 1),
                                    static_cast<uint32_t>(per_sample ? c.rows : c.batch * c.rows),
                                    static_cast<uint32_t>(c.dim));
@@ -366,6 +388,144 @@ int ltx3drope_norm_backward(const ltx3drope_norm_backward_t* call, void* stream,
     p.chunks = aligned16(t, {Role::Param}) && vec % 16 == 0;
     DeviceGuard guard(device);
     if (launch_norm_backward(p, f32, vectors, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int ltx3drope_layer_norm(const ltx3drope_layer_norm_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_layer_norm_t& c = *call;
+    const bool per_sample = c.gate || c.scale || c.shift;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_layer_norm(c, per_sample, &why);
+    if (st == LTX3DROPE_E_UNSUPPORTED) return refuse(why, reason);
+    if (st != LTX3DROPE_OK) return st;
+    if (!c.after && c.r) return LTX3DROPE_E_INVALID;
+    if (c.batch == 0 || c.rows == 0) return LTX3DROPE_OK;
+    if (!c.residual || !c.n || (c.after && (!c.y || !c.r))) return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t es = elem(c.dtype), ps = elem(c.param_dtype);
+    const size_t row = static_cast<size_t>(c.batch * c.rows) * static_cast<size_t>(c.dim) * es;
+    const size_t vec = static_cast<size_t>(c.dim) * ps, vecs = vec * static_cast<size_t>(c.batch);
+    Spans t;
+    t.add(c.residual, row, es, Role::RowIn);
+    t.add(c.y, row, es, Role::RowIn);
+    t.add(c.r, row, es, Role::RowOut);
+    t.add(c.n, row, es, Role::RowOut);
+    t.add(c.weight, vec, ps, Role::Param);
+    t.add(c.bias, vec, ps, Role::Param);
+    t.add(c.gate, vecs, ps, Role::Param);
+    t.add(c.scale, vecs, ps, Role::Param);
+    t.add(c.shift, vecs, ps, Role::Param);
+    int device = -1;
+    why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    LayerNormForward p;
+    p.y = c.y;
+    p.residual = c.residual;
+    p.gate = c.gate;
+    p.weight = c.weight;
+    p.bias = c.bias;
+    p.scale = c.scale;
+    p.shift = c.shift;
+    p.r = c.r;
+    p.n = c.n;
+    p.batch = static_cast<uint32_t>(per_sample ? c.batch : 1);
+    p.rows = static_cast<uint32_t>(per_sample ? c.rows : c.batch * c.rows);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.eps = c.eps;
+    p.square_scale = norm_square_scale(c.eps);
+    p.after = c.after != 0;
+    p.param_f32 = c.param_dtype == LTX3DROPE_DTYPE_F32;
+    const bool f32 = c.dtype == LTX3DROPE_DTYPE_F32;
+    const bool vectors = aligned16(t, {Role::RowIn, Role::RowOut}) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
+    p.chunks = aligned16(t, {Role::Param}) && vec % 16 == 0;
+    DeviceGuard guard(device);
+    if (launch_layer_norm_forward(p, f32, vectors, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int64_t ltx3drope_layer_norm_backward_workspace(const ltx3drope_layer_norm_backward_t* call) {
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_layer_norm(*call, layer_norm_per_sample(*call), &why);
+    return st == LTX3DROPE_OK ? static_cast<int64_t>(layer_norm_workspace(*call)) : st;
+}
+
+int ltx3drope_layer_norm_backward(const ltx3drope_layer_norm_backward_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_layer_norm_backward_t& c = *call;
+    const bool per_sample = layer_norm_per_sample(c);
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_layer_norm(c, per_sample, &why);
+    if (st == LTX3DROPE_E_UNSUPPORTED) return refuse(why, reason);
+    if (st != LTX3DROPE_OK) return st;
+    if ((!c.after && (c.dy || c.dgate)) || (c.dgate && !c.gate) || (c.dweight && !c.weight) || (c.dscale && !c.scale))
+        return LTX3DROPE_E_INVALID;
+    const size_t ws = layer_norm_workspace(c);
+    if (c.workspace_bytes < 0 || static_cast<size_t>(c.workspace_bytes) < ws) return LTX3DROPE_E_INVALID;
+    const bool empty = c.batch == 0 || c.rows == 0, need_y = c.dgate != nullptr;
+    if (!empty && (!c.dresidual || !c.dn || !c.r || (c.after && !c.dy) || (need_y && !c.y) || (ws != 0 && !c.workspace)))
+        return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t es = elem(c.dtype), ps = elem(c.param_dtype);
+    const size_t row = static_cast<size_t>(c.batch * c.rows) * static_cast<size_t>(c.dim) * es;
+    const size_t vec = static_cast<size_t>(c.dim) * ps, vecs = vec * static_cast<size_t>(c.batch);
+    Spans t;
+    t.add(c.dr, row, es, Role::RowIn);
+    t.add(c.dn, row, es, Role::RowIn);
+    if (need_y) t.add(c.y, row, es, Role::RowIn);
+    t.add(c.r, row, es, Role::RowIn);
+    t.add(c.dresidual, row, es, Role::RowOut);
+    t.add(c.dy, row, es, Role::RowOut);
+    if (!empty) {
+        t.add(c.weight, vec, ps, Role::Param);
+        t.add(c.bias, vec, ps, Role::Param);
+        t.add(c.gate, vecs, ps, Role::Param);
+        t.add(c.scale, vecs, ps, Role::Param);
+    }
+    t.add(c.dweight, vec, ps, Role::ParamOut);
+    t.add(c.dbias, vec, ps, Role::ParamOut);
+    t.add(c.dgate, vecs, ps, Role::ParamOut);
+    t.add(c.dscale, vecs, ps, Role::ParamOut);
+    t.add(c.dshift, vecs, ps, Role::ParamOut);
+    if (ws != 0) t.add(c.workspace, ws, 16, Role::Scratch);
+    if (t.n == 0) return LTX3DROPE_OK;  // an empty call without a vector's gradient
+    int device = -1;
+    why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    LayerNormBackward p;
+    p.dr = c.dr;
+    p.dn = c.dn;
+    p.y = need_y ? c.y : nullptr;
+    p.r = c.r;
+    p.gate = c.gate;
+    p.weight = c.weight;
+    p.bias = c.bias;
+    p.scale = c.scale;
+    p.dresidual = c.dresidual;
+    p.dy = c.dy;
+    p.dgate = c.dgate;
+    p.dweight = c.dweight;
+    p.dbias = c.dbias;
+    p.dscale = c.dscale;
+    p.dshift = c.dshift;
+    p.partial = ws != 0 ? static_cast<float*>(c.workspace) : nullptr;
+    p.batch = static_cast<uint32_t>(per_sample ? c.batch : 1);
+    p.rows = static_cast<uint32_t>(per_sample ? c.rows : c.batch * c.rows);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.eps = c.eps;
+    p.square_scale = norm_square_scale(c.eps);
+    p.after = c.after != 0;
+    p.param_f32 = c.param_dtype == LTX3DROPE_DTYPE_F32;
+    const bool f32 = c.dtype == LTX3DROPE_DTYPE_F32;
+    const bool vectors = aligned16(t, {Role::RowIn, Role::RowOut}) && (static_cast<size_t>(c.dim) * es) % 16 == 0;
+    p.chunks = aligned16(t, {Role::Param}) && vec % 16 == 0;
+    DeviceGuard guard(device);
+    if (launch_layer_norm_backward(p, f32, vectors, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return LTX3DROPE_E_HIP;
     count_launch();
     return LTX3DROPE_OK;
 }

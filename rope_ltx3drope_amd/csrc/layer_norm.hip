@@ -1,0 +1,377 @@
+// Layer norms before and after a transformer block, fused with the block's gate, the residual and the
+// norm's own weight, bias and per-sample scale and shift; and their backward pass.
+//
+// Per row of width D (rows of sample b), all in fp32:
+//     r      = residual + gate_b * y                     (before a block: r is the input itself)
+//     hat(r) = (r - mean(r)) * rstd,  rstd = 1 / sqrt(mean((r - mean(r))^2) + eps)
+//     n      = (hat(r) * w + bias) * (1 + scale_b) + shift_b
+//
+// Backward, with v = dn * w * (1 + scale_b):
+//     dR = dr + rstd * (v - mean(v) - hat(r) * mean(v * hat(r)))     (dr: what reaches r past the norm)
+//     dresidual = dR,  dy = gate_b * dR
+// and per sample P1 = sum_rows dn * hat(r), P2 = sum_rows dn, P3 = sum_rows dR * y, from which
+//     dscale_b = w P1 + bias P2, dshift_b = P2, dw = sum_b (1 + scale_b) P1,
+//     dbias = sum_b (1 + scale_b) P2, dgate_b = P3.
+//
+// The mean is taken first and the squares around it: their difference would lose what a row with a large
+// mean has left.  fp32 rounds that mean by up to 2^-24 of it, which may be many times the row's spread, so
+// the sum of the differences, which would be zero, goes along with that of their squares and takes
+// the rounding out again: d = r - mean', e = mean(d), var = mean(d^2) - e^2, hat = (d - e) * rstd.
+//
+// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.
+#include <hip/hip_runtime.h>
+
+#include <utility>
+
+#include "block.h"
+#include "rows.h"
+
+namespace ltx3drope {
+namespace {
+
+// The sum of a thread's values times 2^-14, which stays in fp32's range wherever the row's mean does (a row
+// has at most 2^14 values); scaled as a whole unless a wavefront's sum passes the range.
+constexpr float kSumScale = 0x1p-14f;
+static_assert(kNormMaxDim == 1 << 14, "kSumScale takes a row's length out of its sum");
+
+template <int E>
+__device__ __forceinline__ float scaled_sum(const float (&v)[E]) {
+    float even = 0.f, odd = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+        even += v[k];
+        odd += v[k + 1];
+    }
+    const float s = (even + odd) * kSumScale;
+    if (__builtin_expect(!__any(!(fabsf(s) < __builtin_inff())), 1)) return s;
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) t = fmaf(v[k], kSumScale, t);
+    return t;
+}
+
+// r less its mean as fp32 has it, with zeros past the row's end (where r is zero).
+template <bool F32, int E, bool VEC>
+__device__ __forceinline__ void subtract(float (&r)[E], float mean, uint32_t t, uint32_t T, uint32_t D) {
+    constexpr int V = RowPart<F32, E, VEC>::V;
+#pragma unroll
+    for (int i = 0; i < E / V; ++i) {
+        const float m = (i * T + t) * V < D ? mean : 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) r[i * V + j] -= m;
+    }
+}
+
+// mean((d - e)^2) from mean(d^2) and e = mean(d): no less than zero, which the rounding of two equal numbers
+// may miss (a row of equal large values).
+__device__ __forceinline__ float variance(float squares, float e) { return fmaxf(fmaf(-e, e, squares), 0.f); }
+
+// The norm's factor w * (1 + scale_b) and, if asked for, its term bias * (1 + scale_b) + shift_b.
+template <bool F32, int E, bool VEC, class Call>
+__device__ __forceinline__ void load_factor(float (&f)[E], float* term, const Call& p, const void* shift, uint32_t b,
+                                            uint32_t t, uint32_t T) {
+    const size_t first = static_cast<size_t>(b) * p.dim;
+    float s[E];
+    load_params<F32, E, VEC>(f, p.weight, 0, p.param_f32, p.chunks, 1.f, t, T, p.dim);
+    load_params<F32, E, VEC>(s, p.scale, first, p.param_f32, p.chunks, 0.f, t, T, p.dim);
+#pragma unroll
+    for (int k = 0; k < E; ++k) f[k] *= 1.f + s[k];
+    if (term == nullptr) return;
+    float bias[E], sh[E];
+    load_params<F32, E, VEC>(bias, p.bias, 0, p.param_f32, p.chunks, 0.f, t, T, p.dim);
+    load_params<F32, E, VEC>(sh, shift, first, p.param_f32, p.chunks, 0.f, t, T, p.dim);
+#pragma unroll
+    for (int k = 0; k < E; ++k) term[k] = fmaf(bias[k], 1.f + s[k], sh[k]);
+}
+
+template <bool F32, int E, bool VEC, bool AFTER>
+__global__ __launch_bounds__(1024) void layer_norm_forward(LayerNormForward p) {
+    __shared__ float lds[2][3 * kMaxWaves];
+    const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
+    const uint32_t D = p.dim, b = blockIdx.y;
+    const float sq = p.square_scale, inv_d = 1.0f / static_cast<float>(D);
+    const float inv_sum = inv_d / kSumScale, inv_sq = inv_d / sq;  // powers of two
+
+    constexpr size_t es = F32 ? 4 : 2;
+    const uint32_t step = gridDim.x * G;
+    RowPart<F32, E, VEC> yr, rr;
+    auto load = [&](uint32_t s) {
+        const size_t off = (static_cast<size_t>(b) * p.rows + s) * D * es;
+        if (s < p.rows) {
+            if constexpr (AFTER) yr.load(static_cast<const char*>(p.y) + off, t, T, D);
+            rr.load(static_cast<const char*>(p.residual) + off, t, T, D);
+        } else {
+            if constexpr (AFTER) yr.clear();
+            rr.clear();
+        }
+    };
+    load(blockIdx.x * G + g);
+    float fy[AFTER ? E : 1], fn[E], sh[E];
+    if constexpr (AFTER)
+        load_params<F32, E, VEC>(fy, p.gate, static_cast<size_t>(b) * D, p.param_f32, p.chunks, 1.f, t, T, D);
+    load_factor<F32, E, VEC>(fn, sh, p, p.shift, b, t, T);
+    int phase = 0;
+    for (uint32_t s0 = blockIdx.x * G; s0 < p.rows; s0 += step, phase ^= 1) {
+        const uint32_t s = s0 + g;
+        const bool live = s < p.rows;  // every thread keeps the barriers
+        const size_t off = (static_cast<size_t>(b) * p.rows + s) * D * es;
+        float r[E];
+        rr.unpack(r);
+        if constexpr (AFTER) {
+            float y[E];
+            yr.unpack(y);
+#pragma unroll
+            for (int k = 0; k < E; ++k) r[k] = fmaf(y[k], fy[k], r[k]);
+        }
+        load(s + step);  // the next row travels while this one is summed
+        if constexpr (AFTER)
+            if (live) store_row<F32, E, VEC>(static_cast<char*>(p.r) + off, r, t, T, D);
+        float sum[1] = {scaled_sum(r)};
+        row_sum(sum, lds[phase], t, T, g);
+        subtract<F32, E, VEC>(r, sum[0] * inv_sum, t, T, D);
+        float ss[2] = {scaled_sum(r), square_sum(r, sq)};
+        row_sum(ss, lds[phase] + kMaxWaves, t, T, g);
+        const float e = ss[0] * inv_sum;
+        const float rstd = rsqrtf(variance(ss[1] * inv_sq, e) + p.eps);
+#pragma unroll
+        for (int k = 0; k < E; ++k) r[k] = fmaf((r[k] - e) * rstd, fn[k], sh[k]);
+        if (live) store_row<F32, E, VEC>(static_cast<char*>(p.n) + off, r, t, T, D);
+    }
+}
+
+template <bool F32, int E, bool VEC, bool AFTER>
+__global__ __launch_bounds__(1024) void layer_norm_backward(LayerNormBackward p) {
+    __shared__ float lds[2][5 * kMaxWaves];
+    extern __shared__ float cols[];  // (G - 1) * D: the rows' partial sums on their way to row 0
+    const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
+    const uint32_t D = p.dim, b = blockIdx.y;
+    const float sq = p.square_scale, inv_d = 1.0f / static_cast<float>(D);
+    const float inv_sum = inv_d / kSumScale, inv_sq = inv_d / sq;
+
+    float fy[AFTER ? E : 1], fn[E];
+    float p1[E] = {}, p2[E] = {}, p3[AFTER ? E : 1] = {};
+    if constexpr (AFTER)
+        load_params<F32, E, VEC>(fy, p.gate, static_cast<size_t>(b) * D, p.param_f32, p.chunks, 1.f, t, T, D);
+    load_factor<F32, E, VEC>(fn, nullptr, p, nullptr, b, t, T);
+
+    constexpr size_t es = F32 ? 4 : 2;
+    const uint32_t step = gridDim.x * G;
+    int phase = 0;
+    for (uint32_t s0 = blockIdx.x * G; s0 < p.rows; s0 += step, phase ^= 1) {
+        const uint32_t s = s0 + g;
+        const bool live = s < p.rows;
+        const size_t off = (static_cast<size_t>(b) * p.rows + s) * D * es;
+        float d[E], r[E], dn[E];
+        RowPart<F32, E, VEC> raw_d, raw_y, raw_r, raw_n;
+        auto get = [&](RowPart<F32, E, VEC>& to, const void* from) {
+            if (live && from) to.load(static_cast<const char*>(from) + off, t, T, D);
+            else to.clear();
+        };
+        get(raw_r, p.r);
+        get(raw_n, p.dn);
+        get(raw_d, p.dr);
+        if constexpr (AFTER) get(raw_y, p.y);
+        raw_r.unpack(r);
+        raw_n.unpack(dn);
+        float sum[1] = {scaled_sum(r)};
+        row_sum(sum, lds[phase], t, T, g);
+        subtract<F32, E, VEC>(r, sum[0] * inv_sum, t, T, D);
+        float ss[4] = {scaled_sum(r), square_sum(r, sq), 0.f, 0.f};  // ..., v, v.(r - mean)
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const float v = dn[k] * fn[k];
+            ss[2] += v;
+            ss[3] = fmaf(v, r[k], ss[3]);
+        }
+        row_sum(ss, lds[phase] + kMaxWaves, t, T, g);
+        const float e = ss[0] * inv_sum;
+        const float rstd = rsqrtf(variance(ss[1] * inv_sq, e) + p.eps);
+        const float mean_v = ss[2] * inv_d;
+        const float proj = fmaf(-e, ss[2], ss[3]) * rstd * inv_d;  // mean(v * hat(r))
+        raw_d.unpack(d);
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const float hat = (r[k] - e) * rstd;
+            p1[k] = fmaf(dn[k], hat, p1[k]);
+            p2[k] += dn[k];
+            d[k] = fmaf(rstd, fmaf(-hat, proj, fmaf(dn[k], fn[k], -mean_v)), d[k]);
+        }
+        if (live) store_row<F32, E, VEC>(static_cast<char*>(p.dresidual) + off, d, t, T, D);
+        if constexpr (AFTER) {
+            float y[E];
+            raw_y.unpack(y);
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                p3[k] = fmaf(d[k], y[k], p3[k]);
+                d[k] *= fy[k];
+            }
+            if (live) store_row<F32, E, VEC>(static_cast<char*>(p.dy) + off, d, t, T, D);
+        }
+    }
+
+    // one partial row a workgroup: partial[which][b][part][D]
+    if (p.partial == nullptr) return;
+    const size_t plane = static_cast<size_t>(p.batch) * gridDim.x * D;
+    float* out = p.partial + (static_cast<size_t>(b) * gridDim.x + blockIdx.x) * D;
+    auto leave = [&](const float* v, int which) {
+        if (G > 1) {
+            __syncthreads();
+            if (g > 0) {
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const uint32_t c = column<F32, E, VEC>(k, t, T);
+                    if (c < D) cols[(g - 1) * D + c] = v[k];
+                }
+            }
+            __syncthreads();
+        }
+        if (g == 0) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const uint32_t c = column<F32, E, VEC>(k, t, T);
+                if (c >= D) continue;
+                float s = v[k];
+                for (uint32_t o = 1; o < G; ++o) s += cols[(o - 1) * D + c];
+                out[which * plane + c] = s;
+            }
+        }
+    };
+    leave(p1, 0);
+    leave(p2, 1);
+    if constexpr (AFTER)
+        if (p.dgate) leave(p3, 2);
+}
+
+// Sums over the partial rows and from them the gradients: blockIdx.z = 0 the norm's (P1 and P2), 1 the
+// gate's (P3); kCols columns a workgroup, kLanes threads down the parts.  A workgroup goes through all
+// samples, and adds up the weight's and the bias's gradients on the way, where they are few (gridDim.y
+// = 1); else each has its own workgroup and leaves its part in partial row 0 for
+// layer_norm_backward_weights.
+__global__ __launch_bounds__(kCols* kLanes) void layer_norm_backward_join(LayerNormBackward p, uint32_t parts) {
+    __shared__ float lds[kLanes][kCols + 1];
+    const bool gate = blockIdx.z == 1;
+    const uint32_t col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
+    const uint32_t c = blockIdx.x * kCols + col;
+    const bool all = gridDim.y == 1, pf = p.param_f32, mine = lane == 0 && c < p.dim;
+    const size_t plane = static_cast<size_t>(p.batch) * parts * p.dim;
+    const float w = mine && !gate && p.weight ? load_param(p.weight, pf, c) : 1.f;
+    const float bias = mine && !gate && p.bias ? load_param(p.bias, pf, c) : 0.f;
+    float dw = 0.f, dbias = 0.f;
+    for (uint32_t b = blockIdx.y; b < (all ? p.batch : blockIdx.y + 1); ++b) {
+        float* part = p.partial + static_cast<size_t>(b) * parts * p.dim + c;
+        float s1 = 0.f, s2 = 0.f;
+        if (c < p.dim) {
+            if (gate) {
+#pragma unroll 4
+                for (uint32_t i = lane; i < parts; i += kLanes) s1 += part[2 * plane + static_cast<size_t>(i) * p.dim];
+            } else {
+#pragma unroll 4
+                for (uint32_t i = lane; i < parts; i += kLanes) {
+                    s1 += part[static_cast<size_t>(i) * p.dim];
+                    s2 += part[plane + static_cast<size_t>(i) * p.dim];
+                }
+            }
+        }
+        s1 = lane_sum(s1, lds, col, lane);
+        if (!gate) s2 = lane_sum(s2, lds, col, lane);
+        if (!mine) continue;
+        const size_t bc = static_cast<size_t>(b) * p.dim + c;
+        if (gate) {
+            store_param(p.dgate, pf, bc, s1);
+            continue;
+        }
+        const float f = 1.f + (p.scale ? load_param(p.scale, pf, bc) : 0.f);
+        if (p.dshift) store_param(p.dshift, pf, bc, s2);
+        if (p.dscale) store_param(p.dscale, pf, bc, fmaf(w, s1, bias * s2));
+        if (all) {
+            dw = fmaf(f, s1, dw);
+            dbias = fmaf(f, s2, dbias);
+        } else {
+            part[0] = f * s1;
+            part[plane] = f * s2;
+        }
+    }
+    if (!all || gate || !mine) return;
+    if (p.dweight) store_param(p.dweight, pf, c, dw);
+    if (p.dbias) store_param(p.dbias, pf, c, dbias);
+}
+
+// The weight's (blockIdx.z = 0) and the bias's (1) gradients: sums over the samples of what
+// layer_norm_backward_join left.
+__global__ __launch_bounds__(kCols* kLanes) void layer_norm_backward_weights(LayerNormBackward p, uint32_t parts) {
+    __shared__ float lds[kLanes][kCols + 1];
+    const uint32_t col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
+    const uint32_t c = blockIdx.x * kCols + col;
+    void* out = blockIdx.z == 0 ? p.dweight : p.dbias;
+    if (out == nullptr) return;
+    float s = 0.f;
+    if (c < p.dim)
+        for (uint32_t b = lane; b < p.batch; b += kLanes)
+            s += p.partial[(static_cast<size_t>(blockIdx.z) * p.batch + b) * parts * p.dim + c];
+    s = lane_sum(s, lds, col, lane);
+    if (lane == 0 && c < p.dim) store_param(out, p.param_f32, c, s);
+}
+
+template <bool F32, int E>
+hipError_t forward_of(const LayerNormForward& p, bool vec, dim3 grid, dim3 block, hipStream_t stream) {
+    if (vec) {
+        if (p.after) layer_norm_forward<F32, E, true, true><<<grid, block, 0, stream>>>(p);
+        else layer_norm_forward<F32, E, true, false><<<grid, block, 0, stream>>>(p);
+    } else {
+        if (p.after) layer_norm_forward<F32, E, false, true><<<grid, block, 0, stream>>>(p);
+        else layer_norm_forward<F32, E, false, false><<<grid, block, 0, stream>>>(p);
+    }
+    return hipGetLastError();
+}
+
+template <bool F32, int E>
+hipError_t backward_of(const LayerNormBackward& p, bool vec, dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
+    if (vec) {
+        if (p.after) layer_norm_backward<F32, E, true, true><<<grid, block, lds, stream>>>(p);
+        else layer_norm_backward<F32, E, true, false><<<grid, block, lds, stream>>>(p);
+    } else {
+        if (p.after) layer_norm_backward<F32, E, false, true><<<grid, block, lds, stream>>>(p);
+        else layer_norm_backward<F32, E, false, false><<<grid, block, lds, stream>>>(p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm_forward(const LayerNormForward& p, bool f32, bool vec, hipStream_t stream) {
+    const Shape s = row_shape(p.batch, p.rows, p.dim);
+    const dim3 block(s.T, s.G), grid(row_parts(p.batch, p.rows, s.G), p.batch);
+    if (f32)
+        return s.wide ? forward_of<true, 16>(p, vec, grid, block, stream) : forward_of<true, 8>(p, vec, grid, block, stream);
+    return s.wide ? forward_of<false, 16>(p, vec, grid, block, stream) : forward_of<false, 8>(p, vec, grid, block, stream);
+}
+
+hipError_t launch_layer_norm_backward(const LayerNormBackward& p, bool f32, bool vec, hipStream_t stream) {
+    if (p.batch == 0 || p.rows == 0) {  // no rows: every sum is zero
+        const size_t D = p.dim, BD = size_t(p.batch) * p.dim;
+        const std::pair<void*, size_t> sums[5] = {{p.dweight, D}, {p.dbias, D}, {p.dgate, BD}, {p.dscale, BD},
+                                                  {p.dshift, BD}};
+        for (const auto& v : sums)
+            if (v.first != nullptr && v.second != 0) norm_zero<<<64, 256, 0, stream>>>(v.first, v.second, p.param_f32);
+        return hipGetLastError();
+    }
+    const Shape s = row_shape(p.batch, p.rows, p.dim);
+    const uint32_t parts = row_parts(p.batch, p.rows, s.G);
+    const dim3 block(s.T, s.G), grid(parts, p.batch);
+    const size_t lds = size_t(s.G - 1) * p.dim * sizeof(float);
+    hipError_t e;
+    if (f32)
+        e = s.wide ? backward_of<true, 16>(p, vec, grid, block, lds, stream) : backward_of<true, 8>(p, vec, grid, block, lds, stream);
+    else
+        e = s.wide ? backward_of<false, 16>(p, vec, grid, block, lds, stream) : backward_of<false, 8>(p, vec, grid, block, lds, stream);
+    if (e != hipSuccess || p.partial == nullptr) return e;
+    const uint32_t cols = (p.dim + kCols - 1) / kCols;
+    const bool few = p.batch <= 4;
+    layer_norm_backward_join<<<dim3(cols, few ? 1 : p.batch, p.dgate ? 2 : 1), kCols * kLanes, 0, stream>>>(p, parts);
+    e = hipGetLastError();
+    if (e != hipSuccess || few || (!p.dweight && !p.dbias)) return e;
+    layer_norm_backward_weights<<<dim3(cols, 1, 2), kCols * kLanes, 0, stream>>>(p, parts);
+    return hipGetLastError();
+}
+
+}  // namespace ltx3drope
