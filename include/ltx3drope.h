@@ -41,7 +41,9 @@
  * the rotate-half form, patchify, the DiT frequency grid, and the rest of a
  * transformer block: norms before and after it with gate, scaled residual and
  * the next modulated norm, the gated feed-forward block, and the linear layer
- * in 8-bit integers.  Each is documented at its declaration.
+ * in 8-bit integers; and the way from the residual stream to rotated queries and
+ * keys: layer norms, the linear layer in 8-bit floating point, and rotary positions
+ * with several axes.  Each is documented at its declaration.
  */
 #ifndef LTX3DROPE_H
 #define LTX3DROPE_H
@@ -370,6 +372,66 @@ int ltx3drope_unpatchify(void* x, const void* y, int elem_bytes, int64_t B, int6
  */
 int ltx3drope_dit_freq_grid(double theta, int64_t dim, int64_t num_rope_elems, int double_precision, float* out,
                             void* stream, int64_t* count);
+
+/*
+ * Rotary positions with several axes: q and k turned by angles of any positions a
+ * token has on `axes` axes (time, height, width; images and videos of any sizes
+ * in one sequence; text, whose axes are all alike; fractional positions).  With
+ * pair i of a head (0 <= i < pairs) on axis axis[i]:
+ *     angle = positions[axis[i]][token] * frequencies[i]
+ *     e' = e cos(angle) - o sin(angle),  o' = e sin(angle) + o cos(angle)
+ * (e, o) being channels (2i, 2i+1) (pairing ADJACENT) or (i, i + pairs) (HALVES);
+ * channels from 2 * pairs on pass through, and so do the pairs of an axis[i] >=
+ * axes, bit for bit.  inverse = 1 turns by -angle: the gradients of q and k from
+ * those of q_out and k_out.
+ *
+ * q, q_out [batch, tokens, q_heads, head_dim], k, k_out [batch, tokens, k_heads,
+ * head_dim] of `dtype` (F32 or BF16), head_dim innermost and contiguous, the other
+ * strides (batch, token, head, in elements) any that are >= 0: views of one
+ * projection, heads before tokens.  k may be NULL with k_heads 0.  positions
+ * [axes, batch, tokens] of any strides >= 0 (a batch stride of 0: the same for all
+ * samples), int64, int32 or fp32; frequencies [pairs] (F64, or F32), radians a unit of
+ * position; axis [pairs] bytes; all device memory, the last two contiguous.
+ * Angles are formed in 64 bits; sine and cosine are within 2e-7, the rotation is
+ * fp32 and each output rounded once to `dtype`.
+ *
+ * An output may be exactly its own input (the same address and strides); outputs
+ * may interleave with other tensors of the call (heads of q and k in one row of a
+ * projection) as long as no element is shared.  batch, tokens or all heads of 0
+ * are an empty call.  E_INVALID: a NULL descriptor, an unknown pairing, position or
+ * frequency type, inverse other than 0 or 1, axes outside 1 to 255, a stride < 0, or
+ * k or k_out given without heads.  E_UNSUPPORTED, the first that fails of: DTYPE;
+ * NONPOSITIVE_DIM (head_dim or pairs <= 0, a size < 0); SPLIT_SUM (2 * pairs >
+ * head_dim); TOO_LARGE (batch > 65535, heads of q or k or head_dim > 65536, tokens of 2^31 or more,
+ * or a tensor that spans 2^60 bytes or more); NULLPTR; ALIGN (a pointer not aligned to
+ * its element); OVERLAP (an output whose own elements overlap, or that shares one
+ * with another tensor); then NOT_DEVICE_PTR, TABLE_DEVICE and EXTENT.  E_HIP.
+ * Asynchronous on `stream`; allocates nothing.
+ */
+enum { LTX3DROPE_PAIRING_ADJACENT = 0, LTX3DROPE_PAIRING_HALVES = 1 };
+enum { LTX3DROPE_POSITION_I64 = 0, LTX3DROPE_POSITION_I32 = 1, LTX3DROPE_POSITION_F32 = 2 };
+enum { LTX3DROPE_FREQUENCY_F64 = 0, LTX3DROPE_FREQUENCY_F32 = 1 };
+typedef struct {
+    int32_t dtype, pairing, inverse, position_type, frequency_type, axes;
+    int64_t batch, tokens, q_heads, k_heads, head_dim, pairs;
+    int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3]; /* batch, token, head */
+    int64_t position_strides[3];                                            /* axis, batch, token */
+    const void *q, *k;
+    void *q_out, *k_out;
+    const void *positions, *frequencies;
+    const uint8_t* axis;
+} ltx3drope_axes_t;
+int ltx3drope_axes_apply(const ltx3drope_axes_t* call, void* stream, int* reason);
+
+/*
+ * The frequencies and axes of a head cut into `axes` chunks of widths[a] channels, into host memory
+ * (sum(widths) / 2 numbers each): pair i of a chunk of width d has base^(-2i/d) (joint = 0, the
+ * frequencies of ltx3drope_tables_build), or pair j of all base^(-2j/sum(widths)) (joint = 1), in
+ * float64.  E_INVALID: axes outside 1 to 255, a width that is odd, <= 0 or > 65536, base not finite or
+ * <= 0, joint other than 0 or 1, a NULL pointer.
+ */
+int ltx3drope_axes_frequencies(int axes, const int64_t* widths, double base, int joint, double* frequencies,
+                               uint8_t* axis);
 
 /*
  * RMS norms before and after a transformer block, fused with the block's gate,

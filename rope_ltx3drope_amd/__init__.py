@@ -46,7 +46,7 @@ __all__ = [
     "cache_clear", "copy_bytes", "version", "neox_can_use", "neox_apply_qk", "neox_position_errors", "patchify",
     "unpatchify", "dit_freq_grid", "norm_before", "norm_after", "norm_before_backward", "norm_after_backward",
     "NormBeforeGrads", "NormAfterGrads", "layer_norm_before", "layer_norm_after", "layer_norm_before_backward",
-    "layer_norm_after_backward", "LayerNormBeforeGrads", "LayerNormAfterGrads", "gated_ffn", "gated_ffn_backward", "q8_quantize", "q8_matmul",
+    "layer_norm_after_backward", "axes_frequencies", "axes_apply_qk", "axes_apply_qk_backward", "LayerNormBeforeGrads", "LayerNormAfterGrads", "gated_ffn", "gated_ffn_backward", "q8_quantize", "q8_matmul",
 ]
 
 
@@ -82,6 +82,8 @@ def _refused(status: int, reason: ctypes.c_int, what: str):
 
 _torch_module = None
 _dtype_codes: dict = {}
+_position_types: dict = {}
+_frequency_types: dict = {}
 
 
 def _torch():
@@ -89,6 +91,9 @@ def _torch():
     if _torch_module is None:
         import torch
 
+        _position_types.update({torch.int64: _lib.POSITION_I64, torch.int32: _lib.POSITION_I32,
+                                torch.float32: _lib.POSITION_F32})
+        _frequency_types.update({torch.float64: _lib.FREQUENCY_F64, torch.float32: _lib.FREQUENCY_F32})
         _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
         _torch_module = torch
     return _torch_module
@@ -436,6 +441,118 @@ def dit_freq_grid(theta: float, dim: int, num_rope_elems: int, double_precision:
         raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR", st)
     _check(st, "dit_freq_grid")
     return out
+
+
+def axes_frequencies(widths: Sequence[int], base: float = 10000.0, *, joint: bool = False, device=None):
+    """(frequencies float64 [pairs], axis uint8 [pairs]) on `device` (default: the current one) for heads cut
+    into one chunk of channels an axis: base^(-2i/width) for pair i of a chunk, or with joint=True
+    base^(-2j/sum(widths)) for pair j of all chunks."""
+    import numpy as np
+
+    torch = _torch()
+    widths = [int(w) for w in widths]
+    n = sum(w for w in widths if w > 0) // 2
+    frequencies, axis = np.empty(n, np.float64), np.empty(n, np.uint8)
+    _check(_lib.lib().ltx3drope_axes_frequencies(
+        len(widths), (_lib.i64 * len(widths))(*widths), float(base), int(bool(joint)),
+        frequencies.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+        axis.ctypes.data_as(ctypes.POINTER(ctypes.c_uint8))), "axes_frequencies")
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return torch.from_numpy(frequencies).to(device), torch.from_numpy(axis).to(device)
+
+
+def _axes_marshal(t, like, device, out):
+    """Checks one of the call's tensors and gives its (batch, token, head) strides."""
+    if t.dim() != like.dim() or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]:
+        raise Ltx3dRopeUnsupported("OUTPUT_MISMATCH" if out else "SHAPE_MISMATCH")
+    if t.dtype is not like.dtype:
+        raise Ltx3dRopeUnsupported("OUTPUT_MISMATCH" if out else "DTYPE")
+    if t.get_device() != device or device < 0:
+        raise Ltx3dRopeUnsupported("OUTPUT_MISMATCH" if out else "NOT_DEVICE_PTR")
+    s = t.stride()
+    if s[-1] != 1 and t.shape[-1] != 1:
+        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    return s[:3] if len(s) == 4 else (0, *s[:2])
+
+
+def _axes_apply(q, k, positions, frequencies, axis, pairing, inverse, q_out, k_out, inplace, stream, what):
+    torch = _torch()
+    try:
+        pairing = _lib.PAIRINGS[pairing]
+    except KeyError:
+        raise ValueError(f"pairing must be one of {sorted(_lib.PAIRINGS)}") from None
+    shape, dims, index = q.shape, q.dim(), q.get_device()
+    if dims != 3 and dims != 4:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    if k is None and k_out is not None:
+        raise ValueError("k_out belongs to k")
+    q_strides = _axes_marshal(q, q, index, False)
+    k_strides, k_heads = ((0, 0, 0), 0) if k is None else (_axes_marshal(k, q, index, False), k.shape[-2])
+    batch = shape[0] if dims == 4 else 1
+    # positions: [axes, tokens] (for every sample), or [axes, batch, tokens]
+    if positions.shape[1:] == shape[:-2]:
+        p = positions.stride()
+        position_strides = p if dims == 4 else (p[0], 0, p[1])
+    elif dims == 4 and positions.dim() == 2 and positions.shape[1] == shape[1]:
+        position_strides = (positions.stride(0), 0, positions.stride(1))
+    else:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    if frequencies.dim() != 1 or axis.shape != frequencies.shape:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    position_type = _position_types.get(positions.dtype, -1)
+    frequency_type = _frequency_types.get(frequencies.dtype, -1)
+    if position_type < 0 or frequency_type < 0 or axis.dtype is not torch.uint8:
+        raise Ltx3dRopeUnsupported("DTYPE")
+    if not (positions.get_device() == frequencies.get_device() == axis.get_device() == index):
+        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+    if not (frequencies.is_contiguous() and axis.is_contiguous()):
+        raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    if inplace:
+        if (q_out is not None and q_out is not q) or (k_out is not None and k_out is not k):
+            raise ValueError("inplace=True writes into q and k")
+        q_out, k_out = q, k
+    contiguous = torch.contiguous_format
+    if q_out is None:
+        q_out = _empty(stream, lambda: torch.empty_like(q, memory_format=contiguous))
+    if k_out is None and k is not None:
+        k_out = _empty(stream, lambda: torch.empty_like(k, memory_format=contiguous))
+    if q_out.shape != shape or (k is not None and k_out.shape != k.shape):
+        raise Ltx3dRopeUnsupported("OUTPUT_MISMATCH")
+    out_strides = (*_axes_marshal(q_out, q, index, True),
+                   *((0, 0, 0) if k is None else _axes_marshal(k_out, q, index, True)))
+    reason = ctypes.c_int(0)
+    _lib.lib()
+    st = _lib.axes_apply(
+        _lib.AXES_BYTES.pack(_dtype_code(q), pairing, inverse, position_type, frequency_type, positions.shape[0], batch,
+                             shape[-3], shape[-2], k_heads, shape[-1], frequencies.shape[0], *q_strides, *k_strides,
+                             *out_strides, *position_strides, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out),
+                             positions.data_ptr(), frequencies.data_ptr(), axis.data_ptr()),
+        _raw_stream(index, stream), ctypes.byref(reason))
+    _finish(st, reason, what)
+    return q_out, k_out
+
+
+def axes_apply_qk(q, k, positions, frequencies, axis, *, pairing: str = "adjacent", q_out=None, k_out=None,
+                  inplace: bool = False, stream=None):
+    """Rotary positions with several axes: pair i of every head of q and k turned by
+    positions[axis[i]] * frequencies[i], one launch; (q_out, k_out).
+
+    q [tokens, heads, head_dim] or [batch, tokens, heads, head_dim], k alike with its own heads (or None),
+    float32 or bfloat16, any strides with head_dim innermost (views of one projection).  positions
+    [axes, tokens] or [axes, batch, tokens], int64, int32 or float32, any strides.  frequencies [pairs]
+    float64 or float32 and axis [pairs] uint8, as axes_frequencies() gives them; a pair whose axis is not
+    below `axes` stays as it is, and so do channels from 2 * pairs on.  pairing: "adjacent" (channels 2i,
+    2i + 1) or "halves" (i, i + pairs)."""
+    return _axes_apply(q, k, positions, frequencies, axis, pairing, 0, q_out, k_out, inplace, stream, "axes_apply_qk")
+
+
+def axes_apply_qk_backward(dq_out, dk_out, positions, frequencies, axis, *, pairing: str = "adjacent", dq=None, dk=None,
+                           inplace: bool = False, stream=None):
+    """(dq, dk), the gradients of axes_apply_qk's q and k from those of its outputs: the inverse rotation.
+    Arguments as there."""
+    return _axes_apply(dq_out, dk_out, positions, frequencies, axis, pairing, 1, dq, dk, inplace, stream,
+                       "axes_apply_qk_backward")
 
 
 def _finish(status: int, reason: ctypes.c_int, what: str) -> None:

@@ -53,8 +53,12 @@ EXPORTS = (
     "ltx3drope_gated_ffn_backward_workspace", "ltx3drope_q8_quantize", "ltx3drope_q8_matmul",
     "ltx3drope_q8_matmul_workspace",
     "ltx3drope_layer_norm", "ltx3drope_layer_norm_backward", "ltx3drope_layer_norm_backward_workspace",
+    "ltx3drope_axes_apply", "ltx3drope_axes_frequencies",
 )
 
+POSITION_I64, POSITION_I32, POSITION_F32 = 0, 1, 2
+FREQUENCY_F64, FREQUENCY_F32 = 0, 1
+PAIRINGS = {"adjacent": 0, "halves": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 i64 = ctypes.c_int64
@@ -133,6 +137,13 @@ class Q8Matmul(ctypes.Structure):
         ("workspace_bytes", i64)]
 
 
+class Axes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "pairing", "inverse", "position_type", "frequency_type", "axes")] + [
+        (n, i64) for n in ("batch", "tokens", "q_heads", "k_heads", "head_dim", "pairs")] + [
+        (n, i64 * 3) for n in ("q_strides", "k_strides", "q_out_strides", "k_out_strides", "position_strides")] + [
+        (n, vp) for n in ("q", "k", "q_out", "k_out", "positions", "frequencies", "axis")]
+
+
 # The same descriptors as bytes, for the calls that single tokens wait for: a struct.pack takes a
 # tenth of the time of filling a ctypes.Structure by name.
 NORM_BYTES = struct.Struct("@6i3q3f9P")
@@ -142,9 +153,11 @@ LAYER_NORM_BACKWARD_BYTES = struct.Struct("@4i3qf16Pq")
 FFN_BYTES = struct.Struct("@2i3q7Pq")
 FFN_BACKWARD_BYTES = struct.Struct("@2i3q10Pq")
 Q8_BYTES = struct.Struct("@2i3q7Pq")
+AXES_BYTES = struct.Struct("@6i21q7P")
 
 # entry points that take a descriptor as bytes (bound in lib())
 norm = norm_backward = layer_norm = layer_norm_backward = gated_ffn = gated_ffn_backward = q8_matmul = None
+axes_apply = None
 norm_backward_workspace = layer_norm_backward_workspace = gated_ffn_workspace = gated_ffn_backward_workspace = None
 q8_matmul_workspace = None
 
@@ -153,9 +166,9 @@ def _bind_bytes(L) -> None:
     call = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, vp, vp)
     size = ctypes.CFUNCTYPE(i64, ctypes.c_char_p)
     for name in ("norm", "norm_backward", "layer_norm", "layer_norm_backward", "gated_ffn", "gated_ffn_backward",
-                 "q8_matmul"):
+                 "q8_matmul", "axes_apply"):
         globals()[name] = call(("ltx3drope_" + name, L))
-        if name not in ("norm", "layer_norm"):
+        if name not in ("norm", "layer_norm", "axes_apply"):
             globals()[name + "_workspace"] = size((f"ltx3drope_{name}_workspace", L))
 
 
@@ -227,6 +240,10 @@ def lib() -> ctypes.CDLL:
             "ltx3drope_layer_norm_backward": (ctypes.c_int, [ctypes.POINTER(LayerNormBackward), vp,
                                                              ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_layer_norm_backward_workspace": (i64, [ctypes.POINTER(LayerNormBackward)]),
+            "ltx3drope_axes_apply": (ctypes.c_int, [ctypes.POINTER(Axes), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_axes_frequencies": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(i64), ctypes.c_double,
+                                                          ctypes.c_int, ctypes.POINTER(ctypes.c_double),
+                                                          ctypes.POINTER(ctypes.c_uint8)]),
             "ltx3drope_gated_ffn": (ctypes.c_int, [ctypes.POINTER(GatedFfn), vp, ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_gated_ffn_workspace": (i64, [ctypes.POINTER(GatedFfn)]),
             "ltx3drope_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(GatedFfnBackward), vp,
