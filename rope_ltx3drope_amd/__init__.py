@@ -14,7 +14,8 @@ forward_pair() the decoder-side entry that ties them together.
 
 Of the transformer block around it: norm_before(), norm_after(),
 layer_norm_before(), layer_norm_after() and their backward passes, gated_ffn() and its backward pass, q8_quantize() and
-q8_matmul().
+q8_matmul(), f8_quantize(), f8_quantize_weight() and f8_matmul(), and
+axes_apply_qk(), the rotation at any positions, with its backward pass.
 
 No call here is recorded by autograd: results never require gradients, whatever
 the arguments do.  To train through an operator, call it and its *_backward in
@@ -47,6 +48,7 @@ __all__ = [
     "unpatchify", "dit_freq_grid", "norm_before", "norm_after", "norm_before_backward", "norm_after_backward",
     "NormBeforeGrads", "NormAfterGrads", "layer_norm_before", "layer_norm_after", "layer_norm_before_backward",
     "layer_norm_after_backward", "axes_frequencies", "axes_apply_qk", "axes_apply_qk_backward", "LayerNormBeforeGrads", "LayerNormAfterGrads", "gated_ffn", "gated_ffn_backward", "q8_quantize", "q8_matmul",
+    "f8_quantize", "f8_quantize_weight", "f8_matmul",
 ]
 
 
@@ -982,6 +984,110 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
     st = _lib.q8_matmul(descriptor if ws is None else pack(*head, ws.data_ptr(), size), _raw_stream(index, stream),
                         ctypes.byref(reason))
     _finish(st, reason, "q8_matmul")
+    return out
+
+
+def _f8_quantize(x, blocks, turned, q_out, scale_out, stream, what):
+    torch = _torch()
+    xs, index, device = x.shape, x.get_device(), x.device
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if len(xs) < 1 or ((blocks or turned) and len(xs) != 2):
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    dim = xs[-1]
+    rows = x.numel() // dim if dim else 0
+    across = -(-dim // 128)
+    scales = (-(-rows // 128), across) if blocks else xs[:-1] + (across,)
+    _operands(index, (x, xs, x.dtype), (q_out, xs, f8), (scale_out, scales, f32))
+
+    def outputs():
+        q = torch.empty_like(x, dtype=f8) if q_out is None else q_out
+        scale = x.new_empty(scales, dtype=f32) if scale_out is None else scale_out
+        if not turned:
+            return q, scale
+        # rows that start on 128 bytes: a product then copies them straight to LDS
+        pitch = -(-rows // 128) * 128
+        t = torch.empty(dim, pitch, dtype=f8, device=device)
+        down = torch.empty((across, scales[0]) if blocks else (dim, -(-rows // 128)), dtype=f32, device=device)
+        return q, scale, t[:, :rows], down
+
+    outs = outputs() if stream is None else _empty(stream, outputs)
+    reason = ctypes.c_int(0)
+    _lib.lib()
+    more = (outs[2].data_ptr(), outs[3].data_ptr()) if turned else (0, 0)
+    st = _lib.f8_quantize(
+        _lib.F8_QUANTIZE_BYTES.pack(_dtype_code(x), blocks, rows, dim, -(-rows // 128) * 128 if turned else 0,
+                                    x.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), *more),
+        _raw_stream(index, stream), ctypes.byref(reason))
+    _finish(st, reason, what)
+    return outs
+
+
+def f8_quantize(x, *, turned: bool = False, q_out=None, scale_out=None, stream=None):
+    """Rows to 8-bit floating point: (q float8_e4m3fn like x, scale float32 [..., ceil(dim / 128)]) with scale =
+    max |block| / 448 for each 128 numbers of a row and q = x / scale rounded.  x [..., dim], float32 or
+    bfloat16.
+
+    turned=True (x [rows, dim]) gives (q, scale, q_turned, scale_turned) in one pass: the same of x's transpose
+    [dim, rows], blocks of 128 rows of each column, for the products of a backward pass."""
+    return _f8_quantize(x, 0, turned, q_out, scale_out, stream, "f8_quantize")
+
+
+def f8_quantize_weight(w, *, turned: bool = False, q_out=None, scale_out=None, stream=None):
+    """Weights [out, dim] to 8-bit floating point: (q, scale float32 [ceil(out / 128), ceil(dim / 128)]), one
+    scale for each 128 x 128 block.  turned=True adds (q_turned [dim, out], scale_turned), the same blocks
+    of the transpose, for the input's gradient."""
+    return _f8_quantize(w, 1, turned, q_out, scale_out, stream, "f8_quantize_weight")
+
+
+def f8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream=None):
+    """The linear layer in 8-bit floating point: a b^T, each 128 of k with its scales, + bias.
+
+    a float8_e4m3fn [..., dim] with a_scale float32 [..., ceil(dim / 128)] and b [out, dim] with b_scale
+    [ceil(out / 128), ceil(dim / 128)] (as f8_quantize_weight gives it) or [out, ceil(dim / 128)]
+    (f8_quantize); two-dimensional operands may have rows further apart than dim.  bias float32 [out] or
+    None; dtype of the result: bfloat16 (default) or float32.
+
+    Of y = x w^T the gradients are f8_matmul(dy, ., w_turned, .) and f8_matmul(dy_turned, ., x_turned, .)."""
+    torch = _torch()
+    shape, device, index = a.shape, a.device, a.get_device()
+    if len(shape) < 1 or b.dim() != 2:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    dim, n = shape[-1], b.shape[0]
+    rows, channels = shape[:-1], (n,)
+    across, f8, f32 = -(-dim // 128), torch.float8_e4m3fn, torch.float32
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    b_rows = int(n > 1 and b_scale.shape == (n, across))
+    if b.shape[1] != dim:
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    pitches = []
+    for t in (a, b):
+        if t.dtype is not f8:
+            raise Ltx3dRopeUnsupported("DTYPE")
+        if t.get_device() != index or index < 0:
+            raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+        if t.is_contiguous():
+            pitches.append(dim)
+        elif t.dim() == 2 and (t.stride(1) == 1 or dim == 1) and (t.stride(0) >= dim or t.shape[0] == 1):
+            pitches.append(max(t.stride(0), dim))
+        else:
+            raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    _operands(index, (a_scale, rows + (across,), f32), (b_scale, (n if b_rows else -(-n // 128), across), f32),
+              (bias, channels, f32), (out, rows + channels, dtype))
+    if out is None:
+        shape = rows + channels
+        out = (a_scale.new_empty(shape, dtype=dtype) if stream is None
+               else _empty(stream, lambda: a_scale.new_empty(shape, dtype=dtype)))
+    _lib.lib()
+    pack = _lib.F8_BYTES.pack
+    head = (_dtype_code(out), b_rows, a.numel() // dim if dim else 0, dim, n, *pitches, a.data_ptr(), b.data_ptr(),
+            a_scale.data_ptr(), b_scale.data_ptr(), _ptr(bias), out.data_ptr())
+    descriptor = pack(*head, 0, 0)
+    ws, size = _workspace(stream, _lib.f8_matmul_workspace, descriptor, device)
+    reason = ctypes.c_int(0)
+    st = _lib.f8_matmul(descriptor if ws is None else pack(*head, ws.data_ptr(), size), _raw_stream(index, stream),
+                        ctypes.byref(reason))
+    _finish(st, reason, "f8_matmul")
     return out
 
 

@@ -54,6 +54,7 @@ EXPORTS = (
     "ltx3drope_q8_matmul_workspace",
     "ltx3drope_layer_norm", "ltx3drope_layer_norm_backward", "ltx3drope_layer_norm_backward_workspace",
     "ltx3drope_axes_apply", "ltx3drope_axes_frequencies",
+    "ltx3drope_f8_quantize", "ltx3drope_f8_matmul", "ltx3drope_f8_matmul_workspace",
 )
 
 POSITION_I64, POSITION_I32, POSITION_F32 = 0, 1, 2
@@ -137,6 +138,17 @@ class Q8Matmul(ctypes.Structure):
         ("workspace_bytes", i64)]
 
 
+class F8Quantize(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("blocks", ctypes.c_int32)] + [(n, i64) for n in (
+        "rows", "dim", "turned_pitch")] + [(n, vp) for n in ("x", "q", "scale", "q_turned", "scale_turned")]
+
+
+class F8Matmul(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("b_rows", ctypes.c_int32)] + [(n, i64) for n in (
+        "tokens", "dim", "out", "a_pitch", "b_pitch")] + [(n, vp) for n in (
+            "a", "b", "a_scale", "b_scale", "bias", "y", "workspace")] + [("workspace_bytes", i64)]
+
+
 class Axes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "pairing", "inverse", "position_type", "frequency_type", "axes")] + [
         (n, i64) for n in ("batch", "tokens", "q_heads", "k_heads", "head_dim", "pairs")] + [
@@ -153,11 +165,13 @@ LAYER_NORM_BACKWARD_BYTES = struct.Struct("@4i3qf16Pq")
 FFN_BYTES = struct.Struct("@2i3q7Pq")
 FFN_BACKWARD_BYTES = struct.Struct("@2i3q10Pq")
 Q8_BYTES = struct.Struct("@2i3q7Pq")
+F8_QUANTIZE_BYTES = struct.Struct("@2i3q5P")
+F8_BYTES = struct.Struct("@2i5q7Pq")
 AXES_BYTES = struct.Struct("@6i21q7P")
 
 # entry points that take a descriptor as bytes (bound in lib())
 norm = norm_backward = layer_norm = layer_norm_backward = gated_ffn = gated_ffn_backward = q8_matmul = None
-axes_apply = None
+axes_apply = f8_quantize = f8_matmul = f8_matmul_workspace = None
 norm_backward_workspace = layer_norm_backward_workspace = gated_ffn_workspace = gated_ffn_backward_workspace = None
 q8_matmul_workspace = None
 
@@ -166,9 +180,9 @@ def _bind_bytes(L) -> None:
     call = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, vp, vp)
     size = ctypes.CFUNCTYPE(i64, ctypes.c_char_p)
     for name in ("norm", "norm_backward", "layer_norm", "layer_norm_backward", "gated_ffn", "gated_ffn_backward",
-                 "q8_matmul", "axes_apply"):
+                 "q8_matmul", "axes_apply", "f8_quantize", "f8_matmul"):
         globals()[name] = call(("ltx3drope_" + name, L))
-        if name not in ("norm", "layer_norm", "axes_apply"):
+        if name not in ("norm", "layer_norm", "axes_apply", "f8_quantize"):
             globals()[name + "_workspace"] = size((f"ltx3drope_{name}_workspace", L))
 
 
@@ -240,6 +254,9 @@ def lib() -> ctypes.CDLL:
             "ltx3drope_layer_norm_backward": (ctypes.c_int, [ctypes.POINTER(LayerNormBackward), vp,
                                                              ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_layer_norm_backward_workspace": (i64, [ctypes.POINTER(LayerNormBackward)]),
+            "ltx3drope_f8_quantize": (ctypes.c_int, [ctypes.POINTER(F8Quantize), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_f8_matmul": (ctypes.c_int, [ctypes.POINTER(F8Matmul), vp, ctypes.POINTER(ctypes.c_int)]),
+            "ltx3drope_f8_matmul_workspace": (i64, [ctypes.POINTER(F8Matmul)]),
             "ltx3drope_axes_apply": (ctypes.c_int, [ctypes.POINTER(Axes), vp, ctypes.POINTER(ctypes.c_int)]),
             "ltx3drope_axes_frequencies": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(i64), ctypes.c_double,
                                                           ctypes.c_int, ctypes.POINTER(ctypes.c_double),

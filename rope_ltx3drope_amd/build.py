@@ -42,6 +42,7 @@ SOURCES = [  # (file, language, extra flags)
     ("layer_norm.hip", "hip", DEVICE),
     ("ffn.hip", "hip", DEVICE),
     ("q8.hip", "hip", DEVICE),
+    ("f8.hip", "hip", DEVICE),
     ("axes.hip", "hip", DEVICE),
     ("api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),
     ("block_api.cpp", "c++", ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROCM, "include")]),

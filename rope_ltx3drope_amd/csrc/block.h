@@ -1,5 +1,5 @@
 // The transformer-block operators: what the host side (block_api.cpp) hands to the kernel launchers
-// (norm.hip, layer_norm.hip, ffn.hip, q8.hip).  Sizes fit in 32 bits unless they are size_t; offsets into tensors are formed in 64.
+// (norm.hip, layer_norm.hip, ffn.hip, q8.hip, f8.hip).  Sizes fit in 32 bits unless they are size_t; offsets into tensors are formed in 64.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -108,5 +108,35 @@ size_t q8_workspace(const Q8Problem& p);
 hipError_t launch_q8(const Q8Problem& p, bool f32, hipStream_t stream);
 hipError_t launch_q8_quantize(const void* x, void* q, float* scale, uint32_t rows, uint32_t dim, bool f32,
                               hipStream_t stream);
+
+// The linear layer in 8-bit floating point (f8.hip): a [tokens, dim] and b [out, dim] e4m3, their rows a_pitch and
+// b_pitch bytes apart, y [tokens, out]; a scale for 128 of k: a_scale [tokens, blocks], b_scale [out, blocks]
+// (b_rows) or [out / 128, blocks].
+struct F8Problem {
+    const void *a, *b;
+    const float *a_scale, *b_scale, *bias;
+    void* y;
+    void* workspace;
+    uint64_t a_pitch, b_pitch;
+    uint32_t tokens, dim, out;
+    bool b_rows;
+};
+constexpr int64_t kF8MaxDim = int64_t(1) << 21;    // 256 rows of 2^21 scales / 128 and ...
+constexpr int64_t kF8MaxPitch = int64_t(1) << 22;  // ... 256 rows of this many bytes stay within 2^31
+size_t f8_workspace(const F8Problem& p);
+hipError_t launch_f8(const F8Problem& p, bool f32, hipStream_t stream);
+
+// x [rows, dim] to e4m3 with scales for 128 of a row or (blocks) 128 x 128; q_turned [dim, rows], its rows
+// turned_pitch bytes apart, may be NULL.
+struct F8Quantize {
+    const void* x;
+    void *q, *q_turned;
+    float *scale, *scale_turned;
+    uint64_t turned_pitch;
+    uint32_t rows, dim;
+    bool blocks;
+    bool turned_chunks;  // q_turned starts on 16 bytes and so does each of its rows, with room for whole pieces
+};
+hipError_t launch_f8_quantize(const F8Quantize& p, bool f32, hipStream_t stream);
 
 }  // namespace ltx3drope

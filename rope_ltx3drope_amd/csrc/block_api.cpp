@@ -166,6 +166,44 @@ Q8Problem q8_problem(const ltx3drope_q8_matmul_t& c) {
     return p;
 }
 
+int check_f8(const ltx3drope_f8_matmul_t& c, int* why) {
+    if (!flag(c.b_rows)) return LTX3DROPE_E_INVALID;
+    if (c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) {
+        *why = LTX3DROPE_REASON_DTYPE;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    if (c.dim <= 0 || c.tokens < 0 || c.out < 0) {
+        *why = LTX3DROPE_REASON_NONPOSITIVE_DIM;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    if (c.a_pitch < c.dim || c.b_pitch < c.dim) return LTX3DROPE_E_INVALID;
+    const int64_t lim = int64_t(1) << 26;
+    if (c.dim >= kF8MaxDim || c.a_pitch >= kF8MaxPitch || c.b_pitch >= kF8MaxPitch || c.tokens >= lim || c.out >= lim ||
+        too_many_tiles(c.tokens, c.out)) {
+        *why = LTX3DROPE_REASON_TOO_LARGE;
+        return LTX3DROPE_E_UNSUPPORTED;
+    }
+    return LTX3DROPE_OK;
+}
+
+F8Problem f8_problem(const ltx3drope_f8_matmul_t& c) {
+    F8Problem p;
+    p.a = c.a;
+    p.b = c.b;
+    p.a_scale = c.a_scale;
+    p.b_scale = c.b_scale;
+    p.bias = c.bias;
+    p.y = c.y;
+    p.workspace = c.workspace;
+    p.a_pitch = static_cast<uint64_t>(c.a_pitch);
+    p.b_pitch = static_cast<uint64_t>(c.b_pitch);
+    p.tokens = static_cast<uint32_t>(c.tokens);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.out = static_cast<uint32_t>(c.out);
+    p.b_rows = c.b_rows != 0;
+    return p;
+}
+
 }  // namespace
 }  // namespace ltx3drope
 
@@ -614,6 +652,92 @@ int ltx3drope_q8_matmul(const ltx3drope_q8_matmul_t* call, void* stream, int* re
     if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
     DeviceGuard guard(device);
     if (launch_q8(p, c.dtype == LTX3DROPE_DTYPE_F32, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int ltx3drope_f8_quantize(const ltx3drope_f8_quantize_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_f8_quantize_t& c = *call;
+    if (!flag(c.blocks) || (c.q_turned == nullptr) != (c.scale_turned == nullptr) ||
+        (c.q_turned && c.turned_pitch < c.rows))
+        return LTX3DROPE_E_INVALID;
+    if (c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) return refuse(LTX3DROPE_REASON_DTYPE, reason);
+    if (c.dim <= 0 || c.rows < 0) return refuse(LTX3DROPE_REASON_NONPOSITIVE_DIM, reason);
+    const int64_t lim = int64_t(1) << 31;
+    if (c.dim >= lim || c.rows >= lim || (c.q_turned && c.turned_pitch >= 2 * lim))
+        return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
+    const int64_t tiles_r = (c.rows + 127) / 128, tiles_c = (c.dim + 127) / 128;
+    if (tiles_r * tiles_c >= int64_t(1) << 24) return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
+    if (c.rows == 0) return LTX3DROPE_OK;
+    if (!c.x || !c.q || !c.scale) return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t n = static_cast<size_t>(c.rows) * static_cast<size_t>(c.dim), es = elem(c.dtype);
+    Spans t;
+    t.add(c.x, n * es, es, Role::Param);
+    t.add(c.q, n, 1, Role::ParamOut);
+    t.add(c.scale, static_cast<size_t>((c.blocks ? tiles_r : c.rows) * tiles_c) * 4, 4, Role::ParamOut);
+    t.add(c.q_turned, static_cast<size_t>(c.dim) * static_cast<size_t>(c.turned_pitch), 1, Role::ParamOut);
+    t.add(c.scale_turned, static_cast<size_t>((c.blocks ? tiles_c : c.dim) * tiles_r) * 4, 4, Role::ParamOut);
+    int device = -1;
+    const int why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    F8Quantize p;
+    p.x = c.x;
+    p.q = c.q;
+    p.q_turned = c.q_turned;
+    p.scale = c.scale;
+    p.scale_turned = c.scale_turned;
+    p.turned_pitch = static_cast<uint64_t>(c.turned_pitch);
+    p.rows = static_cast<uint32_t>(c.rows);
+    p.dim = static_cast<uint32_t>(c.dim);
+    p.blocks = c.blocks != 0;
+    p.turned_chunks = ((reinterpret_cast<uintptr_t>(c.q_turned) | p.turned_pitch) & 15) == 0;
+    DeviceGuard guard(device);
+    if (launch_f8_quantize(p, c.dtype == LTX3DROPE_DTYPE_F32, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return LTX3DROPE_E_HIP;
+    count_launch();
+    return LTX3DROPE_OK;
+}
+
+int64_t ltx3drope_f8_matmul_workspace(const ltx3drope_f8_matmul_t* call) {
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_f8(*call, &why);
+    if (st != LTX3DROPE_OK) return st;
+    if (call->tokens == 0 || call->out == 0) return 0;
+    return static_cast<int64_t>(f8_workspace(f8_problem(*call)));
+}
+
+int ltx3drope_f8_matmul(const ltx3drope_f8_matmul_t* call, void* stream, int* reason) {
+    if (reason) *reason = LTX3DROPE_REASON_OK;
+    if (call == nullptr) return LTX3DROPE_E_INVALID;
+    const ltx3drope_f8_matmul_t& c = *call;
+    int why = LTX3DROPE_REASON_OK;
+    const int st = check_f8(c, &why);
+    if (st == LTX3DROPE_E_UNSUPPORTED) return refuse(why, reason);
+    if (st != LTX3DROPE_OK) return st;
+    if (c.tokens == 0 || c.out == 0) return LTX3DROPE_OK;
+    const F8Problem p = f8_problem(c);
+    const size_t ws = f8_workspace(p);
+    if (c.workspace_bytes < 0 || static_cast<size_t>(c.workspace_bytes) < ws) return LTX3DROPE_E_INVALID;
+    if (!c.a || !c.b || !c.a_scale || !c.b_scale || !c.y || (ws != 0 && !c.workspace))
+        return refuse(LTX3DROPE_REASON_NULLPTR, reason);
+    const size_t M = p.tokens, K = p.dim, N = p.out, es = elem(c.dtype), blocks = (K + 127) / 128;
+    Spans t;
+    t.add(c.a, (M - 1) * p.a_pitch + K, 1, Role::Param);
+    t.add(c.b, (N - 1) * p.b_pitch + K, 1, Role::Param);
+    t.add(c.a_scale, M * blocks * 4, 4, Role::Param);
+    t.add(c.b_scale, (p.b_rows ? N : (N + 127) / 128) * blocks * 4, 4, Role::Param);
+    t.add(c.bias, N * 4, 4, Role::Param);
+    t.add(c.y, M * N * es, es, Role::ParamOut);
+    if (ws != 0) t.add(c.workspace, ws, 16, Role::Scratch);
+    int device = -1;
+    why = check_spans(t, &device);
+    if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
+    DeviceGuard guard(device);
+    if (launch_f8(p, c.dtype == LTX3DROPE_DTYPE_F32, static_cast<hipStream_t>(stream)) != hipSuccess)
         return LTX3DROPE_E_HIP;
     count_launch();
     return LTX3DROPE_OK;
