@@ -21,7 +21,9 @@ struct AxesProblem {
     const void* frequencies;  // [pairs], radians a unit of position
     const uint8_t* axis;      // [pairs]
     uint32_t batch, tokens, head_dim, pairs, axes;
-    bool f32, halves, inverse, frequency_f32, vectors;
+    uint32_t first_token;  // of a launch's tokens
+    bool f32, halves, inverse, frequency_f32;
+    uint32_t vector;    // elements of an access: 16 bytes, 2 elements or 1
     int position_type;  // LTX3DROPE_POSITION_*
 };
 
@@ -29,11 +31,10 @@ constexpr int64_t kAxesMaxWidth = 65536;  // head_dim
 constexpr int64_t kAxesMaxHeads = 65536;  // of q and of k
 constexpr int64_t kAxesMaxBatch = 65535;  // one grid plane a sample
 
-// Whether 16-byte accesses cover the channels: whole vectors of rotated and of passed-through channels.  The
+// Whether accesses of v elements cover the channels: whole accesses of rotated and of passed-through channels.  The
 // pointers' and strides' alignment is checked by the host.
-inline bool axes_vector_widths(bool f32, bool halves, uint32_t head_dim, uint32_t pairs) {
-    const uint32_t vec = f32 ? 4 : 8, unit = halves ? vec : 4;
-    return pairs % unit == 0 && (head_dim - 2 * pairs) % vec == 0;
+inline bool axes_vector_widths(uint32_t v, bool halves, uint32_t head_dim, uint32_t pairs) {
+    return (halves ? pairs : 2 * pairs) % v == 0 && (head_dim - 2 * pairs) % v == 0;
 }
 
 hipError_t launch_axes(const AxesProblem& p, hipStream_t stream);

@@ -6,41 +6,42 @@
 //
 // Angles are formed in 64 bits: a position of 100000 times a frequency near 1 leaves fp32 0.004 of a radian.
 // The angle is taken in turns, a whole number of quarters is split off (exactly), and sine and cosine of the
-// rest, |x| <= pi/4, are their Taylor sums in fp32 up to x^9 and x^10 (the next terms are below 2e-9).
+// rest, up to half a quarter, are polynomials of degree 7 and 8 in fp32 (fitted to the least largest error,
+// 1.2e-9 and 6e-11).
 //
-// Bound: HBM.  Each channel is read and written once; an angle costs about 35 operations and is used by all heads, so
-// a workgroup forms the (cos, sin) of its tokens once, one or a few a thread, into LDS, and then streams
-// the heads past them, 16 bytes a thread.  A thread keeps its place in the head, and a token's cosines in
-// registers for all its heads.  The tokens' cosines lie in two LDS buffers in turn, so one barrier a step is
-// enough, and the next step's positions travel while this one streams.
+// Bound: HBM.  Each channel is read and written once, 16 bytes a lane, and an angle costs about 30 operations and is
+// used by all heads that a lane sees.
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "axes.h"
+#include "fastdiv.h"
 #include "ltx3drope.h"
+#include "stream_store.h"
 
 namespace ltx3drope {
 namespace {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr uint32_t kThreads = 256;
-constexpr uint32_t kMaxSteps = 4;  // angles a thread forms a step
-
-__device__ __forceinline__ f32x2 cos_sin(double position, double frequency) {
-    const double turns = position * frequency * 0.15915494309189533577;  // 1 / (2 pi)
-    const double part = turns - floor(turns);
-    const double quarters = rint(part * 4.0);
-    const float x = static_cast<float>(fma(quarters, -0.25, part) * 6.283185307179586477);
-    const float z = x * x;
-    const float s = fmaf(fmaf(fmaf(fmaf(2.7557319e-6f, z, -1.9841270e-4f), z, 8.3333333e-3f), z, -1.6666667e-1f) * z, x, x);
-    const float c = fmaf(fmaf(fmaf(fmaf(fmaf(-2.7557319e-7f, z, 2.4801587e-5f), z, -1.3888889e-3f), z, 4.1666667e-2f), z,
-                              -0.5f), z, 1.f);
-    const int k = static_cast<int>(quarters);  // 0 to 4
-    const float a = k & 1 ? s : c, b = k & 1 ? c : s;
+// (cos, sin) of position * turns whole turns.  Adding 1.5 * 2^52 leaves the quarters in the sum's low bits.
+__device__ __forceinline__ f32x2 cos_sin(double position, double turns) {
+    const double part = __builtin_amdgcn_fract(position * turns);
+    const double shifted = fma(part, 4.0, 0x1.8p52);
+    const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, shifted));  // 0 to 4
+    const float r = static_cast<float>(fma(part, 4.0, 0x1.8p52 - shifted));  // quarters, |r| <= 1/2
+    const float z = r * r;
+    const float p = fmaf(z, fmaf(z, fmaf(z, -4.5922891e-3f, 7.9675903e-2f), -6.4596294e-1f), -6.5420830e-8f);
+    const float s = fmaf(r, 1.57079637f, r * p);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 9.0402167e-4f, -2.0860289e-2f), 2.5366924e-1f), -1.2337005f), 1.f);
     // a quarter more: (c, s) -> (-s, c)
-    return f32x2{(k + 1) & 2 ? -a : a, k & 2 ? -b : b};
+    const float a = k & 1 ? s : c, b = k & 1 ? c : s;
+    return f32x2{__uint_as_float(__float_as_uint(a) ^ ((k + 1) << 30 & 0x80000000u)),
+                 __uint_as_float(__float_as_uint(b) ^ (k << 30 & 0x80000000u))};
 }
 
 __device__ __forceinline__ double position_at(const AxesProblem& p, uint32_t axis, uint32_t b, uint32_t n) {
@@ -50,279 +51,349 @@ __device__ __forceinline__ double position_at(const AxesProblem& p, uint32_t axi
     return static_cast<double>(static_cast<const int64_t*>(p.positions)[at]);
 }
 
-// A thread's channels of one head: U pairs of a rotated unit, or V channels that pass through.
-template <bool F32, bool HALVES, bool VEC>
+// A lane's channels of one head: U pairs of a rotated unit, or V channels that pass through.  V elements an access:
+// 16 bytes, two elements, or one.
+template <bool F32, bool HALVES, int V>
 struct Unit {
-    static constexpr int V = VEC ? (F32 ? 4 : 8) : 1;                // elements of an access
-    static constexpr int U = VEC ? (HALVES ? V : 4) : 1;             // pairs
-    static constexpr int N = VEC && !F32 && !HALVES ? 1 : 2;         // accesses
-    static constexpr int kElem = F32 ? 4 : 2;
-    static constexpr int kWords = VEC ? 4 : 1;
+    static constexpr int N = HALVES || V == 1 ? 2 : 1;              // accesses
+    static constexpr int U = HALVES || V == 1 ? V : V / 2;          // pairs
+    static constexpr int kElem = F32 ? 4 : 2, kBytes = V * kElem;
+    static constexpr int kWords = F32 ? V : (V + 1) / 2;            // of an access
+    // of a wavefront: 16 registers of channels a lane, as many bytes on their way
+    static constexpr uint32_t kRounds = 16 / (N * kWords) < 16 ? 16 / (N * kWords) : 16;
     uint32_t w[N][kWords];
 
     // byte offset of the second access from the first
-    static __device__ __forceinline__ uint32_t second(uint32_t pairs) {
-        return (HALVES ? pairs : VEC ? 4u : 1u) * kElem;
-    }
-    __device__ __forceinline__ void load(const char* at, uint32_t next, bool both) {
+    static __device__ __forceinline__ uint32_t second(uint32_t pairs) { return (HALVES ? pairs : 1u) * kElem; }
+
+    static __device__ __forceinline__ void get(uint32_t (&to)[kWords], const char* at) {
+        if constexpr (kBytes == 16) {
+            const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (i == 1 && !both) break;
-            const char* a = at + (i ? next : 0);
-            if constexpr (VEC) {
-                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[i][j] = v[j];
-            } else if constexpr (F32) {
-                w[i][0] = *reinterpret_cast<const uint32_t*>(a);
-            } else {
-                w[i][0] = *reinterpret_cast<const uint16_t*>(a);
-            }
+            for (int j = 0; j < 4; ++j) to[j] = v[j];
+        } else if constexpr (kBytes == 8) {
+            const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(at));
+            to[0] = v[0];
+            to[1 % kWords] = v[1];
+        } else if constexpr (kBytes == 4) {
+            to[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(at));
+        } else {
+            to[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(at));
         }
     }
-    __device__ __forceinline__ void store(char* at, uint32_t next, bool both) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (i == 1 && !both) break;
-            char* a = at + (i ? next : 0);
-            if constexpr (VEC) {
-                __builtin_nontemporal_store(u32x4{w[i][0], w[i][1], w[i][2], w[i][3]}, reinterpret_cast<u32x4*>(a));
-            } else if constexpr (F32) {
-                *reinterpret_cast<uint32_t*>(a) = w[i][0];
-            } else {
-                *reinterpret_cast<uint16_t*>(a) = static_cast<uint16_t>(w[i][0]);
-            }
+    // base: the same in every lane
+    static __device__ __forceinline__ void put(const uint32_t (&from)[kWords], char* base, uint32_t offset) {
+        char* at = base + offset;
+        if constexpr (kBytes == 16) {
+            stream_store16(stream_u32x4{from[0], from[1 % kWords], from[2 % kWords], from[3 % kWords]}, base, 0x80000000u,
+                           offset);
+        } else if constexpr (kBytes == 8) {
+            __builtin_nontemporal_store(u32x2{from[0], from[1 % kWords]}, reinterpret_cast<u32x2*>(at));
+        } else if constexpr (kBytes == 4) {
+            __builtin_nontemporal_store(from[0], reinterpret_cast<uint32_t*>(at));
+        } else {
+            __builtin_nontemporal_store(static_cast<uint16_t>(from[0]), reinterpret_cast<uint16_t*>(at));
         }
     }
-    static __device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
-    static __device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    __device__ __forceinline__ void load(const char* at, uint32_t next, bool rotated) {
+        get(w[0], at);
+        if (N == 2 && rotated) get(w[N - 1], at + next);
     }
-    static __device__ __forceinline__ void turn(float& e, float& o, float c, float s) {
-        const float x = fmaf(e, c, -(o * s));
-        o = fmaf(e, s, o * c);
-        e = x;
+    __device__ __forceinline__ void store(char* base, uint32_t offset, uint32_t next, bool rotated) const {
+        put(w[0], base, offset);
+        if (N == 2 && rotated) put(w[N - 1], base, offset + next);
     }
-    // keep: a bit for each pair that stays as it is
+    // element i of access a
+    __device__ __forceinline__ float element(int a, int i) const {
+        if constexpr (F32) return __uint_as_float(w[a][i]);
+        else return __uint_as_float(i % 2 ? w[a][i / 2] & 0xffff0000u : w[a][i / 2] << 16);
+    }
     __device__ __forceinline__ void rotate(const float (&c)[U], const float (&s)[U], uint32_t keep) {
-        if constexpr (F32) {
+        constexpr bool kApart = N == 2;  // e and o in different accesses
+        const Unit was = *this;
+        float v[2][U];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                // pair j's words: the two accesses' word j, or neighbours
-                uint32_t& we = HALVES || !VEC ? w[0][j % kWords] : w[(2 * j) / kWords][(2 * j) % kWords];
-                uint32_t& wo = HALVES || !VEC ? w[N - 1][j % kWords] : w[(2 * j + 1) / kWords][(2 * j + 1) % kWords];
-                float e = __uint_as_float(we), o = __uint_as_float(wo);
-                turn(e, o, c[j], s[j]);
-                if (!(keep >> j & 1)) {
-                    we = __float_as_uint(e);
-                    wo = __float_as_uint(o);
+        for (int j = 0; j < U; ++j) {
+            const float e = kApart ? element(0, j) : element(0, 2 * j), o = kApart ? element(N - 1, j) : element(0, 2 * j + 1);
+            v[0][j] = fmaf(e, c[j], -(o * s[j]));
+            v[1][j] = fmaf(e, s[j], o * c[j]);
+        }
+        auto at = [&](int a, int i) { return kApart ? v[a][i % U] : v[i % 2][i / 2 % U]; };
+#pragma unroll
+        for (int a = 0; a < N; ++a)
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if constexpr (F32) {
+                    w[a][i] = __float_as_uint(at(a, i));
+                } else {
+                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                    const f32x2 two = {at(a, 2 * i), V == 1 ? 0.f : at(a, 2 * i + 1)};
+                    w[a][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
                 }
             }
-        } else if constexpr (!VEC) {
-            float e = low(w[0][0]), o = low(w[N - 1][0]);
-            turn(e, o, c[0], s[0]);
-            if (!keep) {
-                w[0][0] = pack(e, 0.f);
-                w[N - 1][0] = pack(o, 0.f);
-            }
-        } else if constexpr (HALVES) {
+        if (keep == 0) return;
+        // some pairs stay as they were
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float e0 = low(w[0][j]), o0 = low(w[N - 1][j]), e1 = high(w[0][j]), o1 = high(w[N - 1][j]);
-                turn(e0, o0, c[(2 * j) % U], s[(2 * j) % U]);
-                turn(e1, o1, c[(2 * j + 1) % U], s[(2 * j + 1) % U]);
-                const uint32_t mask = (keep >> (2 * j) & 1 ? 0xffffu : 0u) | (keep >> (2 * j + 1) & 1 ? 0xffff0000u : 0u);
-                w[0][j] = (w[0][j] & mask) | (pack(e0, e1) & ~mask);
-                w[N - 1][j] = (w[N - 1][j] & mask) | (pack(o0, o1) & ~mask);
-            }
-        } else {
+        for (int a = 0; a < N; ++a)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float e = low(w[0][j]), o = high(w[0][j]);
-                turn(e, o, c[j % U], s[j % U]);
-                if (!(keep >> j & 1)) w[0][j] = pack(e, o);
+            for (int i = 0; i < kWords; ++i) {
+                constexpr int kPer = F32 ? 1 : 2;
+                uint32_t mask = 0;
+#pragma unroll
+                for (int h = 0; h < kPer; ++h) {
+                    const int pair = (kApart ? kPer * i + h : (kPer * i + h) / 2) % 32;
+                    if (keep >> pair & 1) mask |= F32 ? 0xffffffffu : 0xffffu << (16 * h);
+                }
+                w[a][i] = (was.w[a][i] & mask) | (w[a][i] & ~mask);
             }
-        }
     }
 };
 
-// What a workgroup covers: a segment of the head's pairs (and, in the last one, the channels that pass
-// through), or of the channels that pass through alone.
+// One wavefront a workgroup and few rounds a wavefront, in a grid as large as the work: the chip's memory runs fastest
+// with short-lived wavefronts that have a few kilobytes on their way (69360 tokens of 32 + 8 heads of 128 in bf16: 259
+// to 295 us with workgroups of four wavefronts that went through all heads of some tokens, in three forms; 238 us
+// so).  A wavefront takes a token, so that its addresses are scalar.  Its lanes hold a segment of a head (or of the
+// channels that pass through), of several heads side by side where that is short, and a round moves those.  The
+// segment's angles are formed once, a pair a lane, and handed over in LDS: loads of a frequency and an axis for each
+// of a unit's pairs, and of a position that waits for the axis, took longer than the channels (2 x 18360 tokens of
+// 4096 in bf16: 634 us so, 462 with the angles handed over, 405 us with none).
 struct AxesShape {
-    uint32_t segments;      // of pairs
-    uint32_t copies;        // segments of channels that pass through, 0: they belong to the last one of pairs
-    uint32_t seg_pairs;     // pairs of a segment (the last may have fewer)
-    uint32_t steps;         // tokens a step: those that the threads cover once, times this
-    uint32_t head_splits;   // workgroups that share out a token's heads
+    uint32_t segments;   // of pairs
+    uint32_t copies;     // segments of channels that pass through, 0: they belong to the last one of pairs
+    uint32_t seg_pairs;  // pairs of a segment (the last may have fewer)
+    uint32_t slots;      // most heads side by side in a wavefront
+    uint32_t q_rounds;
+    uint32_t rounds;     // of q and k
+    uint32_t together;   // tokens whose rounds are one wavefront's; 0: a token has groups of rounds, q's
+    uint32_t q_groups;   // before k's in the grid
+    uint32_t k_groups;
+    FastDiv by_planes, by_q_groups, by_k_groups, by_axes, by_pairs;
 };
 
-template <bool F32, bool HALVES, bool VEC>
-__global__ __launch_bounds__(256) void axes_rotate(AxesProblem p, AxesShape shape) {
-    using T = Unit<F32, HALVES, VEC>;
-    constexpr uint32_t U = T::U, V = T::V, kElem = T::kElem;
-    extern __shared__ __align__(16) f32x2 turns[];  // [2][tokens a step][pairs of the segment]
-    const uint32_t tid = threadIdx.x;
-    const uint32_t seg = blockIdx.y / shape.head_splits, split = blockIdx.y % shape.head_splits, b = blockIdx.z;
+constexpr uint32_t kMostAngles = 512;  // of several tokens
+constexpr float kStays = 2.f;  // in a cosine's place: the pair stays as it is
+
+template <bool F32, bool HALVES, int V, bool SOME>
+__global__ __launch_bounds__(64) void axes_rotate(AxesProblem p, AxesShape shape) {
+    using T = Unit<F32, HALVES, V>;
+    constexpr uint32_t U = T::U, kElem = T::kElem, kRounds = T::kRounds, kForms = SOME ? kMostAngles / 64 : U;
+    __shared__ double place[SOME ? 64 : 256];               // of the tokens on each axis
+    __shared__ __align__(16) f32x2 row[64 * kForms];  // of a segment's pairs, for each token
+    const uint32_t lane = threadIdx.x, b = blockIdx.y;
+    const uint32_t planes = shape.segments + shape.copies;
+    uint32_t rest = fast_div(blockIdx.x, shape.by_planes);
+    const uint32_t seg = blockIdx.x - rest * planes;
+    uint32_t n, round, last;  // the (first) token, its rounds [round, last)
+    uint32_t some = 1;        // tokens
+    if (SOME) {
+        n = rest * shape.together;
+        some = p.tokens - n < shape.together ? p.tokens - n : shape.together;
+        round = 0;
+        last = shape.rounds;
+    } else if (shape.together) {
+        n = rest;
+        round = 0;
+        last = shape.rounds;
+    } else if (rest < p.tokens * shape.q_groups) {
+        n = fast_div(rest, shape.by_q_groups);
+        round = (rest - n * shape.q_groups) * kRounds;
+        last = shape.q_rounds;
+    } else {
+        rest -= p.tokens * shape.q_groups;
+        n = fast_div(rest, shape.by_k_groups);
+        round = shape.q_rounds + (rest - n * shape.k_groups) * kRounds;
+        last = shape.rounds;
+    }
+    n += p.first_token;
     const uint32_t first = seg * shape.seg_pairs;  // pair
     const uint32_t P = seg >= shape.segments ? 0u
                        : p.pairs - first < shape.seg_pairs ? p.pairs - first : shape.seg_pairs;
 
-    // this thread's place in the head, and its slot among the threads that take heads in turn
+    // what the segment's angles need (a token's, or several tokens' side by side)
+    uint32_t axis[kForms], whose[kForms], which[kForms];
+    double turns[kForms], at = 0.0;
+    if (P) {
+        if (lane < p.axes * some) {
+            const uint32_t t = SOME ? fast_div(lane, shape.by_axes) : 0;
+            at = position_at(p, lane - t * p.axes, b, n + t);
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kForms; ++j) {
+            if (SOME && j * 64 >= shape.seg_pairs * some) break;
+            whose[j] = SOME ? fast_div(j * 64 + lane, shape.by_pairs) : 0;
+            which[j] = j * 64 + lane - whose[j] * shape.seg_pairs;
+            const uint32_t i = first + (which[j] < P ? which[j] : 0);
+            axis[j] = p.axis[i];
+            turns[j] = p.frequency_f32 ? static_cast<const float*>(p.frequencies)[i]
+                                       : static_cast<const double*>(p.frequencies)[i];
+        }
+    }
+
+    // this lane's place in the head, and which of the heads side by side it takes
     const uint32_t all_tail = (p.head_dim - 2 * p.pairs) / V, rot = P / U;
     uint32_t tail = 0, tail0 = 0;  // units that pass through, and the first of them
     if (shape.copies == 0) {
-        if (seg + 1 == shape.segments || shape.segments == 0) tail = all_tail;
+        if (seg + 1 == shape.segments) tail = all_tail;
     } else if (seg >= shape.segments) {
-        tail0 = (seg - shape.segments) * kThreads;
-        tail = all_tail - tail0 < kThreads ? all_tail - tail0 : kThreads;
+        tail0 = (seg - shape.segments) * 64;
+        tail = all_tail - tail0 < 64 ? all_tail - tail0 : 64;
     }
-    const uint32_t units = rot + tail, slots = kThreads / units;
-    const uint32_t unit = tid % units, slot = tid / units;
-    const uint32_t heads = p.q.heads + p.k.heads;
-    const uint32_t head_slots = slots < heads ? slots : heads, token_slots = slots / head_slots;
-    const uint32_t head_slot = slot % head_slots, token_slot = slot / head_slots;
-    const bool rotated = unit < rot, working = token_slot < token_slots;
+    const uint32_t units = rot + tail, unit = lane % units, slot = lane / units;
+    const bool rotated = unit < rot;
     const uint32_t pair = first + unit * U;
     const uint32_t channel = rotated ? (HALVES ? pair : 2 * pair) : 2 * p.pairs + (tail0 + unit - rot) * V;
     const uint32_t next = T::second(p.pairs);
-    const bool both = rotated;
-    uint32_t keep = 0;
-    if (rotated)
+    // the rounds' channels set out
+    T x[kRounds];
+    bool in[kRounds];
+    // f(round, token, whether this lane has a head, the first head's channels, bytes from there: below 2^31)
+    auto each = [&](bool out, auto f) {
+        uint32_t r = round, t = 0, h = 0, heads = 0;
+        int64_t head = 0, step = 0;
+        char* at = nullptr;
+        bool fresh = true;
 #pragma unroll
-        for (uint32_t j = 0; j < U; ++j) keep |= (p.axis[pair + j] >= p.axes ? 1u : 0u) << j;
-
-    // the pair whose angles this thread forms
-    const uint32_t lanes = P ? kThreads / P : 0u;  // tokens that the threads cover once
-    const uint32_t my_pair = P ? tid % P : 0u, my_token = P ? tid / P : 0u;
-    const bool forms = P && my_token < lanes;
-    const uint32_t step_tokens = P ? lanes * shape.steps : shape.steps;
-    uint32_t my_axis = 0xff;
-    double my_frequency = 0.0;
-    if (forms) {
-        my_axis = p.axis[first + my_pair];
-        my_frequency = p.frequency_f32 ? static_cast<const float*>(p.frequencies)[first + my_pair]
-                                       : static_cast<const double*>(p.frequencies)[first + my_pair];
-    }
-    const bool turned = forms && my_axis < p.axes;
-    double at[kMaxSteps];
-    auto fetch = [&](uint32_t n0) {
-#pragma unroll
-        for (uint32_t i = 0; i < kMaxSteps; ++i) {
-            const uint32_t n = n0 + i * lanes + my_token;
-            at[i] = 0.0;
-            if (i < shape.steps && turned && n < p.tokens) at[i] = position_at(p, my_axis, b, n);
+        for (uint32_t i = 0; i < kRounds; ++i) {
+            if (r >= last) {
+                if (!SOME || ++t >= some) break;
+                r = round;
+                fresh = true;
+            }
+            if (fresh || r == shape.q_rounds) {
+                const bool is_q = r < shape.q_rounds;
+                h = (is_q ? r : r - shape.q_rounds) * shape.slots;
+                heads = is_q ? p.q.heads : p.k.heads;
+                int64_t sample, token;
+                if (out) {
+                    at = is_q ? p.q.out : p.k.out;
+                    sample = is_q ? p.q.out_batch : p.k.out_batch;
+                    token = is_q ? p.q.out_token : p.k.out_token;
+                    head = is_q ? p.q.out_head : p.k.out_head;
+                } else {
+                    at = const_cast<char*>(is_q ? p.q.in : p.k.in);
+                    sample = is_q ? p.q.in_batch : p.k.in_batch;
+                    token = is_q ? p.q.in_token : p.k.in_token;
+                    head = is_q ? p.q.in_head : p.k.in_head;
+                }
+                at += (b * sample + (n + t) * token + h * head) * kElem;
+                step = shape.slots * head * kElem;
+                fresh = false;
+            }
+            f(i, t, h + slot < heads, at, (slot * static_cast<uint32_t>(head) + channel) * kElem);
+            ++r;
+            h += shape.slots;
+            at += step;
         }
     };
+    each(false, [&](uint32_t i, uint32_t, bool there, const char* at, uint32_t offset) {
+        in[i] = slot < shape.slots && there;
+        if (in[i]) x[i].load(at + offset, next, rotated);
+    });
 
-    const uint32_t stride = gridDim.x * step_tokens;
-    uint32_t phase = 0;
-    uint32_t n0 = blockIdx.x * step_tokens;
-    fetch(n0);
-    for (; n0 < p.tokens; n0 += stride, phase ^= 1) {
-        f32x2* mine = turns + phase * step_tokens * P;
-        if (P) {
+    if (P) {
+        if (lane < p.axes * some) place[lane] = at;
+        for (uint32_t a = 64 + lane; a < p.axes; a += 64) place[a] = position_at(p, a, b, n);
+        __syncthreads();
+        const double unit_turns = p.inverse ? -0.15915494309189533577 : 0.15915494309189533577;  // 1 / (2 pi)
 #pragma unroll
-            for (uint32_t i = 0; i < kMaxSteps; ++i) {
-                if (i >= shape.steps || !forms) break;
-                f32x2 cs = cos_sin(at[i], my_frequency);
-                if (p.inverse) cs[1] = -cs[1];
-                mine[(i * lanes + my_token) * P + my_pair] = cs;
-            }
-            if (n0 + stride < p.tokens) fetch(n0 + stride);
-            __syncthreads();
+        for (uint32_t j = 0; j < kForms; ++j) {
+            if (SOME && j * 64 >= shape.seg_pairs * some) break;
+            if (which[j] < P && whose[j] < some)
+                row[j * 64 + lane] = axis[j] < p.axes
+                                         ? cos_sin(place[whose[j] * p.axes + axis[j]], turns[j] * unit_turns)
+                                         : f32x2{kStays, 0.f};
         }
-        const uint32_t some = p.tokens - n0 < step_tokens ? p.tokens - n0 : step_tokens;
-        if (!working) continue;
-        for (uint32_t t = token_slot; t < some; t += token_slots) {
-            const uint32_t n = n0 + t;
-            float c[U], s[U];
-            if (rotated) {
-                const f32x2* cs = mine + t * P + unit * U;
-                if constexpr (VEC) {  // P and U are multiples of 4
-#pragma unroll
-                    for (uint32_t j = 0; j < U; j += 2) {
-                        const f32x4 two = *reinterpret_cast<const f32x4*>(cs + j);
-                        c[j] = two[0];
-                        s[j] = two[1];
-                        c[j + 1] = two[2];
-                        s[j + 1] = two[3];
-                    }
-                } else {
-                    c[0] = cs[0][0];
-                    s[0] = cs[0][1];
-                }
-            }
-            const char* q_in = p.q.in + (b * p.q.in_batch + n * p.q.in_token + channel) * kElem;
-            const char* k_in = p.k.in + (b * p.k.in_batch + n * p.k.in_token + channel) * kElem;
-            char* q_out = p.q.out + (b * p.q.out_batch + n * p.q.out_token + channel) * kElem;
-            char* k_out = p.k.out + (b * p.k.out_batch + n * p.k.out_token + channel) * kElem;
-            auto place = [&](uint32_t h, const char*& in, char*& out) {
-                const bool is_q = h < p.q.heads;
-                const uint32_t hk = h - p.q.heads;
-                in = is_q ? q_in + h * p.q.in_head * kElem : k_in + hk * p.k.in_head * kElem;
-                out = is_q ? q_out + h * p.q.out_head * kElem : k_out + hk * p.k.out_head * kElem;
-            };
-            const uint32_t h_step = head_slots * shape.head_splits;
-            for (uint32_t h = split * head_slots + head_slot; h < heads; h += 2 * h_step) {
-                const bool more = h + h_step < heads;
-                const char *in0, *in1;
-                char *out0, *out1;
-                T x, y;
-                place(h, in0, out0);
-                place(more ? h + h_step : h, in1, out1);
-                x.load(in0, next, both);
-                if (more) y.load(in1, next, both);
-                if (rotated) x.rotate(c, s, keep);
-                x.store(out0, next, both);
-                if (more) {
-                    if (rotated) y.rotate(c, s, keep);
-                    y.store(out1, next, both);
-                }
-            }
-        }
+        __syncthreads();
     }
+    float c[U], s[U];
+    uint32_t keep = 0;
+    auto take = [&](uint32_t t) {
+        const f32x2* cs = row + t * shape.seg_pairs + unit * U;
+        if constexpr (U % 2 == 0) {
+#pragma unroll
+            for (uint32_t j = 0; j < U; j += 2) {
+                const f32x4 two = *reinterpret_cast<const f32x4*>(cs + j);
+                c[j] = two[0];
+                s[j] = two[1];
+                c[j + 1] = two[2];
+                s[j + 1] = two[3];
+            }
+        } else {
+            c[0] = cs[0][0];
+            s[0] = cs[0][1];
+        }
+        keep = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) keep |= (c[j] == kStays ? 1u : 0u) << j;
+    };
+    if (!SOME && rotated) take(0);
+    uint32_t taken = ~0u;
+    each(true, [&](uint32_t i, uint32_t t, bool, char* at, uint32_t offset) {
+        if (SOME && rotated && t != taken) take(t);
+        taken = t;
+        if (!in[i]) return;
+        if (rotated) x[i].rotate(c, s, keep);
+        x[i].store(at, offset, next, rotated);
+    });
 }
 
-template <bool F32, bool HALVES, bool VEC>
+template <bool F32, bool HALVES, int V>
 hipError_t launch(const AxesProblem& p, hipStream_t stream) {
-    using T = Unit<F32, HALVES, VEC>;
+    using T = Unit<F32, HALVES, V>;
     AxesShape s;
-    const uint32_t tail = (p.head_dim - 2 * p.pairs) / T::V, heads = p.q.heads + p.k.heads;
-    // as many pairs a segment as threads form at once
-    s.segments = (p.pairs + kThreads - 1) / kThreads;
-    s.seg_pairs = p.pairs < kThreads ? (p.pairs ? p.pairs : 1) : kThreads;
-    const uint32_t last = p.pairs - (s.segments ? s.segments - 1 : 0) * s.seg_pairs;
-    s.copies = last / T::U + tail <= kThreads ? 0 : (tail + kThreads - 1) / kThreads;
-    const uint32_t lanes = kThreads / s.seg_pairs;
-    const uint32_t units = s.seg_pairs / T::U, slots = units < kThreads ? kThreads / units : 1;
-    const uint32_t token_slots = slots > heads ? slots / heads : 1;
-    const uint32_t rounds = (heads + slots - 1) / slots;  // heads a thread takes of one token
-    const uint32_t planes = (s.segments + s.copies > 0 ? s.segments + s.copies : 1) * p.batch;
-    // Steps long enough that a thread moves 8 units between barriers, while the chip stays filled
-    s.steps = 1;
-    while (s.steps < kMaxSteps && s.steps * lanes * rounds < 8 * token_slots &&
-           static_cast<uint64_t>(planes) * (p.tokens / (2 * s.steps * lanes)) >= 2048)
-        s.steps *= 2;
-    const uint32_t groups = (p.tokens + s.steps * lanes - 1) / (s.steps * lanes);
-    const uint64_t blocks = static_cast<uint64_t>(planes) * groups;
-    s.head_splits = 1;
-    if (blocks < 512) {
-        const uint32_t want = static_cast<uint32_t>((512 + blocks - 1) / blocks);
-        s.head_splits = want < rounds ? want : rounds;
+    const uint32_t tail = (p.head_dim - 2 * p.pairs) / V, most_pairs = 64 * T::U;
+    s.segments = (p.pairs + most_pairs - 1) / most_pairs;
+    s.seg_pairs = p.pairs < most_pairs ? p.pairs : most_pairs;
+    const uint32_t last = p.pairs - (s.segments - 1) * s.seg_pairs;
+    s.copies = last / T::U + tail <= 64 ? 0 : (tail + 63) / 64;
+    const uint32_t planes = s.segments + s.copies;
+    // heads side by side, as many as fit in every segment; what a lane adds to the first one's address stays below 2^31
+    int64_t head = 1;
+    for (const AxesTensor* t : {&p.q, &p.k}) {
+        head = head > t->in_head ? head : t->in_head;
+        head = head > t->out_head ? head : t->out_head;
     }
-    const uint32_t most = 4096 / planes > 0 ? 4096 / planes : 1;
-    const dim3 grid(groups < most ? groups : most,
-                    (s.segments + s.copies > 0 ? s.segments + s.copies : 1) * s.head_splits, p.batch);
-    const size_t lds = size_t(2) * s.steps * lanes * s.seg_pairs * sizeof(f32x2);
-    axes_rotate<F32, HALVES, VEC><<<grid, kThreads, lds, stream>>>(p, s);
+    const int64_t reach = (int64_t(1) << 30) / (head * T::kElem);
+    const uint32_t units = planes > 1 ? 64 : s.seg_pairs / T::U + tail;
+    s.slots = reach < 63 && static_cast<uint32_t>(reach) + 1 < 64 / units ? static_cast<uint32_t>(reach) + 1 : 64 / units;
+    s.q_rounds = (p.q.heads + s.slots - 1) / s.slots;
+    s.rounds = s.q_rounds + (p.k.heads + s.slots - 1) / s.slots;
+    s.together = s.rounds <= T::kRounds ? 1 : 0;
+    if (s.together && static_cast<uint64_t>(p.tokens) * p.batch * planes >= 16384) {
+        // several tokens, if that leaves wavefronts enough to fill the chip
+        const uint32_t rows = kMostAngles / s.seg_pairs, places = 64 / p.axes;
+        uint32_t t = T::kRounds / s.rounds;
+        t = t < rows ? t : rows;
+        t = t < places ? t : places;
+        s.together = t > 1 ? t : 1;
+    }
+    s.q_groups = (s.q_rounds + T::kRounds - 1) / T::kRounds;
+    s.k_groups = (s.rounds - s.q_rounds + T::kRounds - 1) / T::kRounds;
+    s.by_planes = make_fastdiv(planes);
+    s.by_q_groups = make_fastdiv(s.q_groups ? s.q_groups : 1);
+    s.by_k_groups = make_fastdiv(s.k_groups ? s.k_groups : 1);
+    s.by_axes = make_fastdiv(p.axes);
+    s.by_pairs = make_fastdiv(s.seg_pairs);
+    const uint32_t jobs = planes * (s.together ? 1 : s.q_groups + s.k_groups);  // of a token or some: 2^25 at most
+    // a launch holds fewer than 2^32 threads a dimension; whole groups of tokens
+    const uint32_t most = ((uint32_t(1) << 26) - 1) / jobs / 64 * 64;
+    for (uint64_t n = 0; n < p.tokens; n += most) {
+        AxesProblem some = p;
+        some.first_token = static_cast<uint32_t>(n);
+        some.tokens = p.tokens - some.first_token < most ? p.tokens - some.first_token : most;
+        const uint32_t groups = s.together > 1 ? (some.tokens + s.together - 1) / s.together : some.tokens;
+        const dim3 grid(groups * jobs, p.batch);
+        if (s.together > 1) axes_rotate<F32, HALVES, V, true><<<grid, 64, 0, stream>>>(some, s);
+        else axes_rotate<F32, HALVES, V, false><<<grid, 64, 0, stream>>>(some, s);
+    }
     return hipGetLastError();
 }
 
 template <bool F32, bool HALVES>
 hipError_t launch_of(const AxesProblem& p, hipStream_t stream) {
-    return p.vectors ? launch<F32, HALVES, true>(p, stream) : launch<F32, HALVES, false>(p, stream);
+    if (p.vector == 1) return launch<F32, HALVES, 1>(p, stream);
+    if (p.vector == 2) return launch<F32, HALVES, 2>(p, stream);
+    return launch<F32, HALVES, F32 ? 4 : 8>(p, stream);
 }
 
 }  // namespace

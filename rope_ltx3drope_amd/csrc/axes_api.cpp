@@ -177,10 +177,18 @@ int ltx3drope_axes_apply(const ltx3drope_axes_t* call, void* stream, int* reason
     p.inverse = c.inverse != 0;
     p.frequency_f32 = c.frequency_type == LTX3DROPE_FREQUENCY_F32;
     p.position_type = c.position_type;
-    p.vectors = axes_vector_widths(f32, p.halves, p.head_dim, p.pairs);
-    for (int i = 0; i < n && p.vectors; ++i) {
-        p.vectors = reinterpret_cast<uintptr_t>(t[i].p) % 16 == 0;
-        for (int j = 0; j < t[i].n; ++j) p.vectors = p.vectors && t[i].dims[j].stride * es % 16 == 0;
+    p.vector = 1;
+    for (uint32_t v : {f32 ? 4u : 8u, 2u}) {
+        const int64_t bytes = v * es;
+        bool fit = axes_vector_widths(v, p.halves, p.head_dim, p.pairs);
+        for (int i = 0; i < n && fit; ++i) {
+            fit = reinterpret_cast<uintptr_t>(t[i].p) % bytes == 0;
+            for (int j = 0; j < t[i].n; ++j) fit = fit && t[i].dims[j].stride * es % bytes == 0;
+        }
+        if (fit) {
+            p.vector = v;
+            break;
+        }
     }
     DeviceGuard guard(device);
     if (launch_axes(p, static_cast<hipStream_t>(stream)) != hipSuccess) return LTX3DROPE_E_HIP;

@@ -112,6 +112,16 @@ def test_sizes(B, S, Hq, Hk, pairing, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pairing", PAIRINGS)
+@pytest.mark.parametrize("B,S,Hq,Hk,D,P,axes", [(1, 16385, 3, 1, 64, 32, 3), (2, 8193, 2, 0, 20, 6, 1), (3, 6001, 1, 1, 16, 4, 30),
+                                                (1, 16399, 1, 1, 6, 3, 70), (1, 3001, 1, 1, 1366, 683, 3),
+                                                (1, 5003, 1, 0, 400, 150, 2)])
+def test_many_tokens_of_few_channels(B, S, Hq, Hk, D, P, axes, pairing, dtype):
+    """Tokens enough that a wavefront takes several, the last one fewer."""
+    run(*make(B, S, Hq, Hk, D, P, axes, dtype, S), pairing)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("S", [1, 3, 500])
 @pytest.mark.parametrize("D", [16, 4096, 4098, 8192, 1000])
 def test_whole_width_as_one_head(D, S, dtype):
