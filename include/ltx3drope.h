@@ -687,20 +687,22 @@ int64_t ltx3drope_q8_matmul_workspace(const ltx3drope_q8_matmul_t* call);
  * in fp32, each step rounded once to nearest even.  x [rows, dim] of `dtype` (F32 or BF16),
  * q [rows, dim], contiguous.  blocks = 0: a block is 128 numbers of a row (the last of a row may be
  * shorter), scale [rows, ceil(dim / 128)].  blocks = 1 (weights): 128 x 128, scale
- * [ceil(rows / 128), ceil(dim / 128)].  q_turned and scale_turned (both or neither) receive the same of x
+ * [ceil(rows / 128), ceil(dim / 128)].  Scales have strides (row, block) in numbers: (1, rows), a
+ * block's scales of all rows side by side, is what a product of many rows reads fastest.  q_turned and scale_turned (both or neither) receive the same of x
  * turned over, [dim, rows], in the same pass: blocks of 128 numbers of a column with their
  * own scales, or the same 128 x 128 blocks; q_turned's rows are turned_pitch bytes apart (>= rows; it takes
  * dim * turned_pitch bytes, and those from `rows` on to the next multiple of 16 may be set to zero).
  * A block of zeros gets scale 0 and zeros (so does one so small that its scale rounds to 0).  A block with a
  * NaN or an infinity keeps that as its scale and gets zeros: its products come out NaN.
  * rows = 0 is an empty call.  E_INVALID: a NULL descriptor, blocks other than 0 or 1, q_turned without
- * scale_turned or the reverse, turned_pitch < rows.  E_UNSUPPORTED: DTYPE; NONPOSITIVE_DIM (dim <= 0, rows < 0);
- * TOO_LARGE (rows or dim of 2^31 or more, turned_pitch of 2^32 or more, more than 2^24 - 1 tiles of 128 x 128); NULLPTR; ALIGN;
- * OVERLAP; NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.  E_HIP.  Asynchronous on `stream`, allocates nothing.
+ * scale_turned or the reverse, turned_pitch < rows, a stride < 0.  E_UNSUPPORTED: DTYPE; NONPOSITIVE_DIM (dim <= 0,
+ * rows < 0); TOO_LARGE (rows, dim or a stride of 2^31 or more, turned_pitch of 2^32 or more, scales over 2^58
+ * numbers or more, more than 2^24 - 1 tiles of 128 x 128); NULLPTR; OVERLAP (two scales in one place); ALIGN; OVERLAP; NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.  E_HIP.  Asynchronous on `stream`, allocates nothing.
  */
 typedef struct {
     int32_t dtype, blocks;
     int64_t rows, dim, turned_pitch;
+    int64_t scale_strides[2], scale_turned_strides[2]; /* row, block */
     const void* x;
     void* q;
     float* scale;
@@ -714,20 +716,21 @@ int ltx3drope_f8_quantize(const ltx3drope_f8_quantize_t* call, void* stream, int
  *     y[m][n] = sum_kb a_scale[m][kb] * b_scale[n][kb] * (sum over k of block kb of a[m][k] * b[n][k]) + bias[n]
  * a [tokens, dim] and b [out, dim] e4m3, their rows a_pitch and b_pitch bytes apart (>= dim); a_scale [tokens,
  * ceil(dim / 128)]; b_scale [ceil(out / 128), ceil(dim / 128)] (b_rows = 0: 128 x 128 blocks of weights) or [out,
- * ceil(dim / 128)] (b_rows = 1); bias [out] fp32 or NULL; y [tokens, out] of `dtype` (F32 or BF16),
+ * ceil(dim / 128)] (b_rows = 1), of any strides (row, block) >= 0 in numbers; bias [out] fp32 or NULL; y [tokens, out] of `dtype` (F32 or BF16),
  * contiguous, rounded once.  Products are exact and sums fp32, but for more than 16 tokens with y in
  * BF16: there the products of each 8 neighbours of k are added by the matrix cores' 8-bit units, which
  * keep 2^-13 of the largest of them.  Sums are added in a fixed order: equal inputs give equal bits.  The gradients are products of the same kind: of the input
  * from the output's and the turned weights, of the weights from both turned operands (b_rows = 1).
  * `workspace` as for ltx3drope_gated_ffn.  tokens = 0 or out = 0 is an empty call.  E_INVALID: a NULL
- * descriptor, b_rows other than 0 or 1, a pitch < dim, a workspace that is too small.  E_UNSUPPORTED:
- * DTYPE; NONPOSITIVE_DIM; TOO_LARGE (dim of 2^21 or more, a pitch of 2^22 or more, tokens or out of 2^26 or more, or
- * more than 2^23 output tiles of 64 x 32); NULLPTR; ALIGN; OVERLAP; NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.
+ * descriptor, b_rows other than 0 or 1, a pitch < dim, a stride < 0, a workspace that is too small.  E_UNSUPPORTED:
+ * DTYPE; NONPOSITIVE_DIM; TOO_LARGE (dim of 2^21 or more, a pitch of 2^22 or more, scales whose rows are 2^20 or
+ * more or whose blocks 2^31 or more apart, tokens or out of 2^26 or more, or more than 2^23 output tiles of 64 x 32); NULLPTR; ALIGN; OVERLAP; NOT_DEVICE_PTR, TABLE_DEVICE, EXTENT.
  * E_HIP.  Asynchronous on `stream`, allocates nothing.
  */
 typedef struct {
     int32_t dtype, b_rows;
     int64_t tokens, dim, out, a_pitch, b_pitch;
+    int64_t a_scale_strides[2], b_scale_strides[2]; /* row, block */
     const void *a, *b;
     const float *a_scale, *b_scale, *bias;
     void* y;

@@ -987,6 +987,20 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
     return out
 
 
+def _f8_scale_strides(t, rows, index):
+    """The (row, block) strides of scales [*rows, blocks]; leading dimensions have to be one."""
+    if t.get_device() != index or index < 0:
+        raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
+    s = t.stride()
+    if t.numel() == 0:
+        return 0, 0
+    row = s[-2] if rows else 0
+    for i in range(rows - 1):
+        if t.shape[i] != 1 and s[i] != s[i + 1] * t.shape[i + 1]:
+            raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+    return row, s[-1]
+
+
 def _f8_quantize(x, blocks, turned, q_out, scale_out, stream, what):
     torch = _torch()
     xs, index, device = x.shape, x.get_device(), x.device
@@ -995,28 +1009,42 @@ def _f8_quantize(x, blocks, turned, q_out, scale_out, stream, what):
         raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
     dim = xs[-1]
     rows = x.numel() // dim if dim else 0
-    across = -(-dim // 128)
-    scales = (-(-rows // 128), across) if blocks else xs[:-1] + (across,)
-    _operands(index, (x, xs, x.dtype), (q_out, xs, f8), (scale_out, scales, f32))
+    across, down = -(-dim // 128), -(-rows // 128)
+    scales = (down, across) if blocks else xs[:-1] + (across,)
+    _operands(index, (x, xs, x.dtype), (q_out, xs, f8))
+    strides = (across, 1) if blocks else (1, rows)
+    if scale_out is not None:
+        if scale_out.shape != scales or scale_out.dtype is not f32:
+            raise Ltx3dRopeUnsupported("SHAPE_MISMATCH" if scale_out.shape != scales else "DTYPE")
+        strides = _f8_scale_strides(scale_out, len(scales) - 1, index)
 
     def outputs():
         q = torch.empty_like(x, dtype=f8) if q_out is None else q_out
-        scale = x.new_empty(scales, dtype=f32) if scale_out is None else scale_out
+        if scale_out is not None:
+            scale = scale_out
+        elif blocks:
+            scale = x.new_empty(scales, dtype=f32)
+        else:  # a block's scales of all rows side by side
+            scale = x.new_empty((across, *xs[:-1]), dtype=f32)
+            scale = scale.t() if len(xs) == 2 else scale.movedim(0, -1)
         if not turned:
             return q, scale
         # rows that start on 128 bytes: a product then copies them straight to LDS
-        pitch = -(-rows // 128) * 128
-        t = torch.empty(dim, pitch, dtype=f8, device=device)
-        down = torch.empty((across, scales[0]) if blocks else (dim, -(-rows // 128)), dtype=f32, device=device)
-        return q, scale, t[:, :rows], down
+        t = torch.empty(dim, down * 128, dtype=f8, device=device)
+        scale_t = (torch.empty(across, down, dtype=f32, device=device) if blocks
+                   else torch.empty(down, dim, dtype=f32, device=device).t())
+        return q, scale, t[:, :rows], scale_t
 
     outs = outputs() if stream is None else _empty(stream, outputs)
     reason = ctypes.c_int(0)
     _lib.lib()
-    more = (outs[2].data_ptr(), outs[3].data_ptr()) if turned else (0, 0)
+    if turned:
+        pitch, t_strides, more = down * 128, outs[3].stride(), (outs[2].data_ptr(), outs[3].data_ptr())
+    else:
+        pitch, t_strides, more = 0, (0, 0), (0, 0)
     st = _lib.f8_quantize(
-        _lib.F8_QUANTIZE_BYTES.pack(_dtype_code(x), blocks, rows, dim, -(-rows // 128) * 128 if turned else 0,
-                                    x.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), *more),
+        _lib.F8_QUANTIZE_BYTES.pack(_dtype_code(x), blocks, rows, dim, pitch, *strides, *t_strides, x.data_ptr(),
+                                    outs[0].data_ptr(), outs[1].data_ptr(), *more),
         _raw_stream(index, stream), ctypes.byref(reason))
     _finish(st, reason, what)
     return outs
@@ -1025,7 +1053,7 @@ def _f8_quantize(x, blocks, turned, q_out, scale_out, stream, what):
 def f8_quantize(x, *, turned: bool = False, q_out=None, scale_out=None, stream=None):
     """Rows to 8-bit floating point: (q float8_e4m3fn like x, scale float32 [..., ceil(dim / 128)]) with scale =
     max |block| / 448 for each 128 numbers of a row and q = x / scale rounded.  x [..., dim], float32 or
-    bfloat16.
+    bfloat16.  The scales lie block by block (a view), as a product of many rows reads them fastest.
 
     turned=True (x [rows, dim]) gives (q, scale, q_turned, scale_turned) in one pass: the same of x's transpose
     [dim, rows], blocks of 128 rows of each column, for the products of a backward pass."""
@@ -1044,8 +1072,8 @@ def f8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
 
     a float8_e4m3fn [..., dim] with a_scale float32 [..., ceil(dim / 128)] and b [out, dim] with b_scale
     [ceil(out / 128), ceil(dim / 128)] (as f8_quantize_weight gives it) or [out, ceil(dim / 128)]
-    (f8_quantize); two-dimensional operands may have rows further apart than dim.  bias float32 [out] or
-    None; dtype of the result: bfloat16 (default) or float32.
+    (f8_quantize); scales of any strides, two-dimensional operands with rows further apart than dim.  bias
+    float32 [out] or None; dtype of the result: bfloat16 (default) or float32.
 
     Of y = x w^T the gradients are f8_matmul(dy, ., w_turned, .) and f8_matmul(dy_turned, ., x_turned, .)."""
     torch = _torch()
@@ -1072,16 +1100,20 @@ def f8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
             pitches.append(max(t.stride(0), dim))
         else:
             raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
-    _operands(index, (a_scale, rows + (across,), f32), (b_scale, (n if b_rows else -(-n // 128), across), f32),
-              (bias, channels, f32), (out, rows + channels, dtype))
+    if a_scale.shape != rows + (across,) or b_scale.shape != (n if b_rows else -(-n // 128), across):
+        raise Ltx3dRopeUnsupported("SHAPE_MISMATCH")
+    if a_scale.dtype is not f32 or b_scale.dtype is not f32:
+        raise Ltx3dRopeUnsupported("DTYPE")
+    strides = (*_f8_scale_strides(a_scale, len(rows), index), *_f8_scale_strides(b_scale, 1, index))
+    _operands(index, (bias, channels, f32), (out, rows + channels, dtype))
     if out is None:
         shape = rows + channels
         out = (a_scale.new_empty(shape, dtype=dtype) if stream is None
                else _empty(stream, lambda: a_scale.new_empty(shape, dtype=dtype)))
     _lib.lib()
     pack = _lib.F8_BYTES.pack
-    head = (_dtype_code(out), b_rows, a.numel() // dim if dim else 0, dim, n, *pitches, a.data_ptr(), b.data_ptr(),
-            a_scale.data_ptr(), b_scale.data_ptr(), _ptr(bias), out.data_ptr())
+    head = (_dtype_code(out), b_rows, a.numel() // dim if dim else 0, dim, n, *pitches, *strides, a.data_ptr(),
+            b.data_ptr(), a_scale.data_ptr(), b_scale.data_ptr(), _ptr(bias), out.data_ptr())
     descriptor = pack(*head, 0, 0)
     ws, size = _workspace(stream, _lib.f8_matmul_workspace, descriptor, device)
     reason = ctypes.c_int(0)

@@ -140,12 +140,14 @@ class Q8Matmul(ctypes.Structure):
 
 class F8Quantize(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("blocks", ctypes.c_int32)] + [(n, i64) for n in (
-        "rows", "dim", "turned_pitch")] + [(n, vp) for n in ("x", "q", "scale", "q_turned", "scale_turned")]
+        "rows", "dim", "turned_pitch")] + [(n, i64 * 2) for n in ("scale_strides", "scale_turned_strides")] + [
+        (n, vp) for n in ("x", "q", "scale", "q_turned", "scale_turned")]
 
 
 class F8Matmul(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("b_rows", ctypes.c_int32)] + [(n, i64) for n in (
-        "tokens", "dim", "out", "a_pitch", "b_pitch")] + [(n, vp) for n in (
+        "tokens", "dim", "out", "a_pitch", "b_pitch")] + [
+        (n, i64 * 2) for n in ("a_scale_strides", "b_scale_strides")] + [(n, vp) for n in (
             "a", "b", "a_scale", "b_scale", "bias", "y", "workspace")] + [("workspace_bytes", i64)]
 
 
@@ -165,8 +167,8 @@ LAYER_NORM_BACKWARD_BYTES = struct.Struct("@4i3qf16Pq")
 FFN_BYTES = struct.Struct("@2i3q7Pq")
 FFN_BACKWARD_BYTES = struct.Struct("@2i3q10Pq")
 Q8_BYTES = struct.Struct("@2i3q7Pq")
-F8_QUANTIZE_BYTES = struct.Struct("@2i3q5P")
-F8_BYTES = struct.Struct("@2i5q7Pq")
+F8_QUANTIZE_BYTES = struct.Struct("@2i7q5P")
+F8_BYTES = struct.Struct("@2i9q7Pq")
 AXES_BYTES = struct.Struct("@6i21q7P")
 
 # entry points that take a descriptor as bytes (bound in lib())

@@ -111,18 +111,20 @@ hipError_t launch_q8_quantize(const void* x, void* q, float* scale, uint32_t row
 
 // The linear layer in 8-bit floating point (f8.hip): a [tokens, dim] and b [out, dim] e4m3, their rows a_pitch and
 // b_pitch bytes apart, y [tokens, out]; a scale for 128 of k: a_scale [tokens, blocks], b_scale [out, blocks]
-// (b_rows) or [out / 128, blocks].
+// (b_rows) or [out / 128, blocks], with strides in numbers.
 struct F8Problem {
     const void *a, *b;
     const float *a_scale, *b_scale, *bias;
     void* y;
     void* workspace;
-    uint64_t a_pitch, b_pitch;
+    uint64_t a_pitch, b_pitch, a_scale_block, b_scale_block;
+    uint32_t a_scale_row, b_scale_row;
     uint32_t tokens, dim, out;
     bool b_rows;
 };
-constexpr int64_t kF8MaxDim = int64_t(1) << 21;    // 256 rows of 2^21 scales / 128 and ...
-constexpr int64_t kF8MaxPitch = int64_t(1) << 22;  // ... 256 rows of this many bytes stay within 2^31
+constexpr int64_t kF8MaxDim = int64_t(1) << 21;
+constexpr int64_t kF8MaxPitch = int64_t(1) << 22;     // 256 rows of this many bytes and ...
+constexpr int64_t kF8MaxScaleRow = int64_t(1) << 20;  // ... of this many scales stay within 2^31
 size_t f8_workspace(const F8Problem& p);
 hipError_t launch_f8(const F8Problem& p, bool f32, hipStream_t stream);
 
@@ -133,6 +135,7 @@ struct F8Quantize {
     void *q, *q_turned;
     float *scale, *scale_turned;
     uint64_t turned_pitch;
+    uint64_t scale_row, scale_block, turned_row, turned_block;  // strides in numbers
     uint32_t rows, dim;
     bool blocks;
     bool turned_chunks;  // q_turned starts on 16 bytes and so does each of its rows, with room for whole pieces

@@ -166,6 +166,20 @@ Q8Problem q8_problem(const ltx3drope_q8_matmul_t& c) {
     return p;
 }
 
+// Bytes that rows x blocks scales with these strides (row, block) reach over; the callers' limits keep it below
+// 2^61.
+constexpr int64_t kF8MaxScaleBlock = int64_t(1) << 31;
+size_t scale_bytes(size_t rows, size_t blocks, const int64_t (&strides)[2]) {
+    return ((rows - 1) * static_cast<size_t>(strides[0]) + (blocks - 1) * static_cast<size_t>(strides[1]) + 1) * 4;
+}
+
+// Whether no two of rows x blocks scales share a place.
+bool distinct_scales(int64_t rows, int64_t blocks, const int64_t (&s)[2]) {
+    if (rows > 1 && blocks > 1)
+        return s[0] > 0 && s[1] > 0 && (s[0] > (blocks - 1) * s[1] || s[1] > (rows - 1) * s[0]);
+    return (rows <= 1 || s[0] > 0) && (blocks <= 1 || s[1] > 0);
+}
+
 int check_f8(const ltx3drope_f8_matmul_t& c, int* why) {
     if (!flag(c.b_rows)) return LTX3DROPE_E_INVALID;
     if (c.dtype != LTX3DROPE_DTYPE_F32 && c.dtype != LTX3DROPE_DTYPE_BF16) {
@@ -177,8 +191,12 @@ int check_f8(const ltx3drope_f8_matmul_t& c, int* why) {
         return LTX3DROPE_E_UNSUPPORTED;
     }
     if (c.a_pitch < c.dim || c.b_pitch < c.dim) return LTX3DROPE_E_INVALID;
+    for (const int64_t(*v)[2] : {&c.a_scale_strides, &c.b_scale_strides})
+        if ((*v)[0] < 0 || (*v)[1] < 0) return LTX3DROPE_E_INVALID;
     const int64_t lim = int64_t(1) << 26;
     if (c.dim >= kF8MaxDim || c.a_pitch >= kF8MaxPitch || c.b_pitch >= kF8MaxPitch || c.tokens >= lim || c.out >= lim ||
+        c.a_scale_strides[0] >= kF8MaxScaleRow || c.b_scale_strides[0] >= kF8MaxScaleRow ||
+        c.a_scale_strides[1] >= kF8MaxScaleBlock || c.b_scale_strides[1] >= kF8MaxScaleBlock ||
         too_many_tiles(c.tokens, c.out)) {
         *why = LTX3DROPE_REASON_TOO_LARGE;
         return LTX3DROPE_E_UNSUPPORTED;
@@ -197,6 +215,10 @@ F8Problem f8_problem(const ltx3drope_f8_matmul_t& c) {
     p.workspace = c.workspace;
     p.a_pitch = static_cast<uint64_t>(c.a_pitch);
     p.b_pitch = static_cast<uint64_t>(c.b_pitch);
+    p.a_scale_row = static_cast<uint32_t>(c.a_scale_strides[0]);
+    p.a_scale_block = static_cast<uint64_t>(c.a_scale_strides[1]);
+    p.b_scale_row = static_cast<uint32_t>(c.b_scale_strides[0]);
+    p.b_scale_block = static_cast<uint64_t>(c.b_scale_strides[1]);
     p.tokens = static_cast<uint32_t>(c.tokens);
     p.dim = static_cast<uint32_t>(c.dim);
     p.out = static_cast<uint32_t>(c.out);
@@ -670,16 +692,27 @@ int ltx3drope_f8_quantize(const ltx3drope_f8_quantize_t* call, void* stream, int
     if (c.dim >= lim || c.rows >= lim || (c.q_turned && c.turned_pitch >= 2 * lim))
         return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
     const int64_t tiles_r = (c.rows + 127) / 128, tiles_c = (c.dim + 127) / 128;
+    const int64_t scale_rows = c.blocks ? tiles_r : c.rows, turned_rows = c.blocks ? tiles_c : c.dim;
     if (tiles_r * tiles_c >= int64_t(1) << 24) return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
+    for (const int64_t(*v)[2] : {&c.scale_strides, &c.scale_turned_strides})
+        for (int64_t n : *v) {
+            if (n < 0) return LTX3DROPE_E_INVALID;
+            if (n >= kF8MaxScaleBlock) return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
+        }
+    if (scale_rows * c.scale_strides[0] >= int64_t(1) << 58 || turned_rows * c.scale_turned_strides[0] >= int64_t(1) << 58)
+        return refuse(LTX3DROPE_REASON_TOO_LARGE, reason);
     if (c.rows == 0) return LTX3DROPE_OK;
     if (!c.x || !c.q || !c.scale) return refuse(LTX3DROPE_REASON_NULLPTR, reason);
     const size_t n = static_cast<size_t>(c.rows) * static_cast<size_t>(c.dim), es = elem(c.dtype);
     Spans t;
     t.add(c.x, n * es, es, Role::Param);
     t.add(c.q, n, 1, Role::ParamOut);
-    t.add(c.scale, static_cast<size_t>((c.blocks ? tiles_r : c.rows) * tiles_c) * 4, 4, Role::ParamOut);
+    t.add(c.scale, scale_bytes(scale_rows, tiles_c, c.scale_strides), 4, Role::ParamOut);
     t.add(c.q_turned, static_cast<size_t>(c.dim) * static_cast<size_t>(c.turned_pitch), 1, Role::ParamOut);
-    t.add(c.scale_turned, static_cast<size_t>((c.blocks ? tiles_c : c.dim) * tiles_r) * 4, 4, Role::ParamOut);
+    t.add(c.scale_turned, scale_bytes(turned_rows, tiles_r, c.scale_turned_strides), 4, Role::ParamOut);
+    if (!distinct_scales(scale_rows, tiles_c, c.scale_strides) ||
+        (c.q_turned && !distinct_scales(turned_rows, tiles_r, c.scale_turned_strides)))
+        return refuse(LTX3DROPE_REASON_OVERLAP, reason);
     int device = -1;
     const int why = check_spans(t, &device);
     if (why != LTX3DROPE_REASON_OK) return refuse(why, reason);
@@ -690,6 +723,10 @@ int ltx3drope_f8_quantize(const ltx3drope_f8_quantize_t* call, void* stream, int
     p.scale = c.scale;
     p.scale_turned = c.scale_turned;
     p.turned_pitch = static_cast<uint64_t>(c.turned_pitch);
+    p.scale_row = static_cast<uint64_t>(c.scale_strides[0]);
+    p.scale_block = static_cast<uint64_t>(c.scale_strides[1]);
+    p.turned_row = static_cast<uint64_t>(c.scale_turned_strides[0]);
+    p.turned_block = static_cast<uint64_t>(c.scale_turned_strides[1]);
     p.rows = static_cast<uint32_t>(c.rows);
     p.dim = static_cast<uint32_t>(c.dim);
     p.blocks = c.blocks != 0;
@@ -728,8 +765,8 @@ int ltx3drope_f8_matmul(const ltx3drope_f8_matmul_t* call, void* stream, int* re
     Spans t;
     t.add(c.a, (M - 1) * p.a_pitch + K, 1, Role::Param);
     t.add(c.b, (N - 1) * p.b_pitch + K, 1, Role::Param);
-    t.add(c.a_scale, M * blocks * 4, 4, Role::Param);
-    t.add(c.b_scale, (p.b_rows ? N : (N + 127) / 128) * blocks * 4, 4, Role::Param);
+    t.add(c.a_scale, scale_bytes(M, blocks, c.a_scale_strides), 4, Role::Param);
+    t.add(c.b_scale, scale_bytes(p.b_rows ? N : (N + 127) / 128, blocks, c.b_scale_strides), 4, Role::Param);
     t.add(c.bias, N * 4, 4, Role::Param);
     t.add(c.y, M * N * es, es, Role::ParamOut);
     if (ws != 0) t.add(c.workspace, ws, 16, Role::Scratch);

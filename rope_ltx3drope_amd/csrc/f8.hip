@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include "block.h"
+#include "fastdiv.h"
 #include "product.h"
 
 namespace ltx3drope {
@@ -26,11 +27,18 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > 
 struct Divisor {
     float s, r;
     bool usual;
+    __device__ __forceinline__ Divisor() = default;
     __device__ __forceinline__ explicit Divisor(uint32_t top) {
-        s = __uint_as_float(top) / kTop;
-        // subnormal numbers on the way cost the remainder below its exactness
-        usual = s > 0x1p-80f && s < 0x1p100f;
-        r = 1.0f / s;
+        // Both divisions by a reciprocal and a step with the exact remainder, which rounds like the division: 1/448 is
+        // rounded to nearest, and v_rcp_f32 is within an ulp, from where the step gives the rounded reciprocal of any
+        // number but one of all ones (Markstein).  9 instructions where two general divisions take 30.
+        const float x = __uint_as_float(top), s0 = x * (1.f / kTop);
+        s = fmaf(fmaf(-s0, kTop, x), 1.f / kTop, s0);
+        const float r0 = __builtin_amdgcn_rcpf(s);
+        r = fmaf(fmaf(-s, r0, 1.f), r0, r0);
+        // subnormal numbers on the way cost the remainders below their exactness
+        usual = s > 0x1p-80f && s < 0x1p100f && (~__float_as_uint(s) & 0x7fffffu) != 0;
+        if (!usual) s = x / kTop;
     }
     // x / s rounded to fp32, within e4m3's range.  Usually x * r is within an ulp of the quotient, and one step
     // with the exact remainder gives the rounded quotient (Markstein's division by a rounded reciprocal); its
@@ -110,13 +118,15 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 
 // Rows alone: 16 lanes a block, 8 numbers a lane; a number is read once and its byte written once.
 template <bool F32, bool VEC>
-__global__ __launch_bounds__(256) void f8_rows_of(const char* x, uint8_t* q, float* scale, uint64_t blocks,
-                                                  uint32_t per_row, uint32_t dim) {
+__global__ __launch_bounds__(256) void f8_rows_of(F8Quantize p, uint32_t first_row, uint32_t blocks, FastDiv by_row) {
+    const char* x = static_cast<const char*>(p.x);
+    uint8_t* q = static_cast<uint8_t*>(p.q);
+    const uint32_t dim = p.dim;
     const uint32_t lane = threadIdx.x & 15;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 16 + threadIdx.x / 16; i < blocks;
-         i += static_cast<uint64_t>(gridDim.x) * 16) {
-        const uint64_t r = i / per_row;
-        const uint32_t c = static_cast<uint32_t>(i - r * per_row) * kBlock + lane * 8;
+    const uint32_t i = blockIdx.x * 16 + threadIdx.x / 16;
+    if (i < blocks) {
+        const uint32_t row = fast_div(i, by_row), kb = i - row * by_row.d, c = kb * kBlock + lane * 8;
+        const uint64_t r = first_row + row;
         float f[8];
         load8<F32, VEC>(f, x + r * dim * (F32 ? 4 : 2), c, dim);
         uint32_t top = 0;
@@ -124,92 +134,161 @@ __global__ __launch_bounds__(256) void f8_rows_of(const char* x, uint8_t* q, flo
         for (int k = 0; k < 8; ++k) top = larger(top, magnitude(f[k]));
         const Divisor d(max16(top));
         store8<VEC>(q + r * dim, c, dim, d.four(f[0], f[1], f[2], f[3]), d.four(f[4], f[5], f[6], f[7]));
-        if (lane == 0) scale[i] = d.s;
+        if (lane == 0) p.scale[r * p.scale_row + kb * p.scale_block] = d.s;
     }
 }
 
-// Tiles of 128 x 128: a workgroup of 256 threads holds one in registers, 8 columns and every 16th row a thread.
-// BLOCKS: one scale for the tile; otherwise one a row and, turned, one a column.  TURNED: also x^T, whose
-// bytes cross LDS (a column's 128 are one line of the turned matrix).
+// The bytes of a 4 x 4 square turned: out[j] has byte j of every word.
+__device__ __forceinline__ void turn4(const uint32_t (&in)[4], uint32_t (&out)[4]) {
+    const uint32_t a = __builtin_amdgcn_perm(in[1], in[0], 0x05010400), b = __builtin_amdgcn_perm(in[3], in[2], 0x05010400);
+    const uint32_t c = __builtin_amdgcn_perm(in[1], in[0], 0x07030602), d = __builtin_amdgcn_perm(in[3], in[2], 0x07030602);
+    out[0] = __builtin_amdgcn_perm(b, a, 0x05040100);
+    out[1] = __builtin_amdgcn_perm(b, a, 0x07060302);
+    out[2] = __builtin_amdgcn_perm(d, c, 0x05040100);
+    out[3] = __builtin_amdgcn_perm(d, c, 0x07060302);
+}
+
+// Tiles of 128 x 128: a workgroup of 256 threads holds one in registers, a square of 8 x 8 a thread.
+// BLOCKS: one scale for the tile; otherwise one a row and, turned, one a column, each formed by one thread.  TURNED:
+// also x^T, whose bytes cross LDS (a column's 128 are one line of the turned matrix), 8 rows of a column at once: the
+// squares' rows are neighbours for that (4096 x 8192 bf16, rows and turned: 71 us with every 16th row, a byte at a
+// time and each scale formed by all lanes that use it, 38 us so; the bytes take 20).  bf16 stays packed in registers.
 template <bool F32, bool VEC, bool BLOCKS, bool TURNED>
 __global__ __launch_bounds__(256) void f8_tiles_of(F8Quantize p) {
-    constexpr uint32_t kPitch = kBlock + 16;  // 16-byte pieces of neighbouring columns in different banks
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
     __shared__ uint32_t tops[4][kBlock];
-    __shared__ __align__(16) uint8_t turned[TURNED ? kBlock * kPitch : 16];
+    __shared__ __align__(16) f32x2 scales[2][kBlock];  // of rows and of columns, with their reciprocals
+    __shared__ __align__(16) uint8_t turned[TURNED ? kBlock * kBlock : 16];
     const uint32_t tid = threadIdx.x, lane = tid & 15, line = tid / 16, wave = tid / 64;
-    const uint32_t tiles_c = (p.dim + kBlock - 1) / kBlock, tiles_r = (p.rows + kBlock - 1) / kBlock;
+    const uint32_t tiles_c = (p.dim + kBlock - 1) / kBlock;
     const uint32_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
     const uint32_t r0 = tr * kBlock, c = tc * kBlock + lane * 8;
     const char* x = static_cast<const char*>(p.x);
     uint8_t* q = static_cast<uint8_t*>(p.q);
-    float f[8][8];
-    uint32_t row_top[8], col_top[8] = {};
+    constexpr bool PACKED = VEC && !F32;
+    float f[PACKED ? 1 : 8][8];
+    u32x4 packed[PACKED ? 8 : 1];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t r = r0 + i * 16 + line;
-        if (r < p.rows) {
-            load8<F32, VEC>(f[i], x + static_cast<size_t>(r) * p.dim * (F32 ? 4 : 2), c, p.dim);
+        const uint32_t r = r0 + line * 8 + i;
+        const char* row = x + static_cast<size_t>(r) * p.dim * (F32 ? 4 : 2);
+        if constexpr (PACKED) {
+            packed[i] = u32x4{0, 0, 0, 0};
+            if (r < p.rows && c < p.dim) packed[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + c * 2u));
+        } else if (r < p.rows) {
+            load8<F32, VEC>(f[i], row, c, p.dim);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[i][k] = 0.f;
         }
     }
+    auto number = [&](int i, int k) {
+        if constexpr (PACKED) return __uint_as_float(k & 1 ? packed[i][k / 2] & 0xffff0000u : packed[i][k / 2] << 16);
+        else return f[i][k];
+    };
+    uint32_t row_top[8], col_top[8] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         row_top[i] = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint32_t m = magnitude(f[i][k]);
+            const uint32_t m = magnitude(number(i, k));
             row_top[i] = larger(row_top[i], m);
             col_top[k] = larger(col_top[k], m);
         }
     }
-    if constexpr (BLOCKS || TURNED) {
-        // columns over the four lines of a wavefront, then over the wavefronts
+    // the numbers are unpacked again where they are used: kept as floats they would take twice the registers
+    if constexpr (PACKED)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            col_top[k] = larger(col_top[k], __shfl_xor(col_top[k], 16));
-            col_top[k] = larger(col_top[k], __shfl_xor(col_top[k], 32));
-            if ((tid & 63) < 16) tops[wave][lane * 8 + k] = col_top[k];
+        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(packed[i]));
+    // columns over the four lines of a wavefront; the wavefronts' meet below
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        col_top[k] = larger(col_top[k], __shfl_xor(col_top[k], 16));
+        col_top[k] = larger(col_top[k], __shfl_xor(col_top[k], 32));
+        if ((tid & 63) < 16) tops[wave][lane * 8 + k] = col_top[k];
+    }
+    if constexpr (!BLOCKS) {
+        uint32_t mine = 0;  // lane i keeps row i's
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t top = max16(row_top[i]);
+            mine = lane == i ? top : mine;
         }
-        __syncthreads();
+        if (lane < 8) {
+            const Divisor d(mine);
+            const uint32_t r = r0 + line * 8 + lane;
+            scales[0][line * 8 + lane] = f32x2{d.s, d.usual ? d.r : 0.f};
+            if (r < p.rows) p.scale[r * p.scale_row + tc * p.scale_block] = d.s;
+        }
+    }
+    __syncthreads();
+    Divisor whole;
+    if constexpr (BLOCKS) {
+        uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) col_top[k] = larger(col_top[k], tops[w][lane * 8 + k]);
-    }
-    uint32_t block_top = 0;
-    if constexpr (BLOCKS) {
+            for (int w = 0; w < 4; ++w) top = larger(top, tops[w][lane * 8 + k]);
+        whole = Divisor(max16(top));
+        if (tid == 0) {
+            p.scale[tr * p.scale_row + tc * p.scale_block] = whole.s;
+            if (TURNED) p.scale_turned[tc * p.turned_row + tr * p.turned_block] = whole.s;
+        }
+    } else if (tid < kBlock) {
+        uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) block_top = larger(block_top, col_top[k]);
-        block_top = max16(block_top);
+        for (int w = 0; w < 4; ++w) top = larger(top, tops[w][tid]);
+        const Divisor d(top);
+        scales[1][tid] = f32x2{d.s, d.usual ? d.r : 0.f};
+        if (tc * kBlock + tid < p.dim) p.scale_turned[(tc * kBlock + tid) * p.turned_row + tr * p.turned_block] = d.s;
     }
-    const Divisor whole(block_top);
-    if (BLOCKS && tid == 0) {
-        p.scale[static_cast<size_t>(tr) * tiles_c + tc] = whole.s;
-        if (TURNED) p.scale_turned[static_cast<size_t>(tc) * tiles_r + tr] = whole.s;
-    }
+    auto divisor = [&](int side, uint32_t at) {
+        if constexpr (BLOCKS) return whole;
+        const f32x2 v = scales[side][at];
+        Divisor d;
+        d.s = v[0];
+        d.r = v[1];
+        d.usual = v[1] != 0.f;
+        return d;
+    };
+    uint32_t bytes[8][2];  // of each row
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t r = r0 + i * 16 + line;
-        const Divisor d(BLOCKS ? block_top : max16(row_top[i]));
-        if (r < p.rows) {
-            store8<VEC>(q + static_cast<size_t>(r) * p.dim, c, p.dim, d.four(f[i][0], f[i][1], f[i][2], f[i][3]),
-                        d.four(f[i][4], f[i][5], f[i][6], f[i][7]));
-            if (!BLOCKS && lane == 0) p.scale[static_cast<size_t>(r) * tiles_c + tc] = d.s;
-        }
+        const uint32_t r = r0 + line * 8 + i;
+        const Divisor d = divisor(0, line * 8 + i);
+        bytes[i][0] = d.four(number(i, 0), number(i, 1), number(i, 2), number(i, 3));
+        bytes[i][1] = d.four(number(i, 4), number(i, 5), number(i, 6), number(i, 7));
+        if (r < p.rows) store8<VEC>(q + static_cast<size_t>(r) * p.dim, c, p.dim, bytes[i][0], bytes[i][1]);
     }
     if constexpr (TURNED) {
+        if constexpr (BLOCKS) {
+            // the same bytes, turned
+            uint32_t t[2][2][4];  // [rows][columns]
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const Divisor d(BLOCKS ? block_top : col_top[k]);
-            const uint32_t lo = d.four(f[0][k], f[1][k], f[2][k], f[3][k]);
-            const uint32_t hi = d.four(f[4][k], f[5][k], f[6][k], f[7][k]);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                turned[(lane * 8 + k) * kPitch + i * 16 + line] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i % 4)));
-            if (!BLOCKS && line == 0 && c + k < p.dim) p.scale_turned[static_cast<size_t>(c + k) * tiles_r + tr] = d.s;
+                for (int k = 0; k < 2; ++k)
+                    turn4({bytes[4 * i][k], bytes[4 * i + 1][k], bytes[4 * i + 2][k], bytes[4 * i + 3][k]}, t[i][k]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                bytes[k][0] = t[0][k / 4][k % 4];
+                bytes[k][1] = t[1][k / 4][k % 4];
+            }
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const Divisor d = divisor(1, lane * 8 + k);
+                bytes[k][0] = d.four(number(0, k), number(1, k), number(2, k), number(3, k));
+                bytes[k][1] = d.four(number(4, k), number(5, k), number(6, k), number(7, k));
+            }
         }
+        // a column's pieces of 8 rows change places by its group of 8 columns: other banks for every lane
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<u32x2*>(turned + (lane * 8 + k) * kBlock + (line ^ lane) * 8) = u32x2{bytes[k][0], bytes[k][1]};
         __syncthreads();
         // 8 threads a column, 16 rows each
         uint8_t* out = static_cast<uint8_t*>(p.q_turned);
@@ -217,7 +296,9 @@ __global__ __launch_bounds__(256) void f8_tiles_of(F8Quantize p) {
         for (uint32_t i = 0; i < 4; ++i) {
             const uint32_t col = i * 32 + tid / 8, row = (tid % 8) * 16, cc = tc * kBlock + col;
             if (cc >= p.dim || r0 + row >= p.rows) continue;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(turned + col * kPitch + row);
+            const uint32_t group = col / 8;
+            u32x4 v = *reinterpret_cast<const u32x4*>(turned + col * kBlock + (row / 8 ^ (group & ~1u)) * 8);
+            if (group & 1) v = u32x4{v[2], v[3], v[0], v[1]};
             uint8_t* to = out + cc * p.turned_pitch + r0 + row;
             if (p.turned_chunks) {
                 *reinterpret_cast<u32x4*>(to) = v;  // the pitch has room for whole pieces
@@ -237,9 +318,11 @@ struct OpF8 {
     static constexpr int kElem = 1;
 };
 
-// The scales of one product: a's [M][blocks], b's [N][blocks] or one row for 128 rows of b.
+// The scales of one product: a's [M][blocks], b's [N][blocks] or one row for 128 rows of b; strides in numbers.
 struct F8Scales {
     const float *a, *b;
+    uint32_t a_row, b_row;
+    uint64_t a_block, b_block;
     uint32_t blocks;
 };
 
@@ -253,25 +336,20 @@ struct F8Scales {
 // to 1.7e-3.  A result in fp32 is not made so:
 // Sixteen: e4m3 is exact in bf16, whose instructions have exact products and fp32 sums.
 struct Eight {
-    u32x4 v[2];
-    __device__ __forceinline__ explicit Eight(const u32x4 (&pieces)[2]) : v{pieces[0], pieces[1]} {}
+    typedef int i32x8 __attribute__((ext_vector_type(8)));
+    i32x8 v;
+    __device__ __forceinline__ Eight(u32x4 lo, u32x4 hi)
+        : v(__builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7)) {}
     __device__ __forceinline__ static f32x4 product(const Eight& b, const Eight& a) {
-        typedef int i32x8 __attribute__((ext_vector_type(8)));
-        auto all = [](const Eight& x) {
-            return i32x8{static_cast<int>(x.v[0][0]), static_cast<int>(x.v[0][1]), static_cast<int>(x.v[0][2]),
-                         static_cast<int>(x.v[0][3]), static_cast<int>(x.v[1][0]), static_cast<int>(x.v[1][1]),
-                         static_cast<int>(x.v[1][2]), static_cast<int>(x.v[1][3])};
-        };
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(all(b), all(a), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0,
-                                                                0, 0);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
     }
 };
 struct Sixteen {
     u32x4 v[4];
-    __device__ __forceinline__ explicit Sixteen(const u32x4 (&pieces)[2]) {
+    __device__ __forceinline__ Sixteen(u32x4 lo, u32x4 hi) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t w = pieces[i / 4][i % 4];
+            const uint32_t w = i < 4 ? lo[i % 4] : hi[i % 4];
             v[i / 2][i % 2 * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false));
             v[i / 2][i % 2 * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true));
         }
@@ -285,15 +363,14 @@ struct Sixteen {
 };
 
 // Four bytes a lane from the buffer to LDS, lane l's to lds + 4 * l; as lds_copy16.
-__device__ __forceinline__ void lds_copy4(u32x4 buffer, char* lds, uint32_t voffset, uint32_t soffset) {
+__device__ __forceinline__ void lds_copy4(u32x4 buffer, char* lds, uint32_t voffset) {
     const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(at), "v"(voffset),
-                 "s"(buffer), "s"(soffset));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at), "v"(voffset), "s"(buffer));
 }
 
 // BM x BN tiles, WM x WN wavefronts; a step is one block of k, whose operands and scales come to LDS together.
 // B_ROWS: b has a scale a row.  DIRECT: operands whose rows start on 16 bytes are copied without passing
-// through registers.
+// through registers.  RING: steps in LDS.
 template <class Units, int BM, int BN, int WM, int WN, int RING, bool B_ROWS, bool DIRECT, class Done>
 __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scales, Done done) {
     constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
@@ -302,7 +379,7 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;       // 1 KB copies a wavefront makes of each operand
     constexpr uint32_t RA = BM / NW, RB = BN / NW;          // rows whose scales a wavefront copies
     constexpr int kAtB = BM * kRowBytes, kAtScales = kAtB + BN * kRowBytes;
-    constexpr int kSlot = kAtScales + (B_ROWS ? 2 : 1) * NW * 256;
+    constexpr int kSlot = kAtScales + 2 * NW * 256;
     static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN && RA <= 64 && RB <= 64, "copies split evenly");
     static_assert(FN * 16 <= 128, "a wavefront's rows of b lie in one block of 128");
     __shared__ __align__(1024) char lds[RING * kSlot];
@@ -325,28 +402,21 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
     for (int i = 0; i < CB; ++i) SB::place((i * NW + wave) * 64 + lane, line_b[i], byte_b[i]);
     // scales of rows past the end are those of the last row (their sums are dropped)
     const uint32_t scale_m = m0 + wave * RA + lane % RA, scale_n = n0 + wave * RB + lane % RB;
-    const float* sa = scales.a + static_cast<size_t>(scale_m < p.M ? scale_m : p.M - 1) * scales.blocks;
-    const float* sb = scales.b + static_cast<size_t>(scale_n < p.N ? scale_n : p.N - 1) * (B_ROWS ? scales.blocks : 0);
+    const float* sa = scales.a + static_cast<size_t>(scale_m < p.M ? scale_m : p.M - 1) * scales.a_row;
+    constexpr uint32_t kShare = B_ROWS ? 1 : 128;  // rows of b with one scale
+    const float* sb = scales.b + static_cast<size_t>((scale_n < p.N ? scale_n : p.N - 1) / kShare) * scales.b_row;
 
-    u32x4 ra, rb, rsa, rsb;
+    u32x4 ra, rb;
     uint32_t va[CA], vb[CB], vsa = 0, vsb = 0;
     if constexpr (DIRECT) {
         // whole dwords: the up to three bytes past a row's end are cleared with the rest of its piece
         auto rsrc = [&](const char* base, uint64_t pitch, uint32_t row0, uint32_t rows, uint32_t R) {
             return buffer_of(base + row0 * pitch, pitch, rows - row0 < R ? rows - row0 : R, (p.k + 3) & ~3u);
         };
-        auto scale_rsrc = [&](const float* base, uint32_t row0, uint32_t rows, uint32_t R) {
-            return buffer_of(reinterpret_cast<const char*>(base + static_cast<size_t>(row0) * scales.blocks),
-                             scales.blocks * 4u, rows - row0 < R ? rows - row0 : R, scales.blocks * 4);
-        };
         ra = rsrc(p.a, p.a_pitch, m0, p.M, BM);
         rb = rsrc(p.b[0], p.b_pitch, n0, p.N, BN);
-        rsa = scale_rsrc(scales.a, m0, p.M, BM);
-        vsa = (wave * RA + lane % RA) * scales.blocks * 4;
-        if constexpr (B_ROWS) {
-            rsb = scale_rsrc(scales.b, n0, p.N, BN);
-            vsb = (wave * RB + lane % RB) * scales.blocks * 4;
-        }
+        vsa = scale_m < p.M ? (scale_m - m0) * scales.a_row * 4 : kOutOfRange;
+        vsb = scale_n < p.N ? (scale_n / kShare - n0 / kShare) * scales.b_row * 4 : kOutOfRange;
 #pragma unroll
         for (int i = 0; i < CA; ++i)
             va[i] = m0 + line_a[i] < p.M ? static_cast<uint32_t>(line_a[i] * p.a_pitch) + byte_a[i] : kOutOfRange;
@@ -356,18 +426,28 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
     }
     // a step past this workgroup's last one brings zeros without touching memory
     const uint32_t k_end = last * kRowBytes < p.k ? last * kRowBytes : p.k;
-    constexpr int kCopies = CA + CB + 1 + B_ROWS;
-    auto copy = [&](uint32_t step, uint32_t slot) {
+    constexpr int kCopies = CA + CB + 2;
+    // one step's scales lie a_row (b_row) apart from this tile's first row on
+    auto scale_rsrc = [&](const float* base, uint64_t row0, uint32_t row, uint64_t block, uint32_t step, uint32_t R) {
+        return buffer_of(reinterpret_cast<const char*>(base + row0 * row + step * block), row * 4u, R, 4);
+    };
+    auto copy_one = [&](uint32_t step, uint32_t slot, int c) {
         char* to = lds + slot * kSlot + wave * 1024;
-        const uint32_t k = step * kRowBytes;
-#pragma unroll
-        for (int i = 0; i < CA; ++i) lds_copy16(ra, to + i * NW * 1024, k + byte_a[i] >= k_end ? kOutOfRange : va[i], k);
-#pragma unroll
-        for (int i = 0; i < CB; ++i)
-            lds_copy16(rb, to + kAtB + i * NW * 1024, k + byte_b[i] >= k_end ? kOutOfRange : vb[i], k);
         char* s = lds + slot * kSlot + kAtScales + wave * 256;
-        lds_copy4(rsa, s, step < last ? vsa : kOutOfRange, step * 4);
-        if constexpr (B_ROWS) lds_copy4(rsb, s + NW * 256, step < last ? vsb : kOutOfRange, step * 4);
+        const uint32_t k = step * kRowBytes;
+        if (c < CA) lds_copy16(ra, to + c * NW * 1024, k + byte_a[c % CA] >= k_end ? kOutOfRange : va[c % CA], k);
+        else if (c < CA + CB)
+            lds_copy16(rb, to + kAtB + (c - CA) * NW * 1024,
+                       k + byte_b[(c - CA) % CB] >= k_end ? kOutOfRange : vb[(c - CA) % CB], k);
+        else if (c == CA + CB)
+            lds_copy4(scale_rsrc(scales.a, m0, scales.a_row, scales.a_block, step, BM), s, step < last ? vsa : kOutOfRange);
+        else
+            lds_copy4(scale_rsrc(scales.b, n0 / kShare, scales.b_row, scales.b_block, step, (BN + kShare - 1) / kShare),
+                      s + NW * 256, step < last ? vsb : kOutOfRange);
+    };
+    auto copy = [&](uint32_t step, uint32_t slot) {
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) copy_one(step, slot, c);
     };
     struct Held {
         u32x4 v[DIRECT ? 1 : CA + CB];
@@ -385,8 +465,8 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
                 const uint32_t n = n0 + line_b[i] < p.N ? n0 + line_b[i] : p.N - 1;
                 to.v[CA + i] = load_chunk<OpF8, false, false>(p.b[0] + n * p.b_pitch, step * kRowBytes + byte_b[i], p.k);
             }
-            to.sa = sa[step];
-            if constexpr (B_ROWS) to.sb = sb[step];
+            to.sa = sa[step * scales.a_block];
+            to.sb = sb[step * scales.b_block];
         }
     };
     auto put_held = [&](const Held& from, uint32_t slot) {
@@ -398,7 +478,7 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
             for (int i = 0; i < CB; ++i) *reinterpret_cast<u32x4*>(at + kAtB + i * NW * 1024) = from.v[CA + i];
             float* s = reinterpret_cast<float*>(lds + slot * kSlot + kAtScales + wave * 256) + lane;
             s[0] = from.sa;
-            if constexpr (B_ROWS) s[NW * 64] = from.sb;
+            s[NW * 64] = from.sb;
         }
     };
     // Copies bring whole 16-byte pieces: what a row's last piece holds past k is cleared, a row a thread.
@@ -419,52 +499,44 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
     };
 
     f32x4 acc[FM][FN] = {};
-    // the scale of b's block of 128 rows: lane l holds that of step `from` + l
-    const uint32_t strip = (n0 + wn * FN * 16) / 128;
-    const float* sb_strip = scales.b + static_cast<size_t>(strip) * scales.blocks;
-    float sb_lanes = 0.f;
-    const uint32_t rows_b = (p.N + 127) / 128;
-    auto multiply = [&](uint32_t step, uint32_t slot) {
-        float sbw = 1.f;
-        if constexpr (!B_ROWS) {
-            const uint32_t i = (step - first) & 63;
-            if (i == 0) sb_lanes = strip < rows_b && step + lane < last ? sb_strip[step + lane] : 0.f;
-            sbw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sb_lanes), static_cast<int>(i)));
-        }
-        const char* at = lds + slot * kSlot;
-        const float* s = reinterpret_cast<const float*>(at + kAtScales);
-        auto read = [&](const char* block) {
-            u32x4 v[2];
+    auto read = [&](const char* block) {
+        return Units(*reinterpret_cast<const u32x4*>(block + SB::lane_base(lane, 0)),
+                     *reinterpret_cast<const u32x4*>(block + SB::lane_base(lane, 1)));
+    };
+    auto read_a = [&](uint32_t slot, int i) { return read(lds + slot * kSlot + (wm * FM + i) * 16 * kRowBytes); };
+    auto read_b = [&](uint32_t slot, int j) { return read(lds + slot * kSlot + kAtB + (wn * FN + j) * 16 * kRowBytes); };
+    auto scales_of = [&](uint32_t slot) { return reinterpret_cast<const float*>(lds + slot * kSlot + kAtScales); };
+    auto scale_a = [&](uint32_t slot, int i) {
+        const uint32_t r = (wm * FM + i) * 16 + (lane & 15);
+        return scales_of(slot)[r / RA * 64 + r % RA];
+    };
+    auto scale_b = [&](uint32_t slot, int j) {
+        const uint32_t r = (wn * FN + j) * 16 + (lane >> 4) * 4;
+        return *reinterpret_cast<const f32x4*>(scales_of(slot) + NW * 64 + r / RB * 64 + r % RB);
+    };
+    // the scale of all rows of b that the wavefront holds (they lie in one block of 128)
+    auto strip_scale = [&](uint32_t slot) {
+        const uint32_t r = wn * FN * 16;
+        return B_ROWS ? 1.f : scales_of(slot)[NW * 64 + r / RB * 64 + r % RB];
+    };
+    static_assert(FN == 4 || FN == 2, "a wavefront holds 32 or 64 rows of b");
+    f32x4 sbn[B_ROWS ? FN : 1];
+    auto add = [&](f32x4& to, f32x4 part, float sm, int j) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) v[kk] = *reinterpret_cast<const u32x4*>(block + SB::lane_base(lane, kk));
-            return Units(v);
-        };
-        f32x4 sbn[B_ROWS ? FN : 1];
-        auto b_block = [&](int j) { return read(at + kAtB + (wn * FN + j) * 16 * kRowBytes); };
-        const Units fb[4] = {b_block(0), b_block(1 % FN), b_block(2 % FN), b_block(3 % FN)};
-        static_assert(FN <= 4, "a wavefront holds up to 64 rows of b");
+        for (int e = 0; e < 4; ++e) to[e] = fmaf(part[e], B_ROWS ? sm * sbn[B_ROWS ? j : 0][e] : sm, to[e]);
+    };
+    auto multiply = [&](uint32_t slot) {
+        const float sbw = strip_scale(slot);
+        const Units fb[4] = {read_b(slot, 0), read_b(slot, 1), read_b(slot, 2 % FN), read_b(slot, 3 % FN)};
+        if constexpr (B_ROWS)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            if constexpr (B_ROWS) {
-                const uint32_t r = (wn * FN + j) * 16 + (lane >> 4) * 4;
-                sbn[j] = *reinterpret_cast<const f32x4*>(s + NW * 64 + r / RB * 64 + r % RB);
-            }
-        }
+            for (int j = 0; j < FN; ++j) sbn[j] = scale_b(slot, j);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            const uint32_t row = (wm * FM + i) * 16;
-            const Units fa = read(at + row * kRowBytes);
-            const uint32_t r = row + (lane & 15);
-            const float sm = s[r / RA * 64 + r % RA] * sbw;
+            const Units fa = read_a(slot, i);
+            const float sm = scale_a(slot, i) * sbw;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const f32x4 part = Units::product(fb[j], fa);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float f = B_ROWS ? sm * sbn[B_ROWS ? j : 0][e] : sm;
-                    acc[i][j][e] = fmaf(part[e], f, acc[i][j][e]);
-                }
-            }
+            for (int j = 0; j < FN; ++j) add(acc[i][j], Units::product(fb[j], fa), sm, j);
         }
     };
     const bool tail = DIRECT && p.k % 16 != 0 && last == all_steps;
@@ -477,7 +549,7 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
             copy(s + RING - 1, free);
             free = slot;
             if (tail && s + 1 == last) clear_tail(slot);
-            multiply(s, slot);
+            multiply(slot);
             slot = slot + 1 == RING ? 0 : slot + 1;
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives its workgroup
@@ -487,7 +559,7 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
             const uint32_t slot = (s - first) & 1;
             wait_for_lds_and_meet();
             if (s + 2 < last) hold(after, s + 2);
-            multiply(s, slot);
+            multiply(slot);
             if (s + 1 < last) put_held(next, slot ^ 1);
         };
         hold(even, first);
@@ -520,6 +592,240 @@ __global__ __launch_bounds__(WM* WN * 64) void f8_tiles(Product p, F8Scales scal
     }
 }
 
+// Wide tiles in one stream of steps: a workgroup a compute unit goes from tile to tile (from part to part, where sums
+// are split), and the copies run two steps ahead, into the next tile's first steps, so that neither its start
+// nor the last one's stores leave the matrix cores idle.  Rows quantised and
+// multiplied, 8192 x 4096 -> 10240: 442 us with a workgroup a tile (of which a tile's start and end took 28 us beside
+// 46 for its steps), 340 us so.
+//
+// A step goes row by row of A's blocks: the next row's operands are read and the last row's sums are scaled and added
+// while a row is multiplied.  Before the last two rows every wavefront has read what it needs of the step, and the
+// next one has landed: they meet there, the copies for the step after the next set out, and the two rows go column by
+// column, so that each block of B is followed into its registers by the next step's while the others are still at
+// work.  Rows of k are whole 16-byte pieces.
+template <int BM, int BN, int WM, int WN, int RING, bool B_ROWS, class Done>
+__global__ __launch_bounds__(WM* WN * 64) void f8_walk(Product p, F8Scales scales, Done done) {
+    constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+    using SA = Side<OpF8, BM, false>;
+    using SB = Side<OpF8, BN, false>;
+    constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW, kCopies = CA + CB + 2;
+    constexpr uint32_t RA = BM / NW, RB = BN / NW;  // rows whose scales a wavefront copies
+    constexpr uint32_t kShare = B_ROWS ? 1 : 128;   // rows of b with one scale
+    constexpr int kAtB = BM * kRowBytes, kAtScales = kAtB + BN * kRowBytes, kSlot = kAtScales + 2 * NW * 256;
+    static_assert(CA * 8 * NW == BM && CB * 8 * NW == BN && RA <= 64 && RB <= 64, "copies split evenly");
+    static_assert(FN == 4 && FM % 2 == 0 && FM >= 4 && BN % 128 == 0);
+    __shared__ __align__(1024) char lds[RING * kSlot];
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t wm = wave / WN, wn = wave % WN;
+    const uint32_t tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
+    const uint32_t jobs = tiles * p.splits;
+
+    struct Job {
+        uint32_t m0, n0, first, last;
+    };
+    auto job_of = [&](uint32_t job) {
+        const uint32_t tile = job % tiles, split = job / tiles;
+        uint32_t tm, tn;
+        tile_of(tile, tiles_m, tiles_n, tm, tn);
+        return Job{tm * BM, tn * BN, split * scales.blocks / p.splits, (split + 1) * scales.blocks / p.splits};
+    };
+
+    // ---- copies, two steps ahead.  Rows past an operand's end lie past its buffer's.
+    uint32_t line_a, byte_a, line_b, byte_b;  // of copy 0; copy i's lie i * NW * 8 rows on, at the same byte
+    SA::place(wave * 64 + lane, line_a, byte_a);
+    SB::place(wave * 64 + lane, line_b, byte_b);
+    static_assert(NW * 8 % 16 == 0, "the swizzle repeats every 16 rows");
+    uint32_t va[CA], vb[CB];
+#pragma unroll
+    for (int i = 0; i < CA; ++i) va[i] = static_cast<uint32_t>((line_a + i * NW * 8) * p.a_pitch) + byte_a;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) vb[i] = static_cast<uint32_t>((line_b + i * NW * 8) * p.b_pitch) + byte_b;
+    const uint32_t vsa = (wave * RA + lane % RA) * scales.a_row * 4;
+    const uint32_t vsb = (wave * RB + lane % RB) / kShare * scales.b_row * 4;
+    u32x4 ra, rb;
+    const float *sa, *sb;
+    uint32_t rows_sa, rows_sb;
+    uint32_t ahead_job = blockIdx.x;
+    Job ahead = job_of(ahead_job);
+    auto aim = [&]() {  // at job `ahead`, or at nothing
+        const bool any = ahead_job < jobs;
+        const uint32_t m = any ? (p.M - ahead.m0 < BM ? p.M - ahead.m0 : BM) : 0u;
+        const uint32_t n = any ? (p.N - ahead.n0 < BN ? p.N - ahead.n0 : BN) : 0u;
+        ra = buffer_of(p.a + ahead.m0 * p.a_pitch, p.a_pitch, m, p.k);
+        rb = buffer_of(p.b[0] + ahead.n0 * p.b_pitch, p.b_pitch, n, p.k);
+        sa = scales.a + static_cast<uint64_t>(ahead.m0) * scales.a_row;
+        sb = scales.b + static_cast<uint64_t>(ahead.n0 / kShare) * scales.b_row;
+        rows_sa = m;
+        rows_sb = (n + kShare - 1) / kShare;
+    };
+    uint32_t ahead_step = ahead.first;
+    aim();
+    auto advance = [&]() {
+        if (++ahead_step < ahead.last || ahead_job >= jobs) return;
+        ahead_job += gridDim.x;
+        if (ahead_job < jobs) ahead = job_of(ahead_job);
+        ahead_step = ahead.first;
+        aim();
+    };
+    auto copy_one = [&](uint32_t slot, int c) {
+        char* to = lds + slot * kSlot + wave * 1024;
+        char* s = lds + slot * kSlot + kAtScales + wave * 256;
+        const uint32_t k = ahead_step * kRowBytes;
+        if (c < CA) lds_copy16(ra, to + c * NW * 1024, k + byte_a >= p.k ? kOutOfRange : va[c % CA], k);
+        else if (c < CA + CB)
+            lds_copy16(rb, to + kAtB + (c - CA) * NW * 1024, k + byte_b >= p.k ? kOutOfRange : vb[(c - CA) % CB], k);
+        else if (c == CA + CB)
+            lds_copy4(buffer_of(reinterpret_cast<const char*>(sa + ahead_step * scales.a_block), scales.a_row * 4u, rows_sa, 4),
+                      s, vsa);
+        else
+            lds_copy4(buffer_of(reinterpret_cast<const char*>(sb + ahead_step * scales.b_block), scales.b_row * 4u, rows_sb, 4),
+                      s + NW * 256, vsb);
+    };
+    // A step's copies: kEarly as soon as its slot is free, the others two a row from the next step's first row on.
+    // The way to LDS takes 16 cycles a copy; all at once they hold up the wavefronts' products behind them (8192^3:
+    // 498 us, 478 us so).
+    constexpr int kEarly = 4, kLateRows = (kCopies - kEarly + 1) / 2;
+    static_assert(kLateRows <= FM - 2);
+    auto copies = [&](uint32_t slot, int from, int to) {
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+            if (c >= from && c < to) copy_one(slot, c);
+    };
+
+    // ---- from LDS to the matrix cores
+    auto read = [&](const char* block) {
+        return Eight(*reinterpret_cast<const u32x4*>(block + SB::lane_base(lane, 0)),
+                     *reinterpret_cast<const u32x4*>(block + SB::lane_base(lane, 1)));
+    };
+    auto read_a = [&](uint32_t slot, int i) { return read(lds + slot * kSlot + (wm * FM + i) * 16 * kRowBytes); };
+    auto read_b = [&](uint32_t slot, int j) { return read(lds + slot * kSlot + kAtB + (wn * FN + j) * 16 * kRowBytes); };
+    auto scales_of = [&](uint32_t slot) { return reinterpret_cast<const float*>(lds + slot * kSlot + kAtScales); };
+    auto scale_a = [&](uint32_t slot, int i) {
+        const uint32_t r = (wm * FM + i) * 16 + (lane & 15);
+        return scales_of(slot)[r / RA * 64 + r % RA];
+    };
+    auto scale_b = [&](uint32_t slot, int j) {
+        const uint32_t r = (wn * FN + j) * 16 + (lane >> 4) * 4;
+        return *reinterpret_cast<const f32x4*>(scales_of(slot) + NW * 64 + r / RB * 64 + r % RB);
+    };
+    auto strip_scale = [&](uint32_t slot) {
+        const uint32_t r = wn * FN * 16;
+        return B_ROWS ? 1.f : scales_of(slot)[NW * 64 + r / RB * 64 + r % RB];
+    };
+    f32x4 acc[FM][FN] = {};
+    f32x4 sbn[B_ROWS ? FN : 1];
+    auto add = [&](f32x4& to, f32x4 part, float sm, int j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = fmaf(part[e], B_ROWS ? sm * sbn[B_ROWS ? j : 0][e] : sm, to[e]);
+    };
+
+    uint32_t at_job = blockIdx.x;
+    Job at = ahead;
+    for (int i = 0; i < RING - 1; ++i) {
+        copies(i, 0, kCopies);
+        advance();
+    }
+    copies(RING - 1, 0, kEarly);
+    wait_and_meet<(RING - 2) * kCopies + kEarly>();
+    Eight fb[FN] = {read_b(0, 0), read_b(0, 1), read_b(0, 2), read_b(0, 3)};
+    Eight fa0 = read_a(0, 0), fa1 = fa0, fx = fa0;
+    float raw0 = scale_a(0, 0), sbw = strip_scale(0);
+    uint32_t slot = 0;
+    while (true) {
+        for (uint32_t s = at.first; s < at.last; ++s) {
+            const uint32_t after = RING == 2 ? slot ^ 1 : slot + 1 == RING ? 0 : slot + 1;
+            const uint32_t before = slot == 0 ? RING - 1 : slot - 1;
+            f32x4 part[2][FN];
+            float sm[2] = {0.f, 0.f}, raw1 = 0.f, rawx = 0.f;
+            if constexpr (B_ROWS)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) sbn[j] = scale_b(slot, j);
+            // rows 0 to FM - 3: even ones in fa0, odd ones in fa1
+#pragma unroll
+            for (int i = 0; i < FM - 2; ++i) {
+                Eight& now = i & 1 ? fa1 : fa0;
+                Eight& next = i & 1 ? fa0 : fa1;
+                const float raw = i & 1 ? raw1 : raw0;
+                next = read_a(slot, i + 1);
+                (i & 1 ? raw0 : raw1) = scale_a(slot, i + 1);
+                if (i == FM - 3) {
+                    fx = read_a(slot, FM - 1);
+                    rawx = scale_a(slot, FM - 1);
+                }
+                sm[i & 1] = raw * sbw;
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    part[i & 1][j] = Eight::product(fb[j], now);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (i < kLateRows && j % 2 == 0) copies(before, kEarly + 2 * i + j / 2, kEarly + 2 * i + j / 2 + 1);
+                    if (i > 0) add(acc[(i + FM - 1) % FM][j], part[(i + 1) & 1][j], sm[(i + 1) & 1], j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (i == kLateRows - 1) {
+                    // the sums stay on this side of the branch: the compiler would move them all behind it
+#pragma unroll
+                    for (int a = 0; a < FM; ++a)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[a][j]));
+                    advance();
+                }
+            }
+            // the last two, row FM - 2 in fa0 and FM - 1 in fx
+            const float sm0 = raw0 * sbw, smx = rawx * sbw;
+            wait_and_meet<(RING - 2) * kCopies>();
+            fa1 = read_a(after, 0);
+            raw0 = scale_a(after, 0);
+            sbw = strip_scale(after);
+            f32x4 p0[FN], px[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                p0[j] = Eight::product(fb[j], fa0);
+                px[j] = Eight::product(fb[j], fx);
+                __builtin_amdgcn_sched_barrier(0);
+                fb[j] = read_b(after, j);
+                copies(slot, j * kEarly / FN, (j + 1) * kEarly / FN);
+                add(acc[FM - 3][j], part[(FM - 3) & 1][j], sm[(FM - 3) & 1], j);
+                if (j > 0) {
+                    add(acc[FM - 2][j - 1], p0[j - 1], sm0, j - 1);
+                    add(acc[FM - 1][j - 1], px[j - 1], smx, j - 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            add(acc[FM - 2][FN - 1], p0[FN - 1], sm0, FN - 1);
+            add(acc[FM - 1][FN - 1], px[FN - 1], smx, FN - 1);
+            fa0 = fa1;
+            slot = after;
+        }
+        if (p.splits > 1) {
+            f32x4* out = reinterpret_cast<f32x4*>(p.partial) + static_cast<size_t>(at_job) * (FM * FN * NW * 64) + tid;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) out[(i * FN + j) * NW * 64] = acc[i][j];
+        } else {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const uint32_t m = at.m0 + (wm * FM + i) * 16 + (lane & 15);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const uint32_t n = at.n0 + (wn * FN + j) * 16 + (lane >> 4) * 4;
+                    if (m < p.M && n < p.N) done(m, n, p.N, acc[i][j]);
+                }
+            }
+        }
+        at_job += gridDim.x;
+        if (at_job >= jobs) break;
+        at = job_of(at_job);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives its workgroup
+}
+
 // Up to 16 rows of A: B is read once, straight into registers, 16 of its rows a workgroup, and the wavefronts
 // of a workgroup take blocks of k in turn.  Their sums meet in LDS.  Bound by the bytes of B, beside which the
 // bf16 units cost nothing.
@@ -532,13 +838,13 @@ __global__ __launch_bounds__(512) void f8_few(Product p, F8Scales scales, Done d
     const uint32_t n = n0 + r < p.N ? n0 + r : p.N - 1;  // rows past the end repeat the last one
     const uint32_t m = r < p.M ? r : p.M - 1;
     const char *rb = p.b[0] + n * p.b_pitch, *ra = p.a + m * p.a_pitch;
-    const float* sa = scales.a + static_cast<size_t>(m) * scales.blocks;
+    const float* sa = scales.a + static_cast<size_t>(m) * scales.a_row;
     const uint32_t nn = n0 + (lane >> 4) * 4;
     const float* sb[B_ROWS ? 4 : 1];
 #pragma unroll
     for (uint32_t e = 0; e < (B_ROWS ? 4 : 1); ++e) {
         const uint32_t c = nn + e < p.N ? nn + e : p.N - 1;
-        sb[e] = scales.b + static_cast<size_t>(B_ROWS ? c : n0 / 128) * scales.blocks;
+        sb[e] = scales.b + static_cast<size_t>(B_ROWS ? c : n0 / 128) * scales.b_row;
     }
     f32x4 acc = {};
     for (uint32_t kb0 = wave; kb0 < scales.blocks; kb0 += NW * U) {
@@ -554,12 +860,13 @@ __global__ __launch_bounds__(512) void f8_few(Product p, F8Scales scales, Done d
             }
             const uint32_t at = kb < scales.blocks ? kb : scales.blocks - 1;
 #pragma unroll
-            for (uint32_t e = 0; e < (B_ROWS ? 4 : 1); ++e) s[u][e] = kb < scales.blocks ? sa[at] * sb[e][at] : 0.f;
+            for (uint32_t e = 0; e < (B_ROWS ? 4 : 1); ++e)
+                s[u][e] = kb < scales.blocks ? sa[at * scales.a_block] * sb[e][at * scales.b_block] : 0.f;
         }
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
             if (kb0 + u * NW >= scales.blocks) break;
-            const f32x4 part = Sixteen::product(Sixteen(b[u]), Sixteen(a[u]));
+            const f32x4 part = Sixteen::product(Sixteen(b[u][0], b[u][1]), Sixteen(a[u][0], a[u][1]));
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] = fmaf(part[e], s[u][B_ROWS ? e : 0], acc[e]);
         }
@@ -600,6 +907,17 @@ hipError_t launch_f8_tiles(const Product& p, const F8Scales& s, const Plan& plan
     return hipGetLastError();
 }
 
+template <int BM, int BN, int WM, int WN, int RING, bool B_ROWS>
+hipError_t launch_f8_walk(const Product& p, const F8Scales& s, const Plan& plan, const BiasDone& done, hipStream_t stream) {
+    constexpr int threads = WM * WN * 64;
+    const uint32_t jobs = plan.tiles * p.splits;
+    f8_walk<BM, BN, WM, WN, RING, B_ROWS><<<jobs < 256 ? jobs : 256, threads, 0, stream>>>(p, s, done);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    product_join<OpF8, BM, BN, WM, WN, false><<<plan.tiles * (BM / WM / 16), threads, 0, stream>>>(p, done);
+    return hipGetLastError();
+}
+
 template <bool B_ROWS>
 hipError_t launch_f8_few(const F8Problem& f, const Product& p, const F8Scales& s, const BiasDone& done, hipStream_t stream) {
     const uint32_t groups = (p.N + 15) / 16;
@@ -613,6 +931,11 @@ hipError_t launch_f8_of(const F8Problem& f, Product p, const F8Scales& s, const 
     const Plan plan = plan_product<OpF8, false, false>(p.M, p.N, p.k, direct(f), p.b_pitch);
     p.splits = plan.splits;
     p.partial = static_cast<float*>(f.workspace);
+    if constexpr (std::is_same<Units, Eight>::value) {
+        if (plan.bn >= 128 && p.k % 16 == 0)
+            return plan.bn == 256 ? launch_f8_walk<256, 256, 2, 4, 2, B_ROWS>(p, s, plan, done, stream)
+                                  : launch_f8_walk<256, 128, 4, 2, 3, B_ROWS>(p, s, plan, done, stream);
+    }
     if (plan.bn == 256) return launch_f8_tiles<Units, 256, 256, 2, 4, 2, B_ROWS, true>(p, s, plan, done, stream);
     if (plan.bn == 128) return launch_f8_tiles<Units, 256, 128, 4, 2, 2, B_ROWS, true>(p, s, plan, done, stream);
     if (plan.bm == 128)
@@ -638,7 +961,8 @@ hipError_t launch_f8(const F8Problem& f, bool f32, hipStream_t stream) {
     p.M = f.tokens;
     p.N = f.out;
     p.k = f.dim;
-    const F8Scales s{f.a_scale, f.b_scale, (f.dim + kBlock - 1) / kBlock};
+    const F8Scales s{f.a_scale, f.b_scale, f.a_scale_row, f.b_scale_row, f.a_scale_block, f.b_scale_block,
+                     (f.dim + kBlock - 1) / kBlock};
     const BiasDone done{f32, f.y, f.bias};
     if (f.tokens <= kFewRows)
         return f.b_rows ? launch_f8_few<true>(f, p, s, done, stream) : launch_f8_few<false>(f, p, s, done, stream);
@@ -660,9 +984,12 @@ hipError_t quantize(const F8Quantize& p, hipStream_t stream) {
         f8_tiles_of<F32, VEC, false, true><<<tiles, 256, 0, stream>>>(p);
     } else {
         const uint32_t per_row = (p.dim + kBlock - 1) / kBlock;
-        const uint64_t blocks = static_cast<uint64_t>(p.rows) * per_row, need = (blocks + 15) / 16;
-        f8_rows_of<F32, VEC><<<static_cast<uint32_t>(need < 8192 ? need : 8192), 256, 0, stream>>>(
-            static_cast<const char*>(p.x), static_cast<uint8_t*>(p.q), p.scale, blocks, per_row, p.dim);
+        const uint32_t most = (uint32_t(1) << 27) / per_row;  // rows a launch, which has fewer than 2^32 threads
+        for (uint64_t r = 0; r < p.rows; r += most) {
+            const uint32_t rows = p.rows - r < most ? static_cast<uint32_t>(p.rows - r) : most, blocks = rows * per_row;
+            f8_rows_of<F32, VEC><<<(blocks + 15) / 16, 256, 0, stream>>>(p, static_cast<uint32_t>(r), blocks,
+                                                                        make_fastdiv(per_row));
+        }
     }
     return hipGetLastError();
 }

@@ -126,6 +126,24 @@ def test_quantize_every_tie():
     check_quantize(x * 2.0 ** 110)
 
 
+def test_scales_and_quotients_round_like_divisions():
+    """Largest magnitudes over all exponents and significands, those whose scale is all ones or a power of two
+    among them, and other numbers at random ratios to them: as columns and as rows."""
+    g = torch.Generator().manual_seed(9)
+    n = 1 << 13
+    top = torch.randint(0x00800000, 0x7f000000, (n,), generator=g, dtype=torch.int32)
+    top[: n // 2] = torch.randint(0x30000000, 0x50000000, (n // 2,), generator=g, dtype=torch.int32)
+    top = top.view(torch.float32)
+    # scales of all ones, and one step beside
+    ones = (torch.arange(40, 240, dtype=torch.int32) * 0x800000 + 0x7fffff).view(torch.float32) * 448.0
+    near = torch.cat([torch.nextafter(ones, torch.zeros(())), ones, torch.nextafter(ones, torch.full((), 3e38))])
+    top[100:100 + near.numel()] = near.clamp(max=3e38)
+    x = top[:, None] * torch.rand(n, 128, generator=g) ** 2
+    x[torch.arange(n), torch.randint(0, 128, (n,), generator=g)] = top
+    check_quantize(x)
+    check_quantize(x.t().contiguous())
+
+
 def test_unaligned_and_offset_inputs():
     for dtype in TYPES:
         x = randn(torch.Generator().manual_seed(1), 150, 256, dtype=dtype)
@@ -300,6 +318,28 @@ def test_leading_dimensions_out_and_empty():
     q2, s2 = rla.f8_quantize(x.view(6, 300))
     assert q.shape == x.shape and s.shape == (2, 3, 3) and torch.equal(s.view(6, 3), s2)
     assert torch.equal(q.view(torch.uint8).view(6, 300), q2.view(torch.uint8))
+
+
+def test_scales_of_any_strides():
+    """Scales row by row, block by block, inside wider tensors and spread out: the same bits."""
+    for M, K, N in ((3, 300, 40), (100, 1000, 70), (600, 520, 300)):
+        for b_rows in (False, True):
+            a, sa, b, sb, _ = (None if v is None else v.to(DEV) for v in integers(M, K, N, K, b_rows, False))
+            want = rla.f8_matmul(a, sa, b, sb, dtype=torch.float32)
+            turned = lambda t: t.t().contiguous().t()  # noqa: E731
+            wide = lambda t: torch.full((t.shape[0] + 2, t.shape[1] * 2 + 5), float("nan"), device=DEV)[  # noqa: E731
+                1:-1, 3:3 + 2 * t.shape[1]:2].copy_(t)
+            for f in (turned, wide, lambda t: turned(wide(t))):
+                for d16 in (torch.float32, torch.bfloat16):
+                    got = rla.f8_matmul(a, f(sa), b, f(sb), dtype=d16)
+                    assert torch.equal(got, want.to(d16)), (M, b_rows)
+            assert torch.equal(rla.f8_matmul(a, sa[:, :1].expand(-1, sa.shape[1]), b, sb, dtype=torch.float32),
+                               rla.f8_matmul(a, sa[:, :1].repeat(1, sa.shape[1]), b, sb, dtype=torch.float32))
+    x = randn(torch.Generator().manual_seed(1), 70, 300).to(DEV)
+    q, s = rla.f8_quantize(x)
+    out = torch.full((70, 5), 7.0, device=DEV)
+    q2, s2 = rla.f8_quantize(x, scale_out=out[:, 1:4])
+    assert torch.equal(s, s2) and bool((out[:, 0] == 7).all()) and bool((out[:, 4] == 7).all())
 
 
 def test_outputs_that_are_given():

@@ -63,15 +63,17 @@ def test_gradients_of_the_layer_against_differences():
 
 
 def quantize_status(**kw):
-    c = dict(dtype=0, blocks=0, rows=200, dim=300, turned_pitch=256, x=FAKE, q=FAKE * 2, scale=FAKE * 3,
+    c = dict(dtype=0, blocks=0, rows=200, dim=300, turned_pitch=256, scale_strides=(3, 1), scale_turned_strides=(2, 1), x=FAKE, q=FAKE * 2, scale=FAKE * 3,
              q_turned=FAKE * 4, scale_turned=FAKE * 5)
     c.update(kw)
+    for n in ("scale_strides", "scale_turned_strides"):
+        c[n] = (_lib.i64 * 2)(*c[n])
     reason = ctypes.c_int(-1)
     return L.ltx3drope_f8_quantize(_lib.F8Quantize(**c), None, reason), _lib.REASONS[reason.value]
 
 
 @pytest.mark.parametrize("kw", [dict(blocks=2), dict(blocks=-1), dict(q_turned=None), dict(scale_turned=None),
-                                dict(turned_pitch=199)])
+                                dict(turned_pitch=199), dict(scale_strides=(-1, 1)), dict(scale_turned_strides=(1, -1))])
 def test_quantize_invalid(kw):
     assert quantize_status(**kw)[0] == _lib.E_INVALID
     assert L.ltx3drope_f8_quantize(None, None, None) == _lib.E_INVALID
@@ -87,6 +89,13 @@ def test_quantize_invalid(kw):
     (dict(scale_turned=FAKE * 4 + 300 * 256 - 4), "OVERLAP"), (dict(), "NOT_DEVICE_PTR"),
     (dict(q=FAKE + 240000), "NOT_DEVICE_PTR"), (dict(scale_turned=FAKE * 4 + 300 * 256), "NOT_DEVICE_PTR"),
     (dict(q_turned=None, scale_turned=None, turned_pitch=0), "NOT_DEVICE_PTR"), (dict(blocks=1), "NOT_DEVICE_PTR"),
+    (dict(scale_strides=(1 << 31, 1)), "TOO_LARGE"), (dict(scale_strides=(2, 1)), "OVERLAP"),
+    (dict(scale_strides=(1, 199)), "OVERLAP"), (dict(scale_strides=(0, 1)), "OVERLAP"),
+    (dict(scale_turned_strides=(1, 1)), "OVERLAP"), (dict(scale_strides=(1, 200)), "NOT_DEVICE_PTR"),
+    (dict(scale_turned_strides=(1, 300)), "NOT_DEVICE_PTR"),
+    # 200 rows of 3 blocks, the blocks 1000 apart: the last scale is number 2199
+    (dict(scale_strides=(1, 1000), q=FAKE * 3 + 2199 * 4 + 3), "OVERLAP"),
+    (dict(scale_strides=(1, 1000), q=FAKE * 3 + 2200 * 4), "NOT_DEVICE_PTR"),
 ])
 def test_quantize_refusals(kw, reason):
     assert quantize_status(**kw) == (_lib.E_UNSUPPORTED, reason)
@@ -97,9 +106,12 @@ def test_quantize_empty():
 
 
 def call(**kw):
-    c = dict(dtype=0, b_rows=0, tokens=100, dim=300, out=200, a_pitch=300, b_pitch=300, a=FAKE, b=FAKE * 2,
+    c = dict(dtype=0, b_rows=0, tokens=100, dim=300, out=200, a_pitch=300, b_pitch=300, a_scale_strides=(3, 1),
+             b_scale_strides=(3, 1), a=FAKE, b=FAKE * 2,
              a_scale=FAKE * 3, b_scale=FAKE * 4, y=FAKE * 5, workspace=FAKE * 6, workspace_bytes=1 << 24)
     c.update(kw)
+    for n in ("a_scale_strides", "b_scale_strides"):
+        c[n] = (_lib.i64 * 2)(*c[n])
     return _lib.F8Matmul(**c)
 
 
@@ -109,6 +121,7 @@ def status(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(b_rows=2), dict(a_pitch=299), dict(b_pitch=0), dict(workspace_bytes=-1),
+                                dict(a_scale_strides=(1, -1)), dict(b_scale_strides=(-3, 1)),
                                 dict(tokens=100, dim=8192, out=64, a_pitch=8192, b_pitch=8192, workspace_bytes=16)])
 def test_matmul_invalid(kw):
     assert status(**kw)[0] == _lib.E_INVALID
@@ -121,6 +134,9 @@ def test_matmul_invalid(kw):
     (dict(out=-1), "NONPOSITIVE_DIM"), (dict(dim=1 << 21, a_pitch=1 << 21, b_pitch=1 << 21), "TOO_LARGE"),
     (dict(a_pitch=1 << 22), "TOO_LARGE"), (dict(b_pitch=1 << 40), "TOO_LARGE"), (dict(tokens=1 << 26), "TOO_LARGE"),
     (dict(out=1 << 26), "TOO_LARGE"), (dict(tokens=1 << 18, out=1 << 17), "TOO_LARGE"),
+    (dict(a_scale_strides=(1 << 20, 1)), "TOO_LARGE"), (dict(b_scale_strides=(1, 1 << 31)), "TOO_LARGE"),
+    (dict(a_scale_strides=(1, 5000), y=FAKE * 3 + 10099 * 4), "OVERLAP"),
+    (dict(a_scale_strides=(1, 5000), y=FAKE * 3 + 10100 * 4), "NOT_DEVICE_PTR"),
     (dict(a=None), "NULLPTR"), (dict(b=None), "NULLPTR"), (dict(a_scale=None), "NULLPTR"),
     (dict(b_scale=None), "NULLPTR"), (dict(y=None), "NULLPTR"), (dict(y=FAKE * 5 + 2), "ALIGN"),
     (dict(a_scale=FAKE * 3 + 1), "ALIGN"), (dict(bias=FAKE * 7 + 2), "ALIGN"), (dict(y=FAKE), "OVERLAP"),
@@ -147,7 +163,11 @@ def test_matmul_empty_and_workspace():
 
 def test_descriptors_as_bytes():
     for cls, packed in ((_lib.F8Quantize, _lib.F8_QUANTIZE_BYTES), (_lib.F8Matmul, _lib.F8_BYTES)):
-        values = list(range(1, len(cls._fields_) + 1))
+        values = list(range(1, len(cls._fields_) + 3))  # two fields of two numbers
         raw = packed.pack(*values)
         s = cls.from_buffer_copy(raw)
-        assert len(raw) == ctypes.sizeof(cls) and [getattr(s, n) for n, _ in cls._fields_] == values
+        flat = []
+        for n, _ in cls._fields_:
+            v = getattr(s, n)
+            flat += list(v) if hasattr(v, "__len__") else [v]
+        assert len(raw) == ctypes.sizeof(cls) and flat == values
