@@ -85,8 +85,13 @@ bool same(const Strided& a, const Strided& b) {
     return true;
 }
 
-AxesTensor tensor(const void* in, void* out, const int64_t (&si)[3], const int64_t (&so)[3], int64_t heads) {
-    return AxesTensor{static_cast<const char*>(in), static_cast<char*>(out), si[0], si[1], si[2], so[0], so[1], so[2],
+// A stride that no index passes has any value: the launcher reckons with 0.
+int64_t step(int64_t size, int64_t stride) { return size > 1 ? stride : 0; }
+
+AxesTensor tensor(const void* in, void* out, const int64_t (&si)[3], const int64_t (&so)[3], const ltx3drope_axes_t& c,
+                  int64_t heads) {
+    return AxesTensor{static_cast<const char*>(in), static_cast<char*>(out), step(c.batch, si[0]), step(c.tokens, si[1]),
+                      step(heads, si[2]), step(c.batch, so[0]), step(c.tokens, so[1]), step(heads, so[2]),
                       static_cast<uint32_t>(heads)};
 }
 
@@ -159,12 +164,12 @@ int ltx3drope_axes_apply(const ltx3drope_axes_t* call, void* stream, int* reason
     if (const int why = check_memory(all, &device)) return refuse(why, reason);
 
     AxesProblem p;
-    p.q = tensor(c.q, c.q_out, c.q_strides, c.q_out_strides, c.q_heads);
-    p.k = tensor(c.k, c.k_out, c.k_strides, c.k_out_strides, c.k_heads);
+    p.q = tensor(c.q, c.q_out, c.q_strides, c.q_out_strides, c, c.q_heads);
+    p.k = tensor(c.k, c.k_out, c.k_strides, c.k_out_strides, c, c.k_heads);
     p.positions = c.positions;
-    p.position_axis = c.position_strides[0];
-    p.position_batch = c.position_strides[1];
-    p.position_token = c.position_strides[2];
+    p.position_axis = step(c.axes, c.position_strides[0]);
+    p.position_batch = step(c.batch, c.position_strides[1]);
+    p.position_token = step(c.tokens, c.position_strides[2]);
     p.frequencies = c.frequencies;
     p.axis = c.axis;
     p.batch = static_cast<uint32_t>(c.batch);

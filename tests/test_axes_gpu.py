@@ -122,6 +122,28 @@ def test_many_tokens_of_few_channels(B, S, Hq, Hk, D, P, axes, pairing, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_strides_that_no_index_passes(dtype):
+    """One head, one sample, one axis: their strides are any numbers."""
+    q, k, pos, freq, axis = make(1, 9, 1, 5, 16, 8, 1, dtype, 1)
+    axis[:] = 0
+    far = 1 << 61
+    wide = q.to(DEV).as_strided(q.shape, (far, 16, far + 1, 1))
+    at = pos.to(DEV).as_strided(pos.shape, (far - 1, far, 1))
+    got, got_k = rla.axes_apply_qk(wide, k.to(DEV), at, freq.to(DEV), axis.to(DEV))
+    check(q, got, pos, freq, axis, "adjacent", False, "q")
+    check(k, got_k, pos, freq, axis, "adjacent", False, "k")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("S,Hk", [(5, 70), (20000, 3)])
+def test_keys_alone(S, Hk, dtype):
+    q, k, pos, freq, axis = make(1, S, 0, Hk, 24, 8, 2, dtype, S)
+    q_out, k_out = rla.axes_apply_qk(q.to(DEV), k.to(DEV), pos.to(DEV), freq.to(DEV), axis.to(DEV))
+    assert q_out.shape == q.shape
+    check(k, k_out, pos, freq, axis, "adjacent", False, "k")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("S", [1, 3, 500])
 @pytest.mark.parametrize("D", [16, 4096, 4098, 8192, 1000])
 def test_whole_width_as_one_head(D, S, dtype):
