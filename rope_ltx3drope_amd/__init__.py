@@ -1022,7 +1022,7 @@ def _f8_quantize(x, blocks, turned, q_out, scale_out, stream, what):
         q = torch.empty_like(x, dtype=f8) if q_out is None else q_out
         if scale_out is not None:
             scale = scale_out
-        elif blocks:
+        elif blocks or rows == 1:
             scale = x.new_empty(scales, dtype=f32)
         else:  # a block's scales of all rows side by side
             scale = x.new_empty((across, *xs[:-1]), dtype=f32)
