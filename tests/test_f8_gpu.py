@@ -217,6 +217,38 @@ def test_tiles(M, K, N, b_rows):
     check_matmul(*integers(M, K, N, M + K, b_rows, True), torch.float32, True)
 
 
+@pytest.mark.parametrize("b_rows", [False, True])
+@pytest.mark.parametrize("M,K,N", [(4095, 401, 3329), (2048, 1041, 2050), (4095, 4672, 576), (4095, 4673, 576),
+                                   (1000, 8195, 100)])
+def test_tiles_of_rows_further_apart(M, K, N, b_rows):
+    """Wide tiles, whole and split, whose rows start on 16 bytes and end anywhere; NaN between the rows."""
+    a, sa, b, sb, bias = integers(M, K, N, K, b_rows, True)
+    want = of.matmul(a, sa, b, sb, bias)[0]
+
+    def wide(t):
+        v = torch.full((t.shape[0], -(-K // 16) * 16 + 16), 0x7f, dtype=torch.uint8, device=DEV).view(F8)
+        v.view(torch.uint8)[:, :K] = t.to(DEV).view(torch.uint8)
+        return v[:, :K]
+
+    for dtype in TYPES:
+        y = rla.f8_matmul(wide(a), sa.to(DEV), wide(b), sb.to(DEV), bias=bias.to(DEV), dtype=dtype)
+        assert torch.equal(y.cpu(), want.to(dtype))
+
+
+@pytest.mark.parametrize("b_rows", [False, True])
+def test_the_widest_tiles_split(b_rows):
+    """So few outputs of so deep a product that tiles of 256 x 256 are split; sums stay below 2^22 steps of 1/4."""
+    M, K, N = 256, 131072, 4096
+    a, sa, b, sb, bias = (v.to(DEV) for v in integers(M, K, N, 1, b_rows, True))
+    x = a.double() * sa.double().repeat_interleave(128, 1)
+    want = torch.cat([x @ (b[n:n + 1024].double() * (sb[n:n + 1024] if b_rows else sb[n // 128:n // 128 + 8].repeat_interleave(
+        128, 0)).double().repeat_interleave(128, 1)).t().contiguous() for n in range(0, N, 1024)], 1) + bias.double()
+    assert float(want.abs().max()) < 2.0 ** 20
+    for dtype in TYPES:
+        y = rla.f8_matmul(a, sa, b, sb, bias=bias, dtype=dtype)
+        assert torch.equal(y, want.to(dtype))
+
+
 def random_operands(M, K, N, seed, b_rows=False, bias=True):
     g = torch.Generator().manual_seed(seed)
     a, sa = of.quantize_rows(randn(g, M, K) * torch.exp(randn(g, K)))
