@@ -994,7 +994,7 @@ def _f8_scale_strides(t, rows, index):
     s = t.stride()
     if t.numel() == 0:
         return 0, 0
-    row = s[-2] if rows else 0
+    row = s[-2] if rows and t.numel() != t.shape[-1] else 0  # one row: its stride is any number
     for i in range(rows - 1):
         if t.shape[i] != 1 and s[i] != s[i + 1] * t.shape[i + 1]:
             raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")

@@ -374,6 +374,19 @@ def test_scales_of_any_strides():
     assert torch.equal(s, s2) and bool((out[:, 0] == 7).all()) and bool((out[:, 4] == 7).all())
 
 
+def test_the_stride_of_one_row():
+    """One token, one row of weights' scales: their row strides are any numbers."""
+    a, sa, b, sb, _ = (None if v is None else v.to(DEV) for v in integers(1, 400, 70, 6, False, False))
+    want = rla.f8_matmul(a, sa, b, sb)
+    far = lambda v: v.as_strided(v.shape, (1 << 40, 1))  # noqa: E731
+    assert torch.equal(rla.f8_matmul(a, far(sa), b, far(sb)), want)
+    x = torch.randn(1, 400, device=DEV)
+    q, s = rla.f8_quantize(x)
+    given = torch.empty_like(s)
+    rla.f8_quantize(x, scale_out=far(given))
+    assert torch.equal(given, s)
+
+
 def test_outputs_that_are_given():
     x = randn(torch.Generator().manual_seed(1), 5, 200, dtype=torch.bfloat16).to(DEV)
     want = rla.f8_quantize(x)
