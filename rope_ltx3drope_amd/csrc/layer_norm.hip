@@ -18,7 +18,11 @@
 // the sum of the differences, which would be zero, goes along with that of their squares and takes
 // the rounding out again: d = r - mean', e = mean(d), var = mean(d^2) - e^2, hat = (d - e) * rstd.
 //
-// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.
+// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.  Kernels alone: after a
+// block with gate and modulation, 2 x 34680 x 2048 bf16, 215 us (5.3 TB/s; the RMS norm there takes 210 to 222 and a
+// plain kernel of two streams in and two out 192); its backward, 2 x 18360, 164 us (5.5 TB/s) and 7 to join the
+// vectors' gradients; before a block, fp32 rows of 2053 off the 16 bytes, 3 x 1021, 17 us (2.9 TB/s, 4-byte
+// loads); one row of 4096 for each of four samples 3.8 us.
 #include <hip/hip_runtime.h>
 
 #include <utility>
