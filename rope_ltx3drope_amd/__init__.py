@@ -478,6 +478,19 @@ def _axes_marshal(t, like, device, out):
     return s[:3] if len(s) == 4 else (0, *s[:2])
 
 
+def _axes_out(x, out, index, stream):
+    """The output for x, and its strides."""
+    if out is not None:
+        if out.shape != x.shape:
+            raise Ltx3dRopeUnsupported("OUTPUT_MISMATCH")
+        return out, _axes_marshal(out, x, index, True)
+    torch = _torch()
+    out = (torch.empty_like(x, memory_format=torch.contiguous_format) if stream is None
+           else _empty(stream, lambda: torch.empty_like(x, memory_format=torch.contiguous_format)))
+    s = out.stride()
+    return out, s[:3] if len(s) == 4 else (0, *s[:2])
+
+
 def _axes_apply(q, k, positions, frequencies, axis, pairing, inverse, q_out, k_out, inplace, stream, what):
     torch = _torch()
     try:
@@ -514,22 +527,15 @@ def _axes_apply(q, k, positions, frequencies, axis, pairing, inverse, q_out, k_o
         if (q_out is not None and q_out is not q) or (k_out is not None and k_out is not k):
             raise ValueError("inplace=True writes into q and k")
         q_out, k_out = q, k
-    contiguous = torch.contiguous_format
-    if q_out is None:
-        q_out = _empty(stream, lambda: torch.empty_like(q, memory_format=contiguous))
-    if k_out is None and k is not None:
-        k_out = _empty(stream, lambda: torch.empty_like(k, memory_format=contiguous))
-    if q_out.shape != shape or (k is not None and k_out.shape != k.shape):
-        raise Ltx3dRopeUnsupported("OUTPUT_MISMATCH")
-    out_strides = (*_axes_marshal(q_out, q, index, True),
-                   *((0, 0, 0) if k is None else _axes_marshal(k_out, q, index, True)))
+    q_out, q_out_strides = _axes_out(q, q_out, index, stream)
+    k_out, k_out_strides = (None, (0, 0, 0)) if k is None else _axes_out(k, k_out, index, stream)
     reason = ctypes.c_int(0)
     _lib.lib()
     st = _lib.axes_apply(
         _lib.AXES_BYTES.pack(_dtype_code(q), pairing, inverse, position_type, frequency_type, positions.shape[0], batch,
                              shape[-3], shape[-2], k_heads, shape[-1], frequencies.shape[0], *q_strides, *k_strides,
-                             *out_strides, *position_strides, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out),
-                             positions.data_ptr(), frequencies.data_ptr(), axis.data_ptr()),
+                             *q_out_strides, *k_out_strides, *position_strides, q.data_ptr(), _ptr(k),
+                             q_out.data_ptr(), _ptr(k_out), positions.data_ptr(), frequencies.data_ptr(), axis.data_ptr()),
         _raw_stream(index, stream), ctypes.byref(reason))
     _finish(st, reason, what)
     return q_out, k_out
