@@ -68,7 +68,8 @@ __device__ __forceinline__ void load8(float (&f)[8], const char* row, uint32_t c
         if constexpr (F32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + c * 4u + h * 16));
+                const u32x4 v = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(row) + c + h * 4));  // past 2^32 bytes
 #pragma unroll
                 for (int k = 0; k < 4; ++k) f[4 * h + k] = __uint_as_float(v[k]);
             }
