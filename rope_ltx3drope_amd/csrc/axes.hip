@@ -13,8 +13,6 @@
 // used by all heads that a lane sees.
 #include <hip/hip_runtime.h>
 
-#include <initializer_list>
-
 #include "axes.h"
 #include "fastdiv.h"
 #include "ltx3drope.h"
@@ -55,12 +53,10 @@ __device__ __forceinline__ double position_at(const AxesProblem& p, uint32_t axi
 // 16 bytes, two elements, or one.
 template <bool F32, bool HALVES, int V>
 struct Unit {
-    static constexpr int N = HALVES || V == 1 ? 2 : 1;              // accesses
-    static constexpr int U = HALVES || V == 1 ? V : V / 2;          // pairs
+    static constexpr int N = axes_unit_accesses(HALVES, V), U = axes_unit_pairs(HALVES, V);
     static constexpr int kElem = F32 ? 4 : 2, kBytes = V * kElem;
-    static constexpr int kWords = F32 ? V : (V + 1) / 2;            // of an access
-    // of a wavefront: 16 registers of channels a lane, as many bytes on their way
-    static constexpr uint32_t kRounds = 16 / (N * kWords) < 16 ? 16 / (N * kWords) : 16;
+    static constexpr int kWords = axes_access_words(F32, V);
+    static constexpr uint32_t kRounds = axes_rounds(F32, HALVES, V);
     uint32_t w[N][kWords];
 
     // byte offset of the second access from the first
@@ -157,20 +153,6 @@ struct Unit {
 // segment's angles are formed once, a pair a lane, and handed over in LDS: loads of a frequency and an axis for each
 // of a unit's pairs, and of a position that waits for the axis, took longer than the channels (2 x 18360 tokens of
 // 4096 in bf16: 634 us so, 462 with the angles handed over, 405 us with none).
-struct AxesShape {
-    uint32_t segments;   // of pairs
-    uint32_t copies;     // segments of channels that pass through, 0: they belong to the last one of pairs
-    uint32_t seg_pairs;  // pairs of a segment (the last may have fewer)
-    uint32_t slots;      // most heads side by side in a wavefront
-    uint32_t q_rounds;
-    uint32_t rounds;     // of q and k
-    uint32_t together;   // tokens whose rounds are one wavefront's; 0: a token has groups of rounds, q's
-    uint32_t q_groups;   // before k's in the grid
-    uint32_t k_groups;
-    FastDiv by_planes, by_q_groups, by_k_groups, by_axes, by_pairs;
-};
-
-constexpr uint32_t kMostAngles = 512;  // of several tokens
 constexpr float kStays = 2.f;  // in a cosine's place: the pair stays as it is
 
 template <bool F32, bool HALVES, int V, bool SOME>
@@ -339,54 +321,19 @@ __global__ __launch_bounds__(64) void axes_rotate(AxesProblem p, AxesShape shape
 
 template <bool F32, bool HALVES, int V>
 hipError_t launch(const AxesProblem& p, hipStream_t stream) {
-    using T = Unit<F32, HALVES, V>;
-    AxesShape s;
-    const uint32_t tail = (p.head_dim - 2 * p.pairs) / V, most_pairs = 64 * T::U;
-    s.segments = (p.pairs + most_pairs - 1) / most_pairs;
-    s.seg_pairs = p.pairs < most_pairs ? p.pairs : most_pairs;
-    const uint32_t last = p.pairs - (s.segments - 1) * s.seg_pairs;
-    s.copies = last / T::U + tail <= 64 ? 0 : (tail + 63) / 64;
-    const uint32_t planes = s.segments + s.copies;
-    // heads side by side, as many as fit in every segment; what a lane adds to the first one's address stays below 2^31
-    int64_t head = 1;
-    for (const AxesTensor* t : {&p.q, &p.k}) {
-        head = head > t->in_head ? head : t->in_head;
-        head = head > t->out_head ? head : t->out_head;
-    }
-    const int64_t reach = (int64_t(1) << 30) / (head * T::kElem);
-    const uint32_t units = planes > 1 ? 64 : s.seg_pairs / T::U + tail;
-    s.slots = reach < 63 && static_cast<uint32_t>(reach) + 1 < 64 / units ? static_cast<uint32_t>(reach) + 1 : 64 / units;
-    s.q_rounds = (p.q.heads + s.slots - 1) / s.slots;
-    s.rounds = s.q_rounds + (p.k.heads + s.slots - 1) / s.slots;
-    s.together = s.rounds <= T::kRounds ? 1 : 0;
-    if (s.together && static_cast<uint64_t>(p.tokens) * p.batch * planes >= 16384) {
-        // several tokens, if that leaves wavefronts enough to fill the chip
-        const uint32_t rows = kMostAngles / s.seg_pairs, places = 64 / p.axes;
-        uint32_t t = T::kRounds / s.rounds;
-        t = t < rows ? t : rows;
-        t = t < places ? t : places;
-        s.together = t > 1 ? t : 1;
-    }
-    s.q_groups = (s.q_rounds + T::kRounds - 1) / T::kRounds;
-    s.k_groups = (s.rounds - s.q_rounds + T::kRounds - 1) / T::kRounds;
-    s.by_planes = make_fastdiv(planes);
-    s.by_q_groups = make_fastdiv(s.q_groups ? s.q_groups : 1);
-    s.by_k_groups = make_fastdiv(s.k_groups ? s.k_groups : 1);
-    s.by_axes = make_fastdiv(p.axes);
-    s.by_pairs = make_fastdiv(s.seg_pairs);
-    const uint32_t jobs = planes * (s.together ? 1 : s.q_groups + s.k_groups);  // of a token or some: 2^25 at most
-    // a launch holds fewer than 2^32 threads a dimension; whole groups of tokens
-    const uint32_t most = ((uint32_t(1) << 26) - 1) / jobs / 64 * 64;
+    const AxesShape s = axes_shape(p);
+    const uint32_t most = axes_launch_tokens(s);
     for (uint64_t n = 0; n < p.tokens; n += most) {
         AxesProblem some = p;
         some.first_token = static_cast<uint32_t>(n);
         some.tokens = p.tokens - some.first_token < most ? p.tokens - some.first_token : most;
-        const uint32_t groups = s.together > 1 ? (some.tokens + s.together - 1) / s.together : some.tokens;
-        const dim3 grid(groups * jobs, p.batch);
+        const dim3 grid(axes_launch_groups(s, some.tokens), p.batch);
         if (s.together > 1) axes_rotate<F32, HALVES, V, true><<<grid, 64, 0, stream>>>(some, s);
         else axes_rotate<F32, HALVES, V, false><<<grid, 64, 0, stream>>>(some, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 template <bool F32, bool HALVES>
