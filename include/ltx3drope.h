@@ -520,14 +520,14 @@ int64_t ltx3drope_norm_backward_workspace(const ltx3drope_norm_backward_t* call)
  * Row tensors and vectors as for ltx3drope_norm: weight and bias [dim]; gate,
  * scale and shift [batch, dim]; any vector may be NULL (its factor is then 1, its
  * term 0).  With hat(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps), per
- * row of sample b and all in fp32:
+ * row of sample b and in fp32 but for the mean:
  *     r = residual + gate_b * y
  *     n = (hat(r) * weight + bias) * (1 + scale_b) + shift_b
  * each output rounded once to `dtype` (n is formed from the unrounded r).  The
- * squares are taken around the mean, whose own rounding is taken out again, so a
- * mean that is large beside the row's spread costs no precision.  mean(|v|) and
- * mean((v - mean(v))^2) have to be finite in fp32 (with an eps below 2^-110 the
- * sum of the squares): other rows give zeros or NaN.
+ * mean is formed in 64 bits and the squares are taken around it, so a mean that is
+ * large beside the row's spread costs no precision, and a row of one value is zeros
+ * with a variance of 0.  mean((v - mean(v))^2) has to be finite in fp32 (with an
+ * eps below 2^-110 the sum of the squares): other rows give zeros or NaN.
  *
  * after = 1: y, residual, r and n are required.  after = 0 is the norm before a
  * block alone: n from `residual`; y, gate and r must be NULL.

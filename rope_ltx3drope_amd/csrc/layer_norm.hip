@@ -1,7 +1,7 @@
 // Layer norms before and after a transformer block, fused with the block's gate, the residual and the
 // norm's own weight, bias and per-sample scale and shift; and their backward pass.
 //
-// Per row of width D (rows of sample b), all in fp32:
+// Per row of width D (rows of sample b), in fp32 but for the mean:
 //     r      = residual + gate_b * y                     (before a block: r is the input itself)
 //     hat(r) = (r - mean(r)) * rstd,  rstd = 1 / sqrt(mean((r - mean(r))^2) + eps)
 //     n      = (hat(r) * w + bias) * (1 + scale_b) + shift_b
@@ -14,15 +14,17 @@
 //     dbias = sum_b (1 + scale_b) P2, dgate_b = P3.
 //
 // The mean is taken first and the squares around it: their difference would lose what a row with a large
-// mean has left.  fp32 rounds that mean by up to 2^-24 of it, which may be many times the row's spread, so
-// the sum of the differences, which would be zero, goes along with that of their squares and takes
-// the rounding out again: d = r - mean', e = mean(d), var = mean(d^2) - e^2, hat = (d - e) * rstd.
+// mean has left.  The mean is formed in 64 bits (the sum of up to 2^14 equal numbers is exact there) and taken
+// off as two fp32 numbers: rounded to one it would be off by 2^-24 of itself, which may be many times the
+// row's spread.  A row of one value is zeros with a variance of zero, whatever the value.  It costs no time: a
+// sum in fp32 and a second one of what its rounding left took 228 us a call where this takes 208 (2 x 34680 x
+// 2048 bf16 after a block).
 //
-// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.  Kernels alone: after a
-// block with gate and modulation, 2 x 34680 x 2048 bf16, 215 us (5.3 TB/s; the RMS norm there takes 210 to 222 and a
-// plain kernel of two streams in and two out 192); its backward, 2 x 18360, 164 us (5.5 TB/s) and 7 to join the
-// vectors' gradients; before a block, fp32 rows of 2053 off the 16 bytes, 3 x 1021, 17 us (2.9 TB/s, 4-byte
-// loads); one row of 4096 for each of four samples 3.8 us.
+// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.  After a block with gate
+// and modulation, 2 x 34680 x 2048 bf16, 208 us a call (5.5 TB/s; the RMS norm there takes 210 to 222 and a
+// plain kernel of two streams in and two out 192); its backward, 2 x 18360, 167 us (5.4 TB/s), 7 of them to join the
+// vectors' gradients; before a block, fp32 rows of 2053 off the 16 bytes, 3 x 1021, 15 us (3.4 TB/s, 4-byte
+// loads); one row of 4096 for each of four samples: the kernel 3.8 us.
 #include <hip/hip_runtime.h>
 
 #include <utility>
@@ -33,42 +35,68 @@
 namespace ltx3drope {
 namespace {
 
-// The sum of a thread's values times 2^-14, which stays in fp32's range wherever the row's mean does (a row
-// has at most 2^14 values); scaled as a whole unless a wavefront's sum passes the range.
-constexpr float kSumScale = 0x1p-14f;
-static_assert(kNormMaxDim == 1 << 14, "kSumScale takes a row's length out of its sum");
+// A row's mean as the sum of two fp32 numbers.
+struct Mean {
+    float hi, lo;
+};
 
-template <int E>
-__device__ __forceinline__ float scaled_sum(const float (&v)[E]) {
-    float even = 0.f, odd = 0.f;
-#pragma unroll
-    for (int k = 0; k < E; k += 2) {
-        even += v[k];
-        odd += v[k + 1];
-    }
-    const float s = (even + odd) * kSumScale;
-    if (__builtin_expect(!__any(!(fabsf(s) < __builtin_inff())), 1)) return s;
-    float t = 0.f;
-#pragma unroll
-    for (int k = 0; k < E; ++k) t = fmaf(v[k], kSumScale, t);
-    return t;
+template <int CTRL>
+__device__ __forceinline__ double lanes64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// r less its mean as fp32 has it, with zeros past the row's end (where r is zero).
+// The mean of a row's elements, E a thread with zeros past the row's end, in the order of row_sum, whose rules
+// for `lds` (a number a wavefront) hold.  inv_d: 1 / D; the quotient is corrected by its exact remainder, so
+// that the mean of equal numbers is that number.
+template <int E>
+__device__ __forceinline__ Mean row_mean(const float (&r)[E], double* lds, double d, double inv_d, uint32_t t, uint32_t T,
+                                         uint32_t g) {
+    double even = 0.0, odd = 0.0;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+        even += r[k];
+        odd += r[k + 1];
+    }
+    double v = even + odd;
+    v += lanes64<0xb1>(v);   // quad_perm 1 0 3 2
+    v += lanes64<0x4e>(v);   // quad_perm 2 3 0 1
+    v += lanes64<0x141>(v);  // row_half_mirror
+    v += lanes64<0x140>(v);  // row_mirror
+    auto lane = [&](int l) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
+        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
+        return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    };
+    double sum = (lane(0) + lane(16)) + (lane(32) + lane(48));
+    const uint32_t W = T / 64;
+    if (W > 1) {
+        double* mine = lds + g * W;
+        if ((t & 63) == 0) mine[t / 64] = sum;
+        __syncthreads();
+        sum = 0.0;
+        for (uint32_t w = 0; w < W; ++w) sum += mine[w];
+    }
+    const double about = sum * inv_d, mean = fma(fma(-about, d, sum), inv_d, about);
+    const float hi = static_cast<float>(mean);
+    return Mean{hi, static_cast<float>(mean - hi)};
+}
+
+// r less its mean, with zeros past the row's end (where r is zero).
 template <bool F32, int E, bool VEC>
-__device__ __forceinline__ void subtract(float (&r)[E], float mean, uint32_t t, uint32_t T, uint32_t D) {
+__device__ __forceinline__ void subtract(float (&r)[E], Mean mean, uint32_t t, uint32_t T, uint32_t D) {
     constexpr int V = RowPart<F32, E, VEC>::V;
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
-        const float m = (i * T + t) * V < D ? mean : 0.f;
+        const bool in = (i * T + t) * V < D;
+        const float hi = in ? mean.hi : 0.f, lo = in ? mean.lo : 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) r[i * V + j] -= m;
+        for (int j = 0; j < V; ++j) r[i * V + j] = (r[i * V + j] - hi) - lo;
     }
 }
-
-// mean((d - e)^2) from mean(d^2) and e = mean(d): no less than zero, which the rounding of two equal numbers
-// may miss (a row of equal large values).
-__device__ __forceinline__ float variance(float squares, float e) { return fmaxf(fmaf(-e, e, squares), 0.f); }
 
 // The norm's factor w * (1 + scale_b) and, if asked for, its term bias * (1 + scale_b) + shift_b.
 template <bool F32, int E, bool VEC, class Call>
@@ -90,11 +118,12 @@ __device__ __forceinline__ void load_factor(float (&f)[E], float* term, const Ca
 
 template <bool F32, int E, bool VEC, bool AFTER>
 __global__ __launch_bounds__(1024) void layer_norm_forward(LayerNormForward p) {
-    __shared__ float lds[2][3 * kMaxWaves];
+    __shared__ double lds_sum[2][kMaxWaves];
+    __shared__ float lds[2][kMaxWaves];
     const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
     const uint32_t D = p.dim, b = blockIdx.y;
-    const float sq = p.square_scale, inv_d = 1.0f / static_cast<float>(D);
-    const float inv_sum = inv_d / kSumScale, inv_sq = inv_d / sq;  // powers of two
+    const float sq = p.square_scale, inv_d = 1.0f / static_cast<float>(D), inv_sq = inv_d / sq;  // sq: a power of two
+    const double d64 = D, inv_d64 = 1.0 / d64;
 
     constexpr size_t es = F32 ? 4 : 2;
     const uint32_t step = gridDim.x * G;
@@ -130,27 +159,25 @@ __global__ __launch_bounds__(1024) void layer_norm_forward(LayerNormForward p) {
         load(s + step);  // the next row travels while this one is summed
         if constexpr (AFTER)
             if (live) store_row<F32, E, VEC>(static_cast<char*>(p.r) + off, r, t, T, D);
-        float sum[1] = {scaled_sum(r)};
-        row_sum(sum, lds[phase], t, T, g);
-        subtract<F32, E, VEC>(r, sum[0] * inv_sum, t, T, D);
-        float ss[2] = {scaled_sum(r), square_sum(r, sq)};
-        row_sum(ss, lds[phase] + kMaxWaves, t, T, g);
-        const float e = ss[0] * inv_sum;
-        const float rstd = rsqrtf(variance(ss[1] * inv_sq, e) + p.eps);
+        subtract<F32, E, VEC>(r, row_mean(r, lds_sum[phase], d64, inv_d64, t, T, g), t, T, D);
+        float ss[1] = {square_sum(r, sq)};
+        row_sum(ss, lds[phase], t, T, g);
+        const float rstd = rsqrtf(ss[0] * inv_sq + p.eps);
 #pragma unroll
-        for (int k = 0; k < E; ++k) r[k] = fmaf((r[k] - e) * rstd, fn[k], sh[k]);
+        for (int k = 0; k < E; ++k) r[k] = fmaf(r[k] * rstd, fn[k], sh[k]);
         if (live) store_row<F32, E, VEC>(static_cast<char*>(p.n) + off, r, t, T, D);
     }
 }
 
 template <bool F32, int E, bool VEC, bool AFTER>
 __global__ __launch_bounds__(1024) void layer_norm_backward(LayerNormBackward p) {
-    __shared__ float lds[2][5 * kMaxWaves];
+    __shared__ double lds_sum[2][kMaxWaves];
+    __shared__ float lds[2][3 * kMaxWaves];
     extern __shared__ float cols[];  // (G - 1) * D: the rows' partial sums on their way to row 0
     const uint32_t T = blockDim.x, t = threadIdx.x, G = blockDim.y, g = threadIdx.y;
     const uint32_t D = p.dim, b = blockIdx.y;
-    const float sq = p.square_scale, inv_d = 1.0f / static_cast<float>(D);
-    const float inv_sum = inv_d / kSumScale, inv_sq = inv_d / sq;
+    const float sq = p.square_scale, inv_d = 1.0f / static_cast<float>(D), inv_sq = inv_d / sq;
+    const double d64 = D, inv_d64 = 1.0 / d64;
 
     float fy[AFTER ? E : 1], fn[E];
     float p1[E] = {}, p2[E] = {}, p3[AFTER ? E : 1] = {};
@@ -177,25 +204,22 @@ __global__ __launch_bounds__(1024) void layer_norm_backward(LayerNormBackward p)
         if constexpr (AFTER) get(raw_y, p.y);
         raw_r.unpack(r);
         raw_n.unpack(dn);
-        float sum[1] = {scaled_sum(r)};
-        row_sum(sum, lds[phase], t, T, g);
-        subtract<F32, E, VEC>(r, sum[0] * inv_sum, t, T, D);
-        float ss[4] = {scaled_sum(r), square_sum(r, sq), 0.f, 0.f};  // ..., v, v.(r - mean)
+        subtract<F32, E, VEC>(r, row_mean(r, lds_sum[phase], d64, inv_d64, t, T, g), t, T, D);
+        float ss[3] = {square_sum(r, sq), 0.f, 0.f};  // ..., v, v.(r - mean)
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const float v = dn[k] * fn[k];
-            ss[2] += v;
-            ss[3] = fmaf(v, r[k], ss[3]);
+            ss[1] += v;
+            ss[2] = fmaf(v, r[k], ss[2]);
         }
-        row_sum(ss, lds[phase] + kMaxWaves, t, T, g);
-        const float e = ss[0] * inv_sum;
-        const float rstd = rsqrtf(variance(ss[1] * inv_sq, e) + p.eps);
-        const float mean_v = ss[2] * inv_d;
-        const float proj = fmaf(-e, ss[2], ss[3]) * rstd * inv_d;  // mean(v * hat(r))
+        row_sum(ss, lds[phase], t, T, g);
+        const float rstd = rsqrtf(ss[0] * inv_sq + p.eps);
+        const float mean_v = ss[1] * inv_d;
+        const float proj = ss[2] * rstd * inv_d;  // mean(v * hat(r))
         raw_d.unpack(d);
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-            const float hat = (r[k] - e) * rstd;
+            const float hat = r[k] * rstd;
             p1[k] = fmaf(dn[k], hat, p1[k]);
             p2[k] += dn[k];
             d[k] = fmaf(rstd, fmaf(-hat, proj, fmaf(dn[k], fn[k], -mean_v)), d[k]);
