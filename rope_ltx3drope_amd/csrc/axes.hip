@@ -5,15 +5,15 @@
 // with (e, o) = (x[2i], x[2i+1]) or, in halves, (x[i], x[i + pairs]).
 //
 // Angles are formed in 64 bits: a position of 100000 times a frequency near 1 leaves fp32 0.004 of a radian.
-// The angle is taken in turns, a whole number of quarters is split off (exactly), and sine and cosine of the
-// rest, up to half a quarter, are polynomials of degree 7 and 8 in fp32 (fitted to the least largest error,
-// 1.2e-9 and 6e-11).
+// The angle is taken in turns, whose whole number falls away exactly; sine and cosine of the rest are those of
+// axes_math.h, within 9.4e-8.
 //
 // Bound: HBM.  Each channel is read and written once, 16 bytes a lane, and an angle costs about 30 operations and is
 // used by all heads that a lane sees.
 #include <hip/hip_runtime.h>
 
 #include "axes.h"
+#include "axes_math.h"
 #include "fastdiv.h"
 #include "ltx3drope.h"
 #include "stream_store.h"
@@ -26,20 +26,10 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// (cos, sin) of position * turns whole turns.  Adding 1.5 * 2^52 leaves the quarters in the sum's low bits.
+// (cos, sin) of position * turns whole turns.
 __device__ __forceinline__ f32x2 cos_sin(double position, double turns) {
-    const double part = __builtin_amdgcn_fract(position * turns);
-    const double shifted = fma(part, 4.0, 0x1.8p52);
-    const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, shifted));  // 0 to 4
-    const float r = static_cast<float>(fma(part, 4.0, 0x1.8p52 - shifted));  // quarters, |r| <= 1/2
-    const float z = r * r;
-    const float p = fmaf(z, fmaf(z, fmaf(z, -4.5922891e-3f, 7.9675903e-2f), -6.4596294e-1f), -6.5420830e-8f);
-    const float s = fmaf(r, 1.57079637f, r * p);
-    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 9.0402167e-4f, -2.0860289e-2f), 2.5366924e-1f), -1.2337005f), 1.f);
-    // a quarter more: (c, s) -> (-s, c)
-    const float a = k & 1 ? s : c, b = k & 1 ? c : s;
-    return f32x2{__uint_as_float(__float_as_uint(a) ^ ((k + 1) << 30 & 0x80000000u)),
-                 __uint_as_float(__float_as_uint(b) ^ (k << 30 & 0x80000000u))};
+    const CosSin v = cos_sin_of_turn(__builtin_amdgcn_fract(position * turns));
+    return f32x2{v.c, v.s};
 }
 
 __device__ __forceinline__ double position_at(const AxesProblem& p, uint32_t axis, uint32_t b, uint32_t n) {
