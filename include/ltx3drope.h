@@ -716,11 +716,14 @@ int ltx3drope_f8_quantize(const ltx3drope_f8_quantize_t* call, void* stream, int
  *     y[m][n] = sum_kb a_scale[m][kb] * b_scale[n][kb] * (sum over k of block kb of a[m][k] * b[n][k]) + bias[n]
  * a [tokens, dim] and b [out, dim] e4m3, their rows a_pitch and b_pitch bytes apart (>= dim); a_scale [tokens,
  * ceil(dim / 128)]; b_scale [ceil(out / 128), ceil(dim / 128)] (b_rows = 0: 128 x 128 blocks of weights) or [out,
- * ceil(dim / 128)] (b_rows = 1), of any strides (row, block) >= 0 in numbers; bias [out] fp32 or NULL; y [tokens, out] of `dtype` (F32 or BF16),
- * contiguous, rounded once.  Products are exact and sums fp32, but for more than 16 tokens with y in
- * BF16: there the products of each 8 neighbours of k are added by the matrix cores' 8-bit units, which
- * keep 2^-13 of the largest of them.  Sums are added in a fixed order: equal inputs give equal bits.  The gradients are products of the same kind: of the input
- * from the output's and the turned weights, of the weights from both turned operands (b_rows = 1).
+ * ceil(dim / 128)] (b_rows = 1), of any strides (row, block) >= 0 in numbers; bias [out] fp32 or NULL; y [tokens,
+ * out] of `dtype` (F32 or BF16), contiguous, rounded once.  Products are exact and sums fp32, but for more than 16
+ * tokens with y in BF16: there the products of each 8 neighbours of k are added by the matrix cores' 8-bit units,
+ * which keep 2^-13 of the largest of them.  a_scale * b_scale is formed first, in fp32, and belongs within its normal
+ * range, 2^-126 to 2^128, or is 0: below it a block's sum, of up to 2^25, is off by as many times 2^-150; above it the
+ * product is infinite, and NaN times a sum of 0.  (Blocks whose largest numbers multiply to 2^-108 to 2^145 are
+ * within.)  Sums are added in a fixed order: equal inputs give equal bits.  The gradients are products of the same
+ * kind: of the input from the output's and the turned weights, of the weights from both turned operands (b_rows = 1).
  * `workspace` as for ltx3drope_gated_ffn.  tokens = 0 or out = 0 is an empty call.  E_INVALID: a NULL
  * descriptor, b_rows other than 0 or 1, a pitch < dim, a stride < 0, a workspace that is too small.  E_UNSUPPORTED:
  * DTYPE; NONPOSITIVE_DIM; TOO_LARGE (dim of 2^21 or more, a pitch of 2^22 or more, scales whose rows are 2^20 or
