@@ -17,14 +17,13 @@
 // mean has left.  The mean is formed in 64 bits (the sum of up to 2^14 equal numbers is exact there) and taken
 // off as two fp32 numbers: rounded to one it would be off by 2^-24 of itself, which may be many times the
 // row's spread.  A row of one value is zeros with a variance of zero, whatever the value.  It costs no time: a
-// sum in fp32 and a second one of what its rounding left took 228 us a call where this takes 208 (2 x 34680 x
+// sum in fp32 and a second one of what its rounding left took 228 us a call where this takes 201 to 209 (2 x 34680 x
 // 2048 bf16 after a block).
 //
-// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.  After a block with gate
-// and modulation, 2 x 34680 x 2048 bf16, 208 us a call (5.5 TB/s; the RMS norm there takes 210 to 222 and a
-// plain kernel of two streams in and two out 192); its backward, 2 x 18360, 167 us (5.4 TB/s), 7 of them to join the
-// vectors' gradients; before a block, fp32 rows of 2053 off the 16 bytes, 3 x 1021, 15 us (3.4 TB/s, 4-byte
-// loads); one row of 4096 for each of four samples: the kernel 3.8 us.
+// Bound: HBM.  Layout, walk over the rows and partial sums are those of rows.h and norm.hip.  That call moves 5.4 to
+// 5.65 TB/s (the RMS norm there takes 210 to 222 us and a plain kernel of two streams in and two out 192); its
+// backward, 2 x 18360, 167 us (5.4 TB/s), 7 of them to join the vectors' gradients; before a block, fp32 rows of 2053 off
+// the 16 bytes, 3 x 1021, 15 us (3.4 TB/s, 4-byte loads); one row of 4096 for each of four samples: the kernel 3.8 us.
 #include <hip/hip_runtime.h>
 
 #include <utility>
