@@ -994,16 +994,22 @@ def q8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
 
 
 def _f8_scale_strides(t, rows, index):
-    """The (row, block) strides of scales [*rows, blocks]; leading dimensions have to be one."""
+    """The (row, block) strides of scales [*rows, blocks]; leading dimensions have to be one, but for those of size 1,
+    whose strides are any numbers."""
     if t.get_device() != index or index < 0:
         raise Ltx3dRopeUnsupported("NOT_DEVICE_PTR")
-    s = t.stride()
     if t.numel() == 0:
         return 0, 0
-    row = s[-2] if rows and t.numel() != t.shape[-1] else 0  # one row: its stride is any number
-    for i in range(rows - 1):
-        if t.shape[i] != 1 and s[i] != s[i + 1] * t.shape[i + 1]:
+    s, row, size = t.stride(), 0, 1  # of the dimensions so far, from the last one on
+    for i in range(rows - 1, -1, -1):
+        n = t.shape[i]
+        if n == 1:
+            continue
+        if size == 1:
+            row = s[i]
+        elif s[i] != row * size:
             raise Ltx3dRopeUnsupported("NOT_CONTIGUOUS")
+        size *= n
     return row, s[-1]
 
 
@@ -1083,8 +1089,8 @@ def f8_matmul(a, a_scale, b, b_scale, *, bias=None, dtype=None, out=None, stream
 
     A bfloat16 result of more than 16 tokens is made by the matrix cores' 8-bit units, which add the products of each 8
     neighbours of k with 2^-13 of the largest of them kept (3e-5 of a result on normal data, beside bfloat16's own
-    half step of 2^-8); float32 results, and up to 16 tokens, have exact products and fp32 sums.  a_scale * b_scale is formed first,
-    in fp32: products of scales outside 2^-126 to 2^128 lose bits or become infinite.
+    half step of 2^-8); float32 results, and up to 16 tokens, have exact products and fp32 sums.  a_scale * b_scale is
+    formed first, in fp32: products of scales outside 2^-126 to 2^128 lose bits or become infinite.
 
     Of y = x w^T the gradients are f8_matmul(dy, ., w_turned, .) and f8_matmul(dy_turned, ., x_turned, .)."""
     torch = _torch()

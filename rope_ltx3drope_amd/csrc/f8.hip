@@ -70,7 +70,7 @@ __device__ __forceinline__ void load8(float (&f)[8], const char* row, uint32_t c
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const u32x4 v = __builtin_nontemporal_load(
-                    reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(row) + c + h * 4));  // past 2^32 bytes
+                    reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(row) + c + h * 4));  // rows may pass 2^32 bytes
 #pragma unroll
                 for (int k = 0; k < 4; ++k) f[4 * h + k] = __uint_as_float(v[k]);
             }
