@@ -135,6 +135,8 @@ struct Unit {
     }
 };
 
+constexpr float kStays = 2.f;  // in a cosine's place: the pair stays as it is
+
 // One wavefront a workgroup and few rounds a wavefront, in a grid as large as the work: the chip's memory runs fastest
 // with short-lived wavefronts that have a few kilobytes on their way (69360 tokens of 32 + 8 heads of 128 in bf16: 259
 // to 295 us with workgroups of four wavefronts that went through all heads of some tokens, in three forms; 238 us
@@ -142,9 +144,7 @@ struct Unit {
 // channels that pass through), of several heads side by side where that is short, and a round moves those.  The
 // segment's angles are formed once, a pair a lane, and handed over in LDS: loads of a frequency and an axis for each
 // of a unit's pairs, and of a position that waits for the axis, took longer than the channels (2 x 18360 tokens of
-// 4096 in bf16: 634 us so, 462 with the angles handed over, 405 us with none).
-constexpr float kStays = 2.f;  // in a cosine's place: the pair stays as it is
-
+// 4096 in bf16: 634 us so, 462 with the angles handed over, 405 us with none).  axes_shape (axes.h) gives the numbers.
 template <bool F32, bool HALVES, int V, bool SOME>
 __global__ __launch_bounds__(64) void axes_rotate(AxesProblem p, AxesShape shape) {
     using T = Unit<F32, HALVES, V>;
